@@ -368,25 +368,25 @@ def _run_own(st):
     cache = (st["k"], st["v"], st["ks"], st["vs"])
     if op == "decode":
         if table is None:
-            return gqa.gqa_decode_q8(st["q"], *cache, st["seq_lens"], window, out=st["out"])
-        return gqa.gqa_decode_q8_paged(st["q"], *cache, table, st["seq_lens"], window,
+            return gqa.gqa_decode_quant(st["q"], *cache, st["seq_lens"], window, out=st["out"])
+        return gqa.gqa_decode_quant_paged(st["q"], *cache, table, st["seq_lens"], window,
                                        out=st["out"])
     if op == "append":
         if table is None:
-            gqa.gqa_append_q8(st["k_new"], st["v_new"], st["offsets"], st["seq_lens"], *cache)
+            gqa.gqa_append_quant(st["k_new"], st["v_new"], st["offsets"], st["seq_lens"], *cache)
         else:
-            gqa.gqa_append_q8_paged(st["k_new"], st["v_new"], st["offsets"], table,
+            gqa.gqa_append_quant_paged(st["k_new"], st["v_new"], st["offsets"], table,
                                     st["seq_lens"], *cache)
     elif op == "read":
         if table is None:
-            gqa.gqa_read_q8(*cache, st["seq_lens"], window, st["k_out"], st["v_out"])
+            gqa.gqa_read_quant(*cache, st["seq_lens"], window, st["k_out"], st["v_out"])
         else:
-            gqa.gqa_read_q8_paged(*cache, table, st["seq_lens"], window, st["k_out"], st["v_out"])
+            gqa.gqa_read_quant_paged(*cache, table, st["seq_lens"], window, st["k_out"], st["v_out"])
     elif table is None:
-        gqa.gqa_prepare_decode_q8(st["q_raw"], st["k_raw"], st["v_raw"], st["w_q"], st["w_k"],
+        gqa.gqa_prepare_decode_quant(st["q_raw"], st["k_raw"], st["v_raw"], st["w_q"], st["w_k"],
                                   st["seq_lens"], st["q_out"], *cache)
     else:
-        gqa.gqa_prepare_decode_q8_paged(st["q_raw"], st["k_raw"], st["v_raw"], st["w_q"],
+        gqa.gqa_prepare_decode_quant_paged(st["q_raw"], st["k_raw"], st["v_raw"], st["w_q"],
                                         st["w_k"], table, st["seq_lens"], st["q_out"], *cache)
     return _outputs(st)
 
