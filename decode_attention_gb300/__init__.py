@@ -30,6 +30,8 @@ from ._native import (  # noqa: F401
     GQA_OUT_F32,
     PAGE_SIZE,
     GQAError,
+    gqa_append_quant,
+    gqa_append_quant_paged,
     gqa_decode,
     gqa_decode_keqv,
     gqa_decode_keqv_kernel,
@@ -37,8 +39,14 @@ from ._native import (  # noqa: F401
     gqa_decode_mq,
     gqa_decode_mq_paged,
     gqa_decode_noalloc,
+    gqa_decode_quant,
+    gqa_decode_quant_paged,
     gqa_prepare_decode,
     gqa_prepare_decode_paged,
+    gqa_prepare_decode_quant,
+    gqa_prepare_decode_quant_paged,
+    gqa_read_quant,
+    gqa_read_quant_paged,
     gqa_decode_ring,
     gqa_decode_paged,
     gqa_check_inputs_host,

@@ -44,6 +44,10 @@ EXPORTED_SYMBOLS = ("gqa_workspace_size", "gqa_workspace_init", "gqa_decode", "g
                     "gqa_decode_keqv", "gqa_decode_keqv_paged", "gqa_prepare_decode",
                     "gqa_prepare_decode_paged", "gqa_workspace_size_mq", "gqa_decode_mq",
                     "gqa_decode_mq_paged",
+                    "gqa_append_quant", "gqa_append_quant_paged", "gqa_read_quant",
+                    "gqa_read_quant_paged", "gqa_prepare_decode_quant",
+                    "gqa_prepare_decode_quant_paged", "gqa_decode_quant",
+                    "gqa_decode_quant_paged",
                     "gqa_check_inputs_host", "gqa_noalloc_status", "gqa_decode_keqv_kernel",
                     "gqa_set_test_mode", "gqa_get_test_mode",
                     "gqa_status_string")
@@ -107,6 +111,28 @@ def load_library(build_if_needed: bool = True) -> ctypes.CDLL:
         lib.gqa_decode_mq_paged.argtypes = [vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, ci, ci, ci, ci,
                                             vp, ci, vp, sz, vp]
         lib.gqa_decode_mq_paged.restype = ci
+        lib.gqa_append_quant.argtypes = [vp, vp, vp, vp, ci, ci, ci, ci, ci, vp, vp, vp, vp, vp]
+        lib.gqa_append_quant.restype = ci
+        lib.gqa_append_quant_paged.argtypes = [vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, ci, ci, vp,
+                                               vp, vp, vp, vp]
+        lib.gqa_append_quant_paged.restype = ci
+        lib.gqa_read_quant.argtypes = [vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, vp, vp, ci, ci, vp]
+        lib.gqa_read_quant.restype = ci
+        lib.gqa_read_quant_paged.argtypes = [vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, ci, ci, vp,
+                                             vp, ci, ci, vp]
+        lib.gqa_read_quant_paged.restype = ci
+        lib.gqa_prepare_decode_quant.argtypes = [vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, vp, vp, vp,
+                                                 vp, vp, ci, vp]
+        lib.gqa_prepare_decode_quant.restype = ci
+        lib.gqa_prepare_decode_quant_paged.argtypes = [vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci,
+                                                       ci, ci, ci, vp, vp, vp, vp, vp, vp]
+        lib.gqa_prepare_decode_quant_paged.restype = ci
+        lib.gqa_decode_quant.argtypes = [vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, ci, vp, ci, vp,
+                                         sz, vp]
+        lib.gqa_decode_quant.restype = ci
+        lib.gqa_decode_quant_paged.argtypes = [vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, ci,
+                                               ci, ci, vp, ci, vp, sz, vp]
+        lib.gqa_decode_quant_paged.restype = ci
         lib.gqa_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), vp]
         lib.gqa_device_status.restype = ci
         lib.gqa_check_inputs_host.argtypes = [vp, ci, ci, ci, vp, ci, ci, ctypes.POINTER(ci)]
@@ -473,6 +499,227 @@ def gqa_prepare_decode_paged(q_raw: torch.Tensor, k_raw: torch.Tensor, v_raw, w_
         _ptr(seq_lens), B, P, block_table.shape[1], page_size, H, KVH, D, _ptr(q_out),
         _ptr(k_pages), _ptr(v_pages), _stream_handle(stream, q_raw.device))
     _check("gqa_prepare_decode_paged", st)
+
+
+def _check_quant_cache(k, v, k_scales, v_scales, B: int, block_table):
+    """Codes and scales of an 8-bit cache, contiguous (block_table None) or paged; returns
+    (KVH, D)."""
+    names = ("k", "v") if block_table is None else ("k_pages", "v_pages")
+    _check_tensor(names[0], k, torch.float8_e4m3fn, 4)
+    _check_tensor(names[1], v, torch.float8_e4m3fn, 4)
+    _require(v.shape == k.shape, f"{names[0]} and {names[1]} must have the same shape")
+    n, rows, KVH, D = k.shape
+    if block_table is None:
+        _require(n == B, f"{names[0]} must hold B sequences")
+        shape = (n, (rows + PAGE_SIZE - 1) // PAGE_SIZE, KVH)
+    else:
+        _check_tensor("block_table", block_table, torch.int32, 2)
+        _require(block_table.shape[0] == B, "block_table must have B rows")
+        shape = (n, KVH)
+    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+        _check_tensor(name, t, torch.float32, len(shape))
+        _require(tuple(t.shape) == shape, f"{name} must be {list(shape)}")
+    return KVH, D
+
+
+def _append_quant(fn, k_new, v_new, token_offsets, block_table, seq_lens, k, v, k_scales, v_scales,
+                  stream):
+    _check_tensor("k_new", k_new, torch.bfloat16, 3)
+    _check_tensor("v_new", v_new, torch.bfloat16, 3)
+    _check_tensor("token_offsets", token_offsets, torch.int32, 1)
+    _check_tensor("seq_lens", seq_lens, torch.int32, 1)
+    B = seq_lens.shape[0]
+    KVH, D = _check_quant_cache(k, v, k_scales, v_scales, B, block_table)
+    _require(token_offsets.shape[0] == B + 1, "token_offsets must have B + 1 entries")
+    _require(v_new.shape == k_new.shape and tuple(k_new.shape[1:]) == (KVH, D),
+             "k_new / v_new must be [N, KVH, D]")
+    _same_device(k_new, v_new=v_new, token_offsets=token_offsets, block_table=block_table,
+                 seq_lens=seq_lens, k=k, v=v, k_scales=k_scales, v_scales=v_scales)
+    lib, N, n, rows = _lib_on(k_new.device), k_new.shape[0], k.shape[0], k.shape[1]
+    s = _stream_handle(stream, k_new.device)
+    cache = (_ptr(k), _ptr(v), _ptr(k_scales), _ptr(v_scales))
+    if block_table is None:
+        st = lib.gqa_append_quant(_ptr(k_new), _ptr(v_new), _ptr(token_offsets), _ptr(seq_lens), B,
+                                  N, rows, KVH, D, *cache, s)
+    else:
+        st = lib.gqa_append_quant_paged(_ptr(k_new), _ptr(v_new), _ptr(token_offsets),
+                                        _ptr(block_table), _ptr(seq_lens), B, N, n,
+                                        block_table.shape[1], rows, KVH, D, *cache, s)
+    _check(fn, st)
+
+
+def gqa_append_quant(k_new: torch.Tensor, v_new: torch.Tensor, token_offsets: torch.Tensor,
+                     seq_lens: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                     k_scales: torch.Tensor, v_scales: torch.Tensor, stream=None) -> None:
+    """Quantised append to a contiguous 8-bit cache: rows token_offsets[b] .. token_offsets[b+1]
+    of k_new, v_new [N,KVH,D] (bf16) go to the last positions before seq_lens[b] of k, v
+    [B,S,KVH,D] (float8_e4m3fn) with scales [B,ceil(S/16),KVH] (fp32)."""
+    _append_quant("gqa_append_quant", k_new, v_new, token_offsets, None, seq_lens, k, v, k_scales,
+                  v_scales, stream)
+
+
+def gqa_append_quant_paged(k_new: torch.Tensor, v_new: torch.Tensor, token_offsets: torch.Tensor,
+                           block_table: torch.Tensor, seq_lens: torch.Tensor,
+                           k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales: torch.Tensor,
+                           v_scales: torch.Tensor, stream=None) -> None:
+    """gqa_append_quant into page pools [P,16,KVH,D] with scales [P,KVH]."""
+    _require(block_table is not None, "block_table is required")
+    _append_quant("gqa_append_quant_paged", k_new, v_new, token_offsets, block_table, seq_lens,
+                  k_pages, v_pages, k_scales, v_scales, stream)
+
+
+def _read_quant(fn, k, v, k_scales, v_scales, block_table, seq_lens, window, k_out, v_out,
+                out_rows, out_dtype, stream):
+    _check_tensor("seq_lens", seq_lens, torch.int32, 1)
+    B = seq_lens.shape[0]
+    KVH, D = _check_quant_cache(k, v, k_scales, v_scales, B, block_table)
+    n, rows = k.shape[0], k.shape[1]
+    _require((k_out is None) == (v_out is None), "give both k_out and v_out, or neither")
+    if k_out is None:
+        if out_rows is None:
+            out_rows = rows if block_table is None else block_table.shape[1] * rows
+        k_out = torch.zeros((B, out_rows, KVH, D), dtype=out_dtype, device=k.device)
+        v_out = torch.zeros_like(k_out)
+    _check_tensor("k_out", k_out, k_out.dtype, 4)
+    _check_tensor("v_out", v_out, k_out.dtype, 4)
+    _require(v_out.shape == k_out.shape and k_out.shape[0] == B and
+             tuple(k_out.shape[2:]) == (KVH, D), "k_out / v_out must be [B, rows, KVH, D]")
+    _same_device(k, v=v, k_scales=k_scales, v_scales=v_scales, block_table=block_table,
+                 seq_lens=seq_lens, k_out=k_out, v_out=v_out)
+    lib, s = _lib_on(k.device), _stream_handle(stream, k.device)
+    cache = (_ptr(k), _ptr(v), _ptr(k_scales), _ptr(v_scales))
+    tail = (int(window), _ptr(k_out), _ptr(v_out), k_out.shape[1], _out_code(k_out), s)
+    if block_table is None:
+        st = lib.gqa_read_quant(*cache, _ptr(seq_lens), B, rows, KVH, D, *tail)
+    else:
+        st = lib.gqa_read_quant_paged(*cache, _ptr(block_table), _ptr(seq_lens), B, n,
+                                      block_table.shape[1], rows, KVH, D, *tail)
+    _check(fn, st)
+    return k_out, v_out
+
+
+def gqa_read_quant(k: torch.Tensor, v: torch.Tensor, k_scales: torch.Tensor,
+                   v_scales: torch.Tensor, seq_lens: torch.Tensor, window: int,
+                   k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None,
+                   out_rows: int | None = None, out_dtype=torch.bfloat16, stream=None):
+    """Values of a contiguous 8-bit cache: returns (k_out, v_out) [B,rows,KVH,D] (bf16 or fp32)
+    with row s = position s for the last `window` positions (0: all) of each sequence.  Other
+    rows of given outputs are left as they are; new outputs (out_rows rows, default S) start
+    at zero."""
+    return _read_quant("gqa_read_quant", k, v, k_scales, v_scales, None, seq_lens, window, k_out,
+                       v_out, out_rows, out_dtype, stream)
+
+
+def gqa_read_quant_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales: torch.Tensor,
+                         v_scales: torch.Tensor, block_table: torch.Tensor,
+                         seq_lens: torch.Tensor, window: int, k_out: torch.Tensor | None = None,
+                         v_out: torch.Tensor | None = None, out_rows: int | None = None,
+                         out_dtype=torch.bfloat16, stream=None):
+    """gqa_read_quant from page pools [P,16,KVH,D] with scales [P,KVH]."""
+    _require(block_table is not None, "block_table is required")
+    return _read_quant("gqa_read_quant_paged", k_pages, v_pages, k_scales, v_scales, block_table,
+                       seq_lens, window, k_out, v_out, out_rows, out_dtype, stream)
+
+
+def _prepare_quant(fn, q_raw, k_raw, v_raw, w_q, w_k, block_table, seq_lens, q_out, k, v, k_scales,
+                   v_scales, stream):
+    _check_tensor("q_raw", q_raw, torch.bfloat16, 3)
+    _check_tensor("k_raw", k_raw, torch.bfloat16, 3)
+    _check_tensor("v_raw", v_raw, torch.bfloat16, 3)
+    _check_tensor("w_q", w_q, torch.bfloat16, 1)
+    _check_tensor("w_k", w_k, torch.bfloat16, 1)
+    _check_tensor("seq_lens", seq_lens, torch.int32, 1)
+    _check_tensor("q_out", q_out, torch.bfloat16, 3)
+    B, H, D = q_raw.shape
+    KVH, Dc = _check_quant_cache(k, v, k_scales, v_scales, B, block_table)
+    _require(Dc == D and tuple(k_raw.shape) == (B, KVH, D) and v_raw.shape == k_raw.shape,
+             "k_raw / v_raw must be [B, KVH, D]")
+    _require(q_out.shape == q_raw.shape, "q_out must match q_raw")
+    _require(w_q.shape[0] == D and w_k.shape[0] == D, "w_q / w_k must be [D]")
+    _require(seq_lens.shape[0] == B, "seq_lens must have B entries")
+    _same_device(q_raw, k_raw=k_raw, v_raw=v_raw, w_q=w_q, w_k=w_k, block_table=block_table,
+                 seq_lens=seq_lens, q_out=q_out, k=k, v=v, k_scales=k_scales, v_scales=v_scales)
+    lib, s = _lib_on(q_raw.device), _stream_handle(stream, q_raw.device)
+    head = (_ptr(q_raw), _ptr(k_raw), _ptr(v_raw), _ptr(w_q), _ptr(w_k))
+    cache = (_ptr(k), _ptr(v), _ptr(k_scales), _ptr(v_scales))
+    if block_table is None:
+        st = lib.gqa_prepare_decode_quant(*head, _ptr(seq_lens), B, H, KVH, D, _ptr(q_out), *cache,
+                                          k.shape[1], s)
+    else:
+        st = lib.gqa_prepare_decode_quant_paged(*head, _ptr(block_table), _ptr(seq_lens), B,
+                                                k.shape[0], block_table.shape[1], k.shape[1], H,
+                                                KVH, D, _ptr(q_out), *cache, s)
+    _check(fn, st)
+
+
+def gqa_prepare_decode_quant(q_raw: torch.Tensor, k_raw: torch.Tensor, v_raw: torch.Tensor,
+                             w_q: torch.Tensor, w_k: torch.Tensor, seq_lens: torch.Tensor,
+                             q_out: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                             k_scales: torch.Tensor, v_scales: torch.Tensor, stream=None) -> None:
+    """gqa_prepare_decode into a contiguous 8-bit cache k, v [B,S,KVH,D] (float8_e4m3fn) with
+    scales [B,ceil(S/16),KVH]: position seq_lens[b] - 1."""
+    _prepare_quant("gqa_prepare_decode_quant", q_raw, k_raw, v_raw, w_q, w_k, None, seq_lens, q_out,
+                   k, v, k_scales, v_scales, stream)
+
+
+def gqa_prepare_decode_quant_paged(q_raw: torch.Tensor, k_raw: torch.Tensor, v_raw: torch.Tensor,
+                                   w_q: torch.Tensor, w_k: torch.Tensor, block_table: torch.Tensor,
+                                   seq_lens: torch.Tensor, q_out: torch.Tensor,
+                                   k_pages: torch.Tensor, v_pages: torch.Tensor,
+                                   k_scales: torch.Tensor, v_scales: torch.Tensor,
+                                   stream=None) -> None:
+    """gqa_prepare_decode_quant into page pools [P,16,KVH,D] with scales [P,KVH]."""
+    _require(block_table is not None, "block_table is required")
+    _prepare_quant("gqa_prepare_decode_quant_paged", q_raw, k_raw, v_raw, w_q, w_k, block_table,
+                   seq_lens, q_out, k_pages, v_pages, k_scales, v_scales, stream)
+
+
+def _decode_quant(fn, q, k, v, k_scales, v_scales, block_table, seq_lens, window, out, out_dtype,
+                  workspace, stream):
+    _check_tensor("q", q, torch.bfloat16, 3)
+    _check_tensor("seq_lens", seq_lens, torch.int32, 1)
+    B, H, D = q.shape
+    KVH, Dc = _check_quant_cache(k, v, k_scales, v_scales, B, block_table)
+    _require(Dc == D, "q and the cache must have the same head size")
+    _require(seq_lens.shape[0] == B, "seq_lens must have B entries")
+    if out is None:
+        out = torch.empty((B, H, D), dtype=out_dtype, device=q.device)
+    _check_tensor("out", out, out.dtype, 3)
+    _require(tuple(out.shape) == (B, H, D), "out must be [B, H, D]")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _same_device(q, k=k, v=v, k_scales=k_scales, v_scales=v_scales, block_table=block_table,
+                 seq_lens=seq_lens, out=out, workspace=workspace)
+    lib, s = _lib_on(q.device), _stream_handle(stream, q.device)
+    head = (_ptr(q), _ptr(k), _ptr(v), _ptr(k_scales), _ptr(v_scales))
+    tail = (H, KVH, D, int(window), _ptr(out), _out_code(out), _ptr(workspace), ws_bytes, s)
+    if block_table is None:
+        st = lib.gqa_decode_quant(*head, _ptr(seq_lens), B, k.shape[1], *tail)
+    else:
+        st = lib.gqa_decode_quant_paged(*head, _ptr(block_table), _ptr(seq_lens), B, k.shape[0],
+                                        block_table.shape[1], k.shape[1], *tail)
+    _check(fn, st)
+    return out
+
+
+def gqa_decode_quant(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_scales: torch.Tensor,
+                     v_scales: torch.Tensor, seq_lens: torch.Tensor, window: int,
+                     out: torch.Tensor | None = None, out_dtype=torch.bfloat16,
+                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """gqa_decode over a contiguous 8-bit cache: q [B,H,D] (bf16), k/v [B,S,KVH,D]
+    (float8_e4m3fn), scales [B,ceil(S/16),KVH] (fp32), seq_lens int32 [B]."""
+    return _decode_quant("gqa_decode_quant", q, k, v, k_scales, v_scales, None, seq_lens, window,
+                         out, out_dtype, workspace, stream)
+
+
+def gqa_decode_quant_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                           k_scales: torch.Tensor, v_scales: torch.Tensor,
+                           block_table: torch.Tensor, seq_lens: torch.Tensor, window: int,
+                           out: torch.Tensor | None = None, out_dtype=torch.bfloat16,
+                           workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """gqa_decode_quant over page pools [P,16,KVH,D] with scales [P,KVH]."""
+    _require(block_table is not None, "block_table is required")
+    return _decode_quant("gqa_decode_quant_paged", q, k_pages, v_pages, k_scales, v_scales,
+                         block_table, seq_lens, window, out, out_dtype, workspace, stream)
 
 
 def gqa_decode_noalloc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_lens: torch.Tensor,

@@ -108,8 +108,11 @@ bool keqv_long_history(int B, int capacity, int KVH, int grid) {
     return cap_tiles >= static_cast<long long>(kKeqvTcTilesPerCta) * grid;
 }
 
-// CTAs of one persistent launch on the current device (its SM count), or 0.
-int device_grid() {
+}  // namespace
+
+namespace gqa {
+
+int device_sms() {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
     DeviceState& ds = g_dev[dev];
@@ -120,12 +123,8 @@ int device_grid() {
             return 0;
         ds.sm_count = n;
     }
-    return ds.sm_count < kMaxCtas ? ds.sm_count : kMaxCtas;
+    return ds.sm_count;
 }
-
-}  // namespace
-
-namespace gqa {
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn_ptr = nullptr;
@@ -144,6 +143,12 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 }  // namespace gqa
 
 namespace {
+
+// CTAs of one persistent launch on the current device (its SM count), or 0.
+int device_grid() {
+    const int n = gqa::device_sms();
+    return n < kMaxCtas ? n : kMaxCtas;
+}
 
 struct CallShape {
     Geometry geo;
@@ -212,7 +217,8 @@ gqa_status_t run(const CallShape& c, bool paged, const void* q, const void* k, c
                  const int32_t* block_table, const int32_t* seq_lens, uint64_t rows,
                  uint64_t outer, int capacity, int ring, int num_pages, int max_pages, void* out,
                  gqa_out_dtype_t out_dtype, void* workspace, size_t workspace_bytes,
-                 cudaStream_t stream, const void* w_k = nullptr, bool multi_query = false) {
+                 cudaStream_t stream, const void* w_k = nullptr, bool multi_query = false,
+                 const float* k_scales = nullptr, const float* v_scales = nullptr) {
     if (!gqa::tensor_map_encoder()) return GQA_ERR_CUDA;
     void* ws = nullptr;
     WorkspaceLayout lay;
@@ -253,6 +259,12 @@ gqa_status_t run(const CallShape& c, bool paged, const void* q, const void* k, c
     a.p.test_flags = g_test_mode.load(std::memory_order_relaxed);
     a.grid = grid;
     a.stream = stream;
+    if (k_scales) {   // 8-bit cache
+        a.k_scales = k_scales;
+        a.v_scales = v_scales;
+        return gqa::launch_quant(a, c.geo == Geometry::kSliding, paged) == cudaSuccess ? GQA_OK
+                                                                                      : GQA_ERR_CUDA;
+    }
     if (w_k) {
         // single K=V cache: keys derived in the kernel with the global layers' rotary
         // frequencies theta^(-2i/D), i < 64, theta = 1e6
@@ -446,6 +458,44 @@ gqa_status_t gqa_decode_mq_paged(const void* q, const void* k_pages, const void*
                static_cast<uint64_t>(P), max_pages * GQA_PAGE_SIZE, 0, P, max_pages, out,
                out_dtype, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream),
                nullptr, true);
+}
+
+gqa_status_t gqa_decode_quant(const void* q, const void* k, const void* v, const float* k_scales,
+                              const float* v_scales, const int32_t* seq_lens, int B, int S, int H,
+                              int KVH, int D, int window, void* out, gqa_out_dtype_t out_dtype,
+                              void* workspace, size_t workspace_bytes, gqa_stream_t stream) {
+    const CallShape c{geometry_of(H, KVH, D), B, H, KVH, D, window};
+    if (S < 1 || S > GQA_MAX_SEQ) return GQA_ERR_INVALID_ARGUMENT;
+    gqa_status_t st = check_common(c, q, out, seq_lens, out_dtype);
+    if (st != GQA_OK || B == 0) return st;
+    if (!k || !v || !k_scales || !v_scales || !aligned(k, 16) || !aligned(v, 16) ||
+        !aligned(k_scales, 4) || !aligned(v_scales, 4))
+        return GQA_ERR_INVALID_ARGUMENT;
+    return run(c, false, q, k, v, nullptr, seq_lens, static_cast<uint64_t>(S),
+               static_cast<uint64_t>(B), S, 0, 0, 0, out, out_dtype, workspace, workspace_bytes,
+               reinterpret_cast<cudaStream_t>(stream), nullptr, false, k_scales, v_scales);
+}
+
+gqa_status_t gqa_decode_quant_paged(const void* q, const void* k_pages, const void* v_pages,
+                                    const float* k_scales, const float* v_scales,
+                                    const int32_t* block_table, const int32_t* seq_lens, int B,
+                                    int P, int max_pages, int page_size, int H, int KVH, int D,
+                                    int window, void* out, gqa_out_dtype_t out_dtype,
+                                    void* workspace, size_t workspace_bytes, gqa_stream_t stream) {
+    const CallShape c{geometry_of(H, KVH, D), B, H, KVH, D, window};
+    if (page_size != GQA_PAGE_SIZE || P < 1 || max_pages < 1 ||
+        static_cast<int64_t>(max_pages) * GQA_PAGE_SIZE > GQA_MAX_SEQ)
+        return GQA_ERR_INVALID_ARGUMENT;
+    gqa_status_t st = check_common(c, q, out, seq_lens, out_dtype);
+    if (st != GQA_OK || B == 0) return st;
+    if (!k_pages || !v_pages || !k_scales || !v_scales || !block_table || !aligned(k_pages, 16) ||
+        !aligned(v_pages, 16) || !aligned(k_scales, 4) || !aligned(v_scales, 4) ||
+        !aligned(block_table, 4))
+        return GQA_ERR_INVALID_ARGUMENT;
+    return run(c, true, q, k_pages, v_pages, block_table, seq_lens, GQA_PAGE_SIZE,
+               static_cast<uint64_t>(P), max_pages * GQA_PAGE_SIZE, 0, P, max_pages, out,
+               out_dtype, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream),
+               nullptr, false, k_scales, v_scales);
 }
 
 gqa_status_t gqa_check_inputs_host(const int32_t* seq_lens, int B, int capacity, int window,

@@ -46,6 +46,53 @@ struct PrepareParams {
     double freq[kPrepareMaxRot];  // theta^(-2i/D), i < n_rot
 };
 
+// (cos, sin) of pos * freq, the angle reduced mod 2 pi in fp64.
+__device__ __forceinline__ float2 rope_angle(int pos, double freq) {
+    const double a = static_cast<double>(pos) * freq;
+    const double turns = rint(a * 0.15915494309189535);   // 1 / (2 pi)
+    const double r = fma(-turns, 6.283185307179586, a);
+    float sn, c;
+    sincosf(static_cast<float>(r), &sn, &c);
+    return make_float2(c, sn);
+}
+
+// One head vector over a warp: x / sqrt(mean(x^2) + 1e-6), and with a weight w times w and
+// rotated by cs (q and k heads; v heads have w = null).  Lane l holds the elements
+// [kPer l, kPer l + kPer) of each half in x.
+template <int D>
+__device__ __forceinline__ void head_norm_rope(float (&x)[2][D / 64], const __nv_bfloat16* w,
+                                               const float2* cs, int n_rot, int lane) {
+    constexpr int kHalf = D / 2;
+    constexpr int kPer = kHalf / 32;
+    float ss = 0.0f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) ss = fmaf(x[h][e], x[h][e], ss);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+    const float inv = 1.0f / sqrtf(ss / static_cast<float>(D) + 1e-6f);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            x[h][e] *= inv;
+            if (w) x[h][e] *= __bfloat162float(w[h * kHalf + kPer * lane + e]);
+        }
+    if (w) {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            const int i = kPer * lane + e;
+            if (i < n_rot) {
+                const float2 r = cs[i];
+                const float x0 = x[0][e], x1 = x[1][e];
+                x[0][e] = x0 * r.x - x1 * r.y;
+                x[1][e] = x1 * r.x + x0 * r.y;
+            }
+        }
+    }
+}
+
 template <int D, bool kPaged>
 __global__ void __launch_bounds__(kPrepareThreads)
     gqa_prepare_kernel(const PrepareParams p) {
@@ -109,46 +156,12 @@ __global__ void __launch_bounds__(kPrepareThreads)
                 x[h][e + 1] = __high2float(t);
             }
     }
-    if (tid < p.n_rot) {
-        const double a = static_cast<double>(pos) * p.freq[tid];
-        const double turns = rint(a * 0.15915494309189535);   // 1 / (2 pi)
-        const double r = fma(-turns, 6.283185307179586, a);
-        float sn, c;
-        sincosf(static_cast<float>(r), &sn, &c);
-        cs[tid] = make_float2(c, sn);
-    }
+    if (tid < p.n_rot) cs[tid] = rope_angle(pos, p.freq[tid]);
     __syncthreads();
     if (!active) return;
 
-    float ss = 0.0f;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) ss = fmaf(x[h][e], x[h][e], ss);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-    const float inv = 1.0f / sqrtf(ss / static_cast<float>(D) + 1e-6f);
     const bool weighted = is_q || is_k;
-    const __nv_bfloat16* w = is_q ? p.w_q : p.w_k;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-            x[h][e] *= inv;
-            if (weighted) x[h][e] *= __bfloat162float(w[h * kHalf + kPer * lane + e]);
-        }
-    if (weighted) {
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-            const int i = kPer * lane + e;
-            if (i < p.n_rot) {
-                const float2 r = cs[i];
-                const float x0 = x[0][e], x1 = x[1][e];
-                x[0][e] = x0 * r.x - x1 * r.y;
-                x[1][e] = x1 * r.x + x0 * r.y;
-            }
-        }
-    }
+    head_norm_rope<D>(x, weighted ? (is_q ? p.w_q : p.w_k) : nullptr, cs, p.n_rot, lane);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll

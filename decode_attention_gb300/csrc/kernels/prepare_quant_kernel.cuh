@@ -1,0 +1,134 @@
+// The decode-step producer (prepare_kernel.cuh: norms, rotary positions) writing the new
+// token of each sequence into the 8-bit cache (quant_cache.cuh).
+//
+// The same grid: a warp per head vector.  A k or v warp codes its row from the fp32
+// result (one rounding); at the first position of a block the scale starts anew, later
+// in the block it never shrinks, and when it grows the warp re-codes the block's earlier
+// rows of its head.
+#pragma once
+
+#include "prepare_kernel.cuh"
+#include "quant_cache.cuh"
+
+namespace gqa {
+
+struct PrepareQuantParams {
+    const __nv_bfloat16* q_raw;   // [B, H, D]
+    const __nv_bfloat16* k_raw;   // [B, KVH, D]
+    const __nv_bfloat16* v_raw;   // [B, KVH, D]
+    const __nv_bfloat16* w_q;     // [D]
+    const __nv_bfloat16* w_k;     // [D]
+    const int32_t* seq_lens;      // [B], lengths after the append
+    __nv_bfloat16* q_out;         // [B, H, D]
+    QuantCache cache;
+    int B, H;
+    int n_rot;                    // rotated pairs
+    double freq[kPrepareMaxRot];  // theta^(-2i/D), i < n_rot
+};
+
+template <int D>
+__global__ void __launch_bounds__(kPrepareThreads)
+    gqa_prepare_quant_kernel(const PrepareQuantParams p) {
+    constexpr int kHalf = D / 2;
+    constexpr int kPer = kHalf / 32;   // elements per lane in each half: 4 or 8
+    constexpr int kWords = kPer / 4;   // code words per lane in each half
+    __shared__ float2 cs[kPrepareMaxRot];
+
+    ptx::grid_dependency_wait();
+    ptx::allow_dependent_launch();
+
+    const QuantCache& c = p.cache;
+    const int b = blockIdx.x;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int vec = blockIdx.y * (kPrepareThreads / 32) + warp;   // q heads, k heads, v heads
+    const int pos = p.seq_lens[b] - 1;
+    if (pos < 0) return;   // no new token
+    const bool is_q = vec < p.H;
+    const bool is_k = !is_q && vec < p.H + c.KVH;
+    const int kvh = is_q ? 0 : (is_k ? vec - p.H : vec - p.H - c.KVH);
+    size_t row = 0, scale_row = 0;
+    const bool active =
+        vec < p.H + 2 * c.KVH &&
+        (is_q || (pos < c.capacity() && c.locate(b, pos / kQuantBlock, &row, &scale_row)));
+    const int slot = pos % kQuantBlock;
+    const size_t stride = static_cast<size_t>(c.KVH) * D;
+    uint8_t* codes = nullptr;   // this head's first row of the block
+    float* scale = nullptr;
+    float old = 0.0f;
+
+    float x[2][kPer];
+    if (active) {
+        const __nv_bfloat16* src =
+            is_q ? p.q_raw + (static_cast<size_t>(b) * p.H + vec) * D
+                 : (is_k ? p.k_raw : p.v_raw) + (static_cast<size_t>(b) * c.KVH + kvh) * D;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < kPer; e += 2) {
+                const __nv_bfloat162 t =
+                    *reinterpret_cast<const __nv_bfloat162*>(src + h * kHalf + kPer * lane + e);
+                x[h][e] = __low2float(t);
+                x[h][e + 1] = __high2float(t);
+            }
+        if (!is_q) {
+            codes = (is_k ? c.k : c.v) + (row * c.KVH + kvh) * D;
+            scale = (is_k ? c.k_scales : c.v_scales) + scale_row * c.KVH + kvh;
+            if (slot > 0) old = *scale;
+        }
+    }
+    if (tid < p.n_rot) cs[tid] = rope_angle(pos, p.freq[tid]);
+    __syncthreads();
+    if (!active) return;
+
+    head_norm_rope<D>(x, is_q ? p.w_q : (is_k ? p.w_k : nullptr), cs, p.n_rot, lane);
+    if (is_q) {
+        __nv_bfloat16* dst = p.q_out + (static_cast<size_t>(b) * p.H + vec) * D;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < kPer; e += 2)
+                *reinterpret_cast<__nv_bfloat162*>(dst + h * kHalf + kPer * lane + e) =
+                    __floats2bfloat162_rn(x[h][e], x[h][e + 1]);
+        return;
+    }
+
+    float amax = 0.0f;   // largest finite magnitude
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            x[h][e] = inf_to_nan(x[h][e]);
+            amax = fmaxf(amax, fabsf(x[h][e]));   // a NaN is passed over
+        }
+    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+    int e = quant_exponent(amax);
+    if (slot > 0) {
+        const int eo = scale_exponent(old);
+        if (e > eo) {
+            const float f = pow2f(max(eo - e, -126));
+            for (int j = 0; j < slot; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t* r = reinterpret_cast<uint32_t*>(codes + j * stride + h * kHalf + kPer * lane);
+#pragma unroll
+                    for (int w = 0; w < kWords; ++w) r[w] = recode4(r[w], f);
+                }
+        } else {
+            e = eo;
+        }
+    }
+    const float inv = pow2f(-e);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t* r = reinterpret_cast<uint32_t*>(codes + slot * stride + h * kHalf + kPer * lane);
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+            const float* y = &x[h][4 * w];
+            r[w] = ptx::float2_to_e4m3x2(y[0] * inv, y[1] * inv) |
+                   (static_cast<uint32_t>(ptx::float2_to_e4m3x2(y[2] * inv, y[3] * inv)) << 16);
+        }
+    }
+    if (lane == 0) *scale = pow2f(e);
+}
+
+}  // namespace gqa

@@ -1,0 +1,91 @@
+// Reading the 8-bit cache (quant_cache.cuh) back: out[b, s] = scale * code for the
+// positions s in [lo_b, min(L_b, out_rows)), in bf16 (exact: 4 significant bits, exponents
+// within range) or fp32.  Other rows of the output are left as they are.
+//
+// A CTA takes one block of 16 positions of K or V, 16 * KVH * D contiguous codes; a
+// thread converts 8 codes at a time.
+#pragma once
+
+#include "quant_cache.cuh"
+
+namespace gqa {
+
+constexpr int kReadThreads = 256;
+
+struct ReadQuantParams {
+    QuantCache cache;
+    const int32_t* seq_lens;   // [B]
+    void* k_out;               // [B, out_rows, KVH, D]
+    void* v_out;
+    int B, window, out_rows;
+};
+
+template <int KVH, int D, bool kF32>
+__global__ void __launch_bounds__(kReadThreads)
+    gqa_read_quant_kernel(const ReadQuantParams p) {
+    constexpr int kRow = KVH * D;                                 // codes per position
+    constexpr int kSteps = kQuantBlock * kRow / (8 * kReadThreads);
+    __shared__ BlockIndex idx;
+
+    ptx::grid_dependency_wait();
+    ptx::allow_dependent_launch();
+
+    const QuantCache& c = p.cache;
+    const int capacity = c.capacity();
+    auto range = [&](int b, int* lo) {   // positions [*lo, returned)
+        const int L = min(max(p.seq_lens[b], 0), capacity);
+        *lo = p.window > 0 && L > p.window ? L - p.window : 0;
+        return min(L, p.out_rows);
+    };
+    idx.build(p.B, [&](int b) {
+        int lo;
+        const int hi = range(b, &lo);
+        return hi > lo ? (hi - 1) / kQuantBlock - lo / kQuantBlock + 1 : 0;
+    });
+    const uint32_t total = 2u * idx.pref[p.B];   // <= 2 * 256 * 2^14 blocks
+
+    for (uint32_t it = blockIdx.x; it < total; it += gridDim.x) {
+        const bool is_v = it & 1u;
+        const uint32_t x = it >> 1;
+        const int b = idx.seq_of(p.B, x);
+        int lo;
+        const int hi = range(b, &lo);
+        const int blk = lo / kQuantBlock + static_cast<int>(x - idx.pref[b]);
+        const int base = blk * kQuantBlock;
+        size_t row, scale_row;
+        if (!c.locate(b, blk, &row, &scale_row)) continue;
+        const uint8_t* src = (is_v ? c.v : c.k) + row * kRow;
+        const float* scale = (is_v ? c.v_scales : c.k_scales) + scale_row * KVH;
+        const size_t out0 = (static_cast<size_t>(b) * p.out_rows + base) * kRow;
+#pragma unroll 4
+        for (int s = 0; s < kSteps; ++s) {
+            const int at = (s * kReadThreads + static_cast<int>(threadIdx.x)) * 8;
+            const int pos = base + at / kRow;
+            if (pos < lo || pos >= hi) continue;
+            const uint2 w = __ldcs(reinterpret_cast<const uint2*>(src + at));
+            const float f = pow2f(scale_exponent(__ldg(scale + (at % kRow) / D)));
+            float2 v[4] = {ptx::e4m3x2_to_float2(static_cast<uint16_t>(w.x)),
+                           ptx::e4m3x2_to_float2(static_cast<uint16_t>(w.x >> 16)),
+                           ptx::e4m3x2_to_float2(static_cast<uint16_t>(w.y)),
+                           ptx::e4m3x2_to_float2(static_cast<uint16_t>(w.y >> 16))};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = make_float2(v[i].x * f, v[i].y * f);
+            if (kF32) {
+                float4* o = reinterpret_cast<float4*>(static_cast<float*>(is_v ? p.v_out : p.k_out) + out0 + at);
+                __stcs(o, make_float4(v[0].x, v[0].y, v[1].x, v[1].y));
+                __stcs(o + 1, make_float4(v[2].x, v[2].y, v[3].x, v[3].y));
+            } else {
+                uint4 o;
+                uint32_t* ow = &o.x;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const __nv_bfloat162 t = __floats2bfloat162_rn(v[i].x, v[i].y);
+                    ow[i] = *reinterpret_cast<const uint32_t*>(&t);
+                }
+                __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_v ? p.v_out : p.k_out) + out0 + at), o);
+            }
+        }
+    }
+}
+
+}  // namespace gqa

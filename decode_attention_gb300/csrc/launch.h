@@ -18,6 +18,8 @@ struct LaunchArgs {
     const void* v;          // V cache / page pool
     uint64_t rows;          // positions per sequence (contiguous) or slots per page (paged)
     uint64_t outer;         // sequences (contiguous) or pages (paged)
+    const float* k_scales;  // 8-bit cache only: block scales
+    const float* v_scales;
     DecodeParams p;
     int grid;
     cudaStream_t stream;
@@ -41,6 +43,13 @@ int mq_max_queries(bool sliding);
 // cache; a.p.keqv_operand: workspace room for the scores' operand).
 cudaError_t launch_keqv_tc(const LaunchArgs& a, bool paged);
 size_t smem_bytes_mq(bool sliding);
+
+// Decode over the 8-bit cache: a.k and a.v are e4m3 codes, a.k_scales and a.v_scales
+// their block scales.
+cudaError_t launch_quant(const LaunchArgs& a, bool sliding, bool paged);
+
+// SM count of the current device (cached per device), or 0.
+int device_sms();
 
 // Bytes of dynamic shared memory each geometry's kernel requests.
 size_t smem_bytes_sliding();

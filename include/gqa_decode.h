@@ -357,6 +357,122 @@ gqa_status_t gqa_decode_mq_paged(const void *q, const void *k_pages, const void 
                                  void *workspace, size_t workspace_bytes, gqa_stream_t stream);
 
 /*
+ * The 8-bit KV cache: half the bytes of a bf16 cache.  Keys and values are held as
+ * e4m3 codes (1-4-3, largest 448, no infinities) with one fp32 scale for each block
+ * of 16 positions and KV head, for K and for V:
+ *     value = scale * code,   scale = 2^e with the smallest e that keeps the block's
+ *     largest finite magnitude within 448 * 2^e, e in [-64, 64].
+ * Writing rounds each value once (nearest even); values beyond 448 * 2^64 are clamped
+ * to it, NaN and infinities are held as NaN.  Every call takes the exponent field of a
+ * stored scale, clamped to [-64, 64], as e.  No counterpart on the reference pages:
+ * a format of this library.
+ *
+ *   contiguous  k, v              e4m3 [B, S, KVH, D], row s is position s
+ *               k_scales, v_scales fp32 [B, ceil(S / 16), KVH]
+ *   paged       k_pages, v_pages  e4m3 [P, 16, KVH, D], as for gqa_decode_paged
+ *               k_scales, v_scales fp32 [P, KVH]
+ * Nothing has to be zeroed before the first use: a block's scale starts anew when its
+ * first position is written, and no row or scale that was not written is used.
+ * Codes are 16-byte aligned, scales 4-byte.  Geometries: those of gqa_decode.
+ *
+ * Quantised append of K/V rows (a prompt, or a chunk of one), already normed and
+ * rotated at their positions.  The batch is ragged: the new tokens of all sequences
+ * are packed one after the other.
+ *
+ *   k_new, v_new   bf16 [N, KVH, D]
+ *   token_offsets  int32 [B + 1] (device): sequence b's tokens are rows
+ *                  [token_offsets[b], token_offsets[b + 1]) of k_new and v_new
+ *   seq_lens       int32 [B] (device): lengths AFTER the append; with n_b new tokens
+ *                  they go to the positions [L_b - n_b, L_b)
+ * A block whose first position is among the new ones gets the scale of its new rows.  A
+ * block that holds earlier rows keeps the larger of its scale and that of the new rows;
+ * when the scale grows, the earlier rows are coded again (exact, but for values that
+ * become subnormal codes).  Rows from L_b on are left as they were.  Sequences without
+ * new tokens are skipped, and so is a sequence whose offsets lie outside [0, N] or
+ * whose length is below n_b or above the capacity.  A page id outside [0, P) skips that
+ * block's write (the decode call then reports it).  The blocks written by one call must
+ * be distinct: sequences that share a page must not both write to it.
+ * N == 0 or B == 0: GQA_OK, nothing enqueued.  Errors as for gqa_decode and
+ * gqa_decode_paged (N outside [0, 256 * 262144]: GQA_ERR_INVALID_ARGUMENT).
+ * One kernel launch, no workspace.
+ */
+gqa_status_t gqa_append_quant(const void *k_new, const void *v_new, const int32_t *token_offsets,
+                              const int32_t *seq_lens, int B, int N, int S, int KVH, int D,
+                              void *k, void *v, float *k_scales, float *v_scales,
+                              gqa_stream_t stream);
+
+gqa_status_t gqa_append_quant_paged(const void *k_new, const void *v_new,
+                                    const int32_t *token_offsets, const int32_t *block_table,
+                                    const int32_t *seq_lens, int B, int N, int P, int max_pages,
+                                    int page_size, int KVH, int D, void *k_pages, void *v_pages,
+                                    float *k_scales, float *v_scales, gqa_stream_t stream);
+
+/*
+ * Reading the 8-bit cache back: row s of k_out[b], v_out[b] gets the values of position
+ * s, for the positions [lo_b, min(L_b, out_rows)) with lo_b = max(0, L_b - window)
+ * (window > 0) or 0.  Other rows are left as they were, and so are those of a page whose
+ * id lies outside [0, P).
+ *
+ *   seq_lens      int32 [B] (device), clamped to [0, capacity]
+ *   k_out, v_out  [B, out_rows, KVH, D], bf16 (exact) or fp32 per out_dtype, 16-byte aligned
+ * One kernel launch, no workspace.  Errors as for gqa_decode and gqa_decode_paged, and
+ * GQA_ERR_INVALID_ARGUMENT for out_rows outside [1, 262144].
+ */
+gqa_status_t gqa_read_quant(const void *k, const void *v, const float *k_scales,
+                            const float *v_scales, const int32_t *seq_lens, int B, int S, int KVH,
+                            int D, int window, void *k_out, void *v_out, int out_rows,
+                            gqa_out_dtype_t out_dtype, gqa_stream_t stream);
+
+gqa_status_t gqa_read_quant_paged(const void *k_pages, const void *v_pages, const float *k_scales,
+                                  const float *v_scales, const int32_t *block_table,
+                                  const int32_t *seq_lens, int B, int P, int max_pages,
+                                  int page_size, int KVH, int D, int window, void *k_out,
+                                  void *v_out, int out_rows, gqa_out_dtype_t out_dtype,
+                                  gqa_stream_t stream);
+
+/*
+ * gqa_prepare_decode into the 8-bit cache: the same norms and rotary positions for one
+ * new token per sequence, q_out in bf16, the token's key and value coded from the fp32
+ * results into position L - 1 under the append's rules (v_raw is required: there is no
+ * 8-bit form of the single K=V cache).  Sequences with L < 1 are skipped; a token past
+ * the capacity or on a page id outside [0, P) is not written.  Errors as for
+ * gqa_prepare_decode.
+ */
+gqa_status_t gqa_prepare_decode_quant(const void *q_raw, const void *k_raw, const void *v_raw,
+                                      const void *w_q, const void *w_k, const int32_t *seq_lens,
+                                      int B, int H, int KVH, int D, void *q_out, void *k, void *v,
+                                      float *k_scales, float *v_scales, int rows,
+                                      gqa_stream_t stream);
+
+gqa_status_t gqa_prepare_decode_quant_paged(const void *q_raw, const void *k_raw, const void *v_raw,
+                                            const void *w_q, const void *w_k,
+                                            const int32_t *block_table, const int32_t *seq_lens,
+                                            int B, int P, int max_pages, int page_size, int H,
+                                            int KVH, int D, void *q_out, void *k_pages,
+                                            void *v_pages, float *k_scales, float *v_scales,
+                                            gqa_stream_t stream);
+
+/*
+ * gqa_decode and gqa_decode_paged over the 8-bit cache: the same attention core on the
+ * values scale * code.  Scores, softmax and sums are held in fp32, and the weights are
+ * applied to at least 16 significant bits, so the result differs from the core's on
+ * those values by fp32 rounding.  Everything else -- q, window, out, workspace (the same
+ * size), status bits, errors -- is as for gqa_decode and gqa_decode_paged; null or
+ * misaligned scales return GQA_ERR_INVALID_ARGUMENT.
+ */
+gqa_status_t gqa_decode_quant(const void *q, const void *k, const void *v, const float *k_scales,
+                              const float *v_scales, const int32_t *seq_lens, int B, int S, int H,
+                              int KVH, int D, int window, void *out, gqa_out_dtype_t out_dtype,
+                              void *workspace, size_t workspace_bytes, gqa_stream_t stream);
+
+gqa_status_t gqa_decode_quant_paged(const void *q, const void *k_pages, const void *v_pages,
+                                    const float *k_scales, const float *v_scales,
+                                    const int32_t *block_table, const int32_t *seq_lens, int B,
+                                    int P, int max_pages, int page_size, int H, int KVH, int D,
+                                    int window, void *out, gqa_out_dtype_t out_dtype,
+                                    void *workspace, size_t workspace_bytes, gqa_stream_t stream);
+
+/*
  * Host-side check of the device-resident inputs, for tests and debugging: the
  * caller copies seq_lens (and the block table) to host memory and passes them
  * here.  The decode calls never read these arrays on the host (they stay on the
