@@ -411,9 +411,14 @@ __device__ __forceinline__ void store_out4(const DecodeParams& p, size_t idx, fl
 // caller passes the first stage buffer, which no copy has been issued to yet).
 // One short pass per warp instead of one warp walking eight sequences per lane
 // keeps the plan's latency (and the code fetched cold on each SM) small.
+//
+// kAlign: ranges are widened to whole blocks of kAlign positions, which makes every piece
+// start and end on a block when `unit` is whole blocks too; the caller masks the
+// positions outside the attended range.
 // ---------------------------------------------------------------------------
 constexpr int kPlanWarps = kMaxBatch / 32;   // 8
 
+template <int kAlign = 1>
 __device__ __forceinline__ void build_plan(PlanSmem& pl, const DecodeParams& p, int grid, int warp,
                                            int lane, int cta, int unit, uint32_t* xsum) {
     const int B = p.B, KVH = p.KVH;
@@ -431,8 +436,10 @@ __device__ __forceinline__ void build_plan(PlanSmem& pl, const DecodeParams& p, 
         // union of the queries' ranges: query 0 (position x - T) starts the
         // earliest window, the last query ends at x
         const int span = p.window > 0 ? p.window + (p.T > 1 ? p.T - 1 : 0) : 0;
-        const int lo = (span > 0 && x > span) ? x - span : 0;
-        n = in_batch ? x - lo : 0;
+        const int first = (span > 0 && x > span) ? x - span : 0;
+        // (kAlign > 1: whole blocks of kAlign positions around the range)
+        const int lo = first / kAlign * kAlign;
+        n = in_batch ? (x + kAlign - 1) / kAlign * kAlign - lo : 0;
         if (in_batch) {
             pl.lo[b] = lo;
             pl.n[b] = n;

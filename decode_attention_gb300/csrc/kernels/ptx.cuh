@@ -155,6 +155,38 @@ __device__ __forceinline__ void bulk_copy_g2s(uint32_t dst, const void* src, uin
         : "memory");
 }
 
+// 4 bytes global -> shared, asynchronous (completion: cp_async_mbar_arrive).
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// One of the arrivals `bar` was initialised for, made when every cp_async4 this thread
+// issued so far has landed.
+__device__ __forceinline__ void cp_async_mbar_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// 2^x, results below 2^-126 flushed to zero.
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two floats as packed f16 (x low), nearest even; and back.
+__device__ __forceinline__ uint32_t f16x2_pack(float x, float y) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+    return r;
+}
+__device__ __forceinline__ float2 f16x2_unpack(uint32_t h) {
+    float2 r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "r"(h));
+    return r;
+}
+
 // ---- barriers among a subset of warps -----------------------------------------
 
 __device__ __forceinline__ void named_barrier_sync(uint32_t id, uint32_t threads) {
@@ -246,13 +278,7 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v) {
     return r;
 }
 __device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t v) {
-    const uint32_t h = e4m3x2_to_f16x2(v);
-    float2 r;
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-        "cvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "r"(h));
-    return r;
+    return f16x2_unpack(e4m3x2_to_f16x2(v));
 }
 // Two floats as e4m3 codes, x in the low byte: nearest even, beyond +-448 clamped, NaN
 // to the NaN code.

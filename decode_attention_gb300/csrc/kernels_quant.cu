@@ -1,4 +1,7 @@
-// Decode attention kernels over the 8-bit cache, both geometries.
+// Decode attention kernels over the 8-bit cache, both geometries, contiguous and paged.
+#include <mutex>
+
+#include "kernels/combine_kernel.cuh"
 #include "kernels/decode_quant_kernel.cuh"
 #include "launch.h"
 
@@ -6,18 +9,67 @@ namespace gqa {
 
 namespace {
 
-template <int G, int D>
+// Tensor map of K or V codes: 4-D view (128 codes, row, 128-code chunk of the KVH * D row,
+// outer), box (128, 16, D / 128, 1) -> shared [D / 128][16 rows][128 B], 16-byte units
+// permuted by row so that 8 consecutive rows of one chunk hit distinct banks.
+bool encode_codes_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t outer, int KVH,
+                      int D) {
+    const uint64_t row_bytes = static_cast<uint64_t>(KVH) * D;
+    const cuuint64_t dims[4] = {128, rows, row_bytes / 128, outer};
+    const cuuint64_t strides[3] = {row_bytes, 128, row_bytes * rows};
+    const cuuint32_t box[4] = {128, kQuantBlock, static_cast<cuuint32_t>(D / 128), 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims,
+                            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class Pol, bool kPaged>
 cudaError_t launch(const LaunchArgs& a, const DecodeQuantParams& p) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.p.KVH), static_cast<unsigned>(a.p.B));
-    cfg.blockDim = dim3(kDecodeQuantThreads);
-    cfg.stream = a.stream;
+    constexpr size_t kSmem = sizeof(QuantSmem<Pol>) + 1024;   // + alignment slack
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+    constexpr int kMaxDevices = 64;
+    static std::once_flag once[kMaxDevices];
+    static cudaError_t attr_err[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    std::call_once(once[dev], [&] {
+        attr_err[dev] = cudaFuncSetAttribute(gqa_decode_quant_kernel<Pol, kPaged>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(kSmem));
+    });
+    if (attr_err[dev] != cudaSuccess) return attr_err[dev];
+    CUtensorMap tm_k, tm_v;
+    if (!encode_codes_map(&tm_k, a.k, a.rows, a.outer, a.p.KVH, Pol::D) ||
+        !encode_codes_map(&tm_v, a.v, a.rows, a.outer, a.p.KVH, Pol::D))
+        return cudaErrorInvalidValue;
+
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.grid));
+    cfg.blockDim = dim3((Pol::NC + 1) * 32);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = a.stream;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gqa_decode_quant_kernel<G, D>, p);
+    e = cudaLaunchKernelEx(&cfg, gqa_decode_quant_kernel<Pol, kPaged>, tm_k, tm_v, p);
+    if (e != cudaSuccess || Pol::kMergeInKernel) return e;
+
+    const int segments = a.p.B * a.p.KVH;
+    constexpr int kChunksPerSeg = (Pol::G * Pol::D / 4 + kCombineThreads - 1) / kCombineThreads;
+    const int items = segments * kChunksPerSeg;
+    const int most = kCombineBlocksPerSm * a.grid;
+    cudaLaunchConfig_t ccfg = cfg;
+    ccfg.gridDim = dim3(static_cast<unsigned>(items < most ? items : most));
+    ccfg.blockDim = dim3(kCombineThreads);
+    ccfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&ccfg, gqa_combine_kernel<Pol::G, Pol::D>, a.p, segments);
 }
 
 }  // namespace
@@ -25,16 +77,11 @@ cudaError_t launch(const LaunchArgs& a, const DecodeQuantParams& p) {
 cudaError_t launch_quant(const LaunchArgs& a, bool sliding, bool paged) {
     DecodeQuantParams p;
     p.d = a.p;
-    p.cache.k = static_cast<uint8_t*>(const_cast<void*>(a.k));
-    p.cache.v = static_cast<uint8_t*>(const_cast<void*>(a.v));
-    p.cache.k_scales = const_cast<float*>(a.k_scales);
-    p.cache.v_scales = const_cast<float*>(a.v_scales);
-    p.cache.block_table = paged ? a.p.block_table : nullptr;
-    p.cache.rows = static_cast<int>(a.rows);
-    p.cache.max_pages = a.p.max_pages;
-    p.cache.num_pages = a.p.num_pages;
-    p.cache.KVH = a.p.KVH;
-    return sliding ? launch<2, 256>(a, p) : launch<8, 512>(a, p);
+    p.k_scales = a.k_scales;
+    p.v_scales = a.v_scales;
+    p.blocks = static_cast<int>((a.rows + kQuantBlock - 1) / kQuantBlock);
+    if (sliding) return paged ? launch<QuantSliding, true>(a, p) : launch<QuantSliding, false>(a, p);
+    return paged ? launch<QuantGlobal, true>(a, p) : launch<QuantGlobal, false>(a, p);
 }
 
 }  // namespace gqa
