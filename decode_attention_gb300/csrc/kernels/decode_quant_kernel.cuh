@@ -13,19 +13,28 @@
 // Both contractions run as warp-level f16 mma (m16n8k16, fp32 accumulate) with the cache
 // as the A operand, so that the g <= 8 query heads of a KV head fill the 8 columns of B
 // and no row is idle.  e4m3 widens to f16 exactly, two codes per instruction.  q is scaled
-// by a power of two per head and half of D, which makes its bf16 values exact in f16 down
-// to 2^-30 of the largest.
-//   scores  S[pos, h] = K[pos, :] . q[h, :], 16 positions (one block) per warp; the k index
+// by a power of two per head, which makes its bf16 values exact in f16 down to 2^-30 of
+// the largest.
+//   scores  S[pos, h] = K[pos, :] . q[h, :] for the 16 positions of a block; the k index
 //           pairs of an A fragment are the bytes (4t, 4t+1) and (4t+2, 4t+3) of a 16-byte
 //           unit, q's B fragment in the same order
-//   P.V     O^T[d, h] += V^T[d, pos] P[pos, h] for a D/8-wide slice of d per warp: 16-bit
-//           ldmatrix.trans delivers dims (2g, 2g+1) of two positions, one byte permute
-//           makes them rows g and g+8 of A.  At g = 2 the hi and lo parts of P are four
-//           of the 8 columns of one mma; at g = 8 they are two mma.
+//   P.V     O^T[d, h] += V^T[d, pos] P[pos, h]; 16-bit ldmatrix.trans delivers dims (2g, 2g+1)
+//           of two positions, one byte permute makes them rows g and g+8 of A.  movmatrix
+//           turns the weights from the scores' layout into B fragments.  At g = 2 the hi
+//           and lo parts of P are columns of one mma; at g = 8 they are two mma.
+// An mma truncates its sum, so long chains of them drift: a block's products start from
+// zero and are added to the accumulators by ordinary additions.
 //
-// Work split, pipeline, timeouts and merging are those of decode_kernel.cuh: a persistent
-// CTA per SM, a plan built from seq_lens on the device, one producer thread that streams K
-// and V tiles with TMA, 8 consumer warps.  Pieces start and end on blocks.
+// A warp works on whole blocks by itself: its own M, l and D x 8 accumulators, no exchange
+// with the other warps until the piece ends, when the 8 states are merged through shared
+// memory.  (With the 8 warps sharing each tile, one part of the dims each and a score tile
+// between the contractions, every warp repeats the softmax of all positions: 1370
+// instructions per warp and 128 positions at g = 2 against ~300 here.)
+//
+// Work split, timeouts and merging between CTAs are those of decode_kernel.cuh: a
+// persistent CTA per SM, a plan built from seq_lens on the device, one producer thread that
+// streams K and V with TMA through a ring of 16 KB slots, which the 8 consumer warps take in
+// turn.  Pieces start and end on blocks.
 #pragma once
 
 #include "decode_kernel.cuh"
@@ -40,295 +49,323 @@ struct DecodeQuantParams {
     int blocks;              // blocks per sequence (contiguous)
 };
 
-template <int kG, int kD, int kTP, int kStages, bool kMerge>
+// Registers: 12 warps (three warpgroups, the last one's first thread the producer) start
+// with 168 each; the producer's warpgroup gives up what the consumers' two take.
+constexpr int kQuantThreads = 384;
+constexpr int kQuantLaunchRegs = 168;
+constexpr int kQuantConsumerRegs = 224;
+constexpr int kQuantProducerRegs = 56;
+static_assert(2 * kQuantConsumerRegs + kQuantProducerRegs <= 3 * kQuantLaunchRegs, "register split");
+
+template <int kG, int kD, int kBlocksPerSlot, int kSlots, bool kMerge>
 struct QuantPolicy {
-    static constexpr int G = kG, D = kD, TP = kTP, STAGES = kStages, NC = 8;
+    static constexpr int G = kG, D = kD, NC = 8;
+    static constexpr int kBlocks = kBlocksPerSlot;       // blocks of 16 positions per slot
+    static constexpr int TP = kBlocks * kQuantBlock;     // positions per slot
+    static constexpr int SLOTS = kSlots;
     static constexpr bool kMergeInKernel = kMerge;
-    static constexpr int kBlocks = TP / kQuantBlock;    // blocks (m-tiles of the scores) per tile
-    static constexpr int kParts = NC / kBlocks;         // parts of D a block's scores are split in
-    static constexpr int kUnits = D / kParts / 16;      // 16-dim steps of a warp's scores
-    static constexpr int kDimTiles = D / NC / 16;       // m-tiles of 16 dims of a warp's output
-    static constexpr bool kSplitCols = G <= 2;          // hi and lo parts of P in one mma
-    static constexpr int kSStride = TP + 8;             // padded row of the score tile
-    static_assert(NC % kBlocks == 0 && kUnits % 2 == 0 && kDimTiles % 2 == 0, "tile shape");
+    static constexpr int kUnits = D / 16;                // 16-dim steps
+    static constexpr bool kSplitCols = G == 2;           // hi and lo parts of P in one mma
+    // q's B fragments: in registers (G = 2: 32), or in shared memory where the D x 8
+    // accumulators (128 registers) leave no room
+    static constexpr bool kQInSmem = D > 256;
+    static constexpr int kMergeDims = G == 2 ? 256 : 64;   // dims merged per round
+    static constexpr int kMergeStride = kMergeDims + 4;    // conflict-free float2 stores
+    static_assert((G == 2 || G == 8) && kUnits % 4 == 0 && D % kMergeDims == 0, "shape");
 };
 
-struct QuantTile {
+// One piece of work, published with its q.
+struct QuantPiece {
     int b, kvh;
-    int vlo, vhi;   // rows [vlo, vhi) of the tile are attended positions
+    int p0, p1;     // positions, whole blocks
+    int lo, hi;     // attended positions of the sequence
     int slot;       // workspace slot of the partial
-    int bad;        // blocks whose page id is out of range, one bit each
-    int flags;
+    int done;       // no more pieces
 };
 
 template <class Pol>
 struct alignas(1024) QuantSmem {
     static constexpr int kTileBytes = Pol::TP * Pol::D;
-    uint8_t kv[Pol::STAGES][2][kTileBytes];   // [stage][K, V][block][chunk][16 rows][128 B]
-    alignas(8) uint64_t full[Pol::STAGES];
-    alignas(8) uint64_t empty[Pol::STAGES];
-    alignas(8) uint64_t q_empty[2];
-    alignas(8) uint64_t stall_bar;            // kTestStall: a barrier nothing completes
-    QuantTile tile[Pol::STAGES];
-    float scales[Pol::STAGES][2][Pol::kBlocks];
+    uint8_t kv[Pol::SLOTS][2][kTileBytes];   // [slot][K, V][block][chunk][16 rows][128 B]
+    alignas(8) uint64_t full[Pol::SLOTS];
+    alignas(8) uint64_t empty[Pol::SLOTS];
+    alignas(8) uint64_t q_full, q_empty;
+    alignas(8) uint64_t stall_bar;           // kTestStall: a barrier nothing completes
+    float scales[Pol::SLOTS][2][Pol::kBlocks];
+    int bad[Pol::SLOTS];                     // blocks whose page id is out of range, one bit each
+    QuantPiece piece;
     PlanSmem plan;
-    int len[kMaxBatch];                       // clamped lengths
-    alignas(128) __nv_bfloat16 q[2][Pol::G * Pol::D];
-    alignas(16) float S[2][Pol::kParts][Pol::G][Pol::kSStride];   // [tile parity][part][head][position]
+    int len[kMaxBatch];                      // clamped lengths
+    alignas(128) __nv_bfloat16 q[Pol::G * Pol::D];
+    alignas(16) uint2 q_frag[Pol::kQInSmem ? Pol::kUnits : 1][32];
+    float wm[Pol::NC][8], wl[Pol::NC][8];    // each warp's M and l per column
+    alignas(16) float wacc[Pol::NC][Pol::G][Pol::kMergeStride];
     int abort_flag;
     int merge_last;
 };
 
 template <class Pol>
 struct QuantConsumer {
-    static constexpr int G = Pol::G, D = Pol::D, TP = Pol::TP;
-    static constexpr int kBlocks = Pol::kBlocks, kUnits = Pol::kUnits, kDimTiles = Pol::kDimTiles;
+    static constexpr int G = Pol::G, D = Pol::D, kUnits = Pol::kUnits;
+    static constexpr float kTop = 15.0f;    // largest exponent of a weight (f16 ends at 2^16)
+    static constexpr float kRoom = 3.0f;    // binades left above the maximum when M is set
 
-    uint32_t qb[kUnits][2];      // B fragments of q (column g = head) for this warp's part of D
-    float q_factor[2];           // undo q's scaling for columns 2t and 2t + 1
-    float acc[kDimTiles][4];     // rows: dims 2g (0, 1) and 2g + 1 (2, 3); columns 2t, 2t + 1
-    float m;                     // M of head column g
-    float l;                     // this lane's share of the normaliser of column g
+    uint2 qb[Pol::kQInSmem ? 1 : kUnits];   // B fragments of q (column g = head g % G)
+    float q_factor[2];           // undo q's scaling for columns 2t and 2t + 1, times log2(e)
+    float acc[kUnits][4];        // rows: dims 2g (0, 1) and 2g + 1 (2, 3); columns 2t, 2t + 1
+    float m[2];                  // M of columns 2t, 2t + 1
+    float l[2];                  // this lane's share of their normalisers
 
-    // Byte address of 16-byte unit `unit` of row r of block `blk` of a tile.
-    __device__ static __forceinline__ uint32_t unit_addr(uint32_t tile, int blk, int r, int unit) {
-        return tile + blk * (kQuantBlock * D) + (unit >> 3) * 2048 + r * 128 +
-               (((unit & 7) ^ (r & 7)) << 4);
+    // Byte address of 16-byte unit `unit` of row r of a block.
+    __device__ static __forceinline__ uint32_t unit_addr(uint32_t block, int r, int unit) {
+        return block + (unit >> 3) * 2048 + r * 128 + (((unit & 7) ^ (r & 7)) << 4);
     }
 
-    // q_heads: [G][D] bf16 in shared memory
-    __device__ __forceinline__ void begin(const __nv_bfloat16* q_heads, int warp, int lane) {
+    // q_heads: [G][D] bf16 in shared memory.  With q in shared memory each warp makes its
+    // share of the fragments (a barrier follows).
+    __device__ __forceinline__ void begin(const __nv_bfloat16* q_heads, uint2 (*frag)[32], int warp,
+                                          int lane) {
         const int g = lane >> 2, t = lane & 3;
-        const bool real = g < G;
-        const __nv_bfloat16* row =
-            q_heads + (real ? g : 0) * D + (warp / kBlocks) * (kUnits * 16) + 4 * t;
-        uint2 w[kUnits];
+        const __nv_bfloat16* row = q_heads + (g % G) * D + 4 * t;
         uint32_t top = 0;   // largest |q|: the bits of |bf16| order like the values
-#pragma unroll
+#pragma unroll 8
         for (int u = 0; u < kUnits; ++u) {
-            w[u] = *reinterpret_cast<const uint2*>(row + u * 16);
-            top = __vmaxu2(top, __vmaxu2(w[u].x & 0x7fff7fffu, w[u].y & 0x7fff7fffu));
+            const uint2 w = *reinterpret_cast<const uint2*>(row + u * 16);
+            top = __vmaxu2(top, __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu));
         }
         top = max(top & 0xffffu, top >> 16);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int e = max(static_cast<int>(top >> 7) - 127, -100);   // |q| < 2^(e + 1)
-        const float f = real ? pow2f(14 - e) : 0.0f;
+        const float f = pow2f(14 - e);
+        auto widen = [&](int u) {
+            const uint2 w = *reinterpret_cast<const uint2*>(row + u * 16);
+            return make_uint2(ptx::f16x2_pack(bf16lo(w.x) * f, bf16hi(w.x) * f),
+                              ptx::f16x2_pack(bf16lo(w.y) * f, bf16hi(w.y) * f));
+        };
+        if constexpr (Pol::kQInSmem) {
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
-            qb[u][0] = ptx::f16x2_pack(bf16lo(w[u].x) * f, bf16hi(w[u].x) * f);
-            qb[u][1] = ptx::f16x2_pack(bf16lo(w[u].y) * f, bf16hi(w[u].y) * f);
+            for (int i = 0; i < kUnits / Pol::NC; ++i) {
+                const int u = warp * (kUnits / Pol::NC) + i;
+                frag[u][lane] = widen(u);
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u) qb[u] = widen(u);
         }
-        const float undo = pow2f(e - 14);
+        const float undo = pow2f(e - 14) * kLog2e;
         q_factor[0] = __shfl_sync(0xffffffffu, undo, 8 * t);
         q_factor[1] = __shfl_sync(0xffffffffu, undo, 8 * t + 4);
 #pragma unroll
-        for (int i = 0; i < kDimTiles; ++i)
+        for (int i = 0; i < kUnits; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-        m = -INFINITY;
-        l = 0.0f;
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.0f;
     }
 
-    // Scores of this warp's block and part of D -> S[part][head][position].
-    __device__ __forceinline__ void scores(uint32_t k_tile, const float* k_scales,
-                                           float (*S)[G][Pol::kSStride], int warp, int lane) {
+    // One block: rows [first, last) are attended (all of them at first <= 0, last >= 16).
+    __device__ __forceinline__ void block(uint32_t k_blk, uint32_t v_blk, float k_scale,
+                                          float v_scale, int first, int last, bool bad,
+                                          uint32_t q_frag, int lane) {
         const int g = lane >> 2, t = lane & 3;
-        const int blk = warp % kBlocks, part = warp / kBlocks;
         const int mat = lane >> 3, r = (mat & 1) * 8 + (lane & 7);
-        float c[2][4];   // two independent accumulation chains
+        const bool whole = first <= 0 && last >= kQuantBlock && !bad;
+
+        float c[4][4];   // four independent chains
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) c[i][j] = 0.0f;
 #pragma unroll
         for (int u = 0; u < kUnits; u += 2) {
             uint32_t a[4];   // rows g, g + 8 of unit u, then of unit u + 1
-            ptx::ldmatrix_x4(unit_addr(k_tile, blk, r, part * kUnits + u + (mat >> 1)), a[0], a[1],
-                             a[2], a[3]);
+            ptx::ldmatrix_x4(unit_addr(k_blk, r, u + (mat >> 1)), a[0], a[1], a[2], a[3]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
+                const uint2 q = Pol::kQInSmem ? ptx::lds64(q_frag + (u + i) * 256 + lane * 8) : qb[Pol::kQInSmem ? 0 : u + i];
                 const uint32_t lo = a[2 * i], hi = a[2 * i + 1];
-                ptx::mma_f16_16816(c[i], ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(lo)),
+                ptx::mma_f16_16816(c[(u + i) & 3], ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(lo)),
                                    ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(hi)),
                                    ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(lo >> 16)),
-                                   ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(hi >> 16)),
-                                   qb[u + i][0], qb[u + i][1]);
+                                   ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(hi >> 16)), q.x, q.y);
             }
         }
-        const float fk = pow2f(scale_exponent(k_scales[blk]));
-        const int pos = blk * kQuantBlock + g;
+        // log2 of the weights: y = log2(e) score + ev - M, rows g (0, 1) and g + 8 (2, 3)
+        const float fk = pow2f(scale_exponent(k_scale));
+        const int ev = scale_exponent(v_scale);
+        const float f[2] = {fk * q_factor[0], fk * q_factor[1]};
+        // (rows outside the range: 2^-inf)
+        const float evf = static_cast<float>(ev);
+        bool row_ok[2] = {true, true};
+        if (!whole) {
+            row_ok[0] = g >= first && g < last;
+            row_ok[1] = g + 8 >= first && g + 8 < last;
+        }
+        auto level = [&](int i, float shift) {
+            const float v = fmaf(c[0][i], f[i & 1], shift);
+            return row_ok[i >> 1] ? v : -INFINITY;
+        };
+        float y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            c[0][i] = (c[0][i] + c[1][i]) + (c[2][i] + c[3][i]);
+            if (bad) c[0][i] = __uint_as_float(0x7fc00000u);
+            y[i] = level(i, evf - m[i & 1]);
+        }
+        // M moves only when a weight would pass 2^kTop (and on the first block, M = -inf)
+        const float ym = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+        if (__any_sync(0xffffffffu, ym > kTop)) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float top = fmaxf(level(j, evf), level(j + 2, evf));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                const float mn = fmaxf(m[j], ceilf(top) - (kTop - kRoom));
+                const float alpha = mn == m[j] ? 1.0f : ptx::ex2(m[j] - mn);
+                l[j] *= alpha;
+#pragma unroll
+                for (int i = 0; i < kUnits; ++i) {
+                    acc[i][j] *= alpha;
+                    acc[i][j + 2] *= alpha;
+                }
+                m[j] = mn;
+                y[j] = level(j, evf - mn);
+                y[j + 2] = level(j + 2, evf - mn);
+            }
+        }
+        uint32_t hi[2], lo[2];   // B fragments: column g, positions (2t, 2t + 1) of each half
+        const float unscale = pow2f(-ev);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float p0 = ptx::ex2(y[2 * i]), p1 = ptx::ex2(y[2 * i + 1]);
+            l[0] = fmaf(p0, unscale, l[0]);
+            l[1] = fmaf(p1, unscale, l[1]);
+            hi[i] = ptx::f16x2_pack(p0, p1);
+            const float2 h = ptx::f16x2_unpack(hi[i]);
+            lo[i] = ptx::f16x2_pack(p0 - h.x, p1 - h.y);
+            if (Pol::kSplitCols) {   // columns 2t, 2t + 1: the hi parts at even t, the lo parts at odd
+                hi[i] = ptx::movmatrix_trans((t & 1) ? lo[i] : hi[i]);
+            } else {
+                hi[i] = ptx::movmatrix_trans(hi[i]);
+                lo[i] = ptx::movmatrix_trans(lo[i]);
+            }
+        }
+        // rows outside the range hold anything: their codes are zeroed (0 * NaN)
+        uint32_t mask[2] = {0xffffffffu, 0xffffffffu};
+        if (!whole) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int pos = 8 * i + 2 * t;
+                mask[i] = ((pos >= first && pos < last) ? 0x0000ffffu : 0u) |
+                          ((pos + 1 >= first && pos + 1 < last) ? 0xffff0000u : 0u);
+                if (bad) mask[i] = 0u;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnits; u += 2) {
+            uint32_t w[4];   // positions 0-7, 8-15 of unit u, then of unit u + 1
+            ptx::ldmatrix_x4_trans(unit_addr(v_blk, r, u + (mat >> 1)), w[0], w[1], w[2], w[3]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t a = __byte_perm(w[2 * i] & mask[0], 0u, 0x3120);
+                const uint32_t b = __byte_perm(w[2 * i + 1] & mask[1], 0u, 0x3120);
+                const uint32_t a0 = ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(a));
+                const uint32_t a1 = ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(a >> 16));
+                const uint32_t a2 = ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(b));
+                const uint32_t a3 = ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(b >> 16));
+                float d[4];
+                if (Pol::kSplitCols) {
+                    ptx::mma_f16_16816_zero(d, a0, a1, a2, a3, hi[0], hi[1]);
+                } else {
+                    ptx::mma_f16_16816_zero(d, a0, a1, a2, a3, lo[0], lo[1]);
+                    ptx::mma_f16_16816(d, a0, a1, a2, a3, hi[0], hi[1]);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[u + i][j] += d[j];
+            }
+        }
+    }
+
+    // Merge of the 8 warps' states: the output (slot < 0; the piece is the whole segment) or
+    // the partial (acc, m, l) at workspace slot `slot`.  The M are whole numbers, so the
+    // factors 2^(M_w - M) are exact.  Called by all consumer warps, after a barrier that
+    // follows the stores of wm and wl.
+    __device__ __forceinline__ void merge(QuantSmem<Pol>& sm, const DecodeParams& p, size_t out_base,
+                                          int slot, int warp, int lane) {
+        const int g = lane >> 2, t = lane & 3, tid = warp * 32 + lane;
+        constexpr int kThreads = Pol::NC * 32;
+        constexpr int W = Pol::kMergeDims;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int h = 2 * t + j;
-            if (h < G) {
-                const float f = fk * q_factor[j];
-                S[part][h][pos] = (c[0][j] + c[1][j]) * f;
-                S[part][h][pos + 8] = (c[0][j + 2] + c[1][j + 2]) * f;
+            float top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < Pol::NC; ++w) top = fmaxf(top, sm.wm[w][2 * t + j]);
+            // (a warp without a finite score weighs 0; its NaN stay)
+            const float f = m[j] == -INFINITY ? 0.0f : ptx::ex2(m[j] - top);
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i) {
+                acc[i][j] *= f;
+                acc[i][j + 2] *= f;
             }
         }
-    }
-
-    // Online softmax over the tile (every warp alike), then P.V for this warp's dims.
-    __device__ __forceinline__ void softmax_pv(const float (*S)[G][Pol::kSStride], uint32_t v_tile,
-                                               const float* v_scales, const QuantTile& d, int warp,
-                                               int lane) {
-        const int g = lane >> 2, t = lane & 3;
-        // the head of column g; at kSplitCols columns G .. 2 G - 1 carry the lo parts
-        const bool real = g < (Pol::kSplitCols ? 2 * G : G);
-        const int head = Pol::kSplitCols ? g % G : (real ? g : 0);
-        const bool whole = d.vlo == 0 && d.vhi == TP && d.bad == 0;
-        float x[kBlocks][4];
-        int ev[kBlocks];
-        float top = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < kBlocks; ++j) {
-            ev[j] = scale_exponent(v_scales[j]);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int pos = j * kQuantBlock + 8 * i + 2 * t;
-                float2 s = *reinterpret_cast<const float2*>(&S[0][head][pos]);
-#pragma unroll
-                for (int q = 1; q < Pol::kParts; ++q) {
-                    const float2 y = *reinterpret_cast<const float2*>(&S[q][head][pos]);
-                    s.x += y.x;
-                    s.y += y.y;
-                }
-                if (!whole) {
-                    const float nan = __uint_as_float(0x7fc00000u);
-                    if ((d.bad >> j) & 1) s = make_float2(nan, nan);
-                    if (pos < d.vlo || pos >= d.vhi) s.x = -INFINITY;
-                    if (pos + 1 < d.vlo || pos + 1 >= d.vhi) s.y = -INFINITY;
-                }
-                x[j][2 * i] = s.x;
-                x[j][2 * i + 1] = s.y;
-                top = fmaxf(top, fmaf(fmaxf(s.x, s.y), kLog2e, static_cast<float>(ev[j])));
-            }
-        }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const float mn = fmaxf(m, ceilf(top) - 15.0f);
-        // (no finite score yet: any finite M)
-        const float mm = mn == -INFINITY ? 0.0f : mn;
-        if (__any_sync(0xffffffffu, mn != m)) {
-            const float alpha = ptx::ex2(m - mm);
-            const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * t);
-            const float a1 = __shfl_sync(0xffffffffu, alpha, 8 * t + 4);
-            l *= alpha;
-#pragma unroll
-            for (int i = 0; i < kDimTiles; ++i) {
-                acc[i][0] *= a0;
-                acc[i][1] *= a1;
-                acc[i][2] *= a0;
-                acc[i][3] *= a1;
-            }
-        }
-        m = mn;
-        uint32_t hi[kBlocks][2], lo[kBlocks][2];
-        float sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < kBlocks; ++j) {
-            const float shift = static_cast<float>(ev[j]) - mm;
-            float block_sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float p0 = ptx::ex2(fmaf(x[j][2 * i], kLog2e, shift));
-                float p1 = ptx::ex2(fmaf(x[j][2 * i + 1], kLog2e, shift));
-                if (!real) p0 = p1 = 0.0f;
-                block_sum += p0 + p1;
-                hi[j][i] = ptx::f16x2_pack(p0, p1);
-                const float2 h = ptx::f16x2_unpack(hi[j][i]);
-                lo[j][i] = ptx::f16x2_pack(p0 - h.x, p1 - h.y);
-                if (Pol::kSplitCols && g >= G) hi[j][i] = lo[j][i];
-            }
-            sum += block_sum * pow2f(-ev[j]);
-        }
-        l += sum;
-
-        const int mat = lane >> 3, r = (mat & 1) * 8 + (lane & 7);
-#pragma unroll
-        for (int j = 0; j < kBlocks; ++j) {
-            // rows outside the range hold anything: their codes are zeroed (0 * NaN)
-            uint32_t mask[2] = {0xffffffffu, 0xffffffffu};
-            if (!whole) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int pos = j * kQuantBlock + 8 * i + 2 * t;
-                    mask[i] = ((pos >= d.vlo && pos < d.vhi) ? 0x0000ffffu : 0u) |
-                              ((pos + 1 >= d.vlo && pos + 1 < d.vhi) ? 0xffff0000u : 0u);
-                    if ((d.bad >> j) & 1) mask[i] = 0u;
-                }
-            }
-#pragma unroll
-            for (int n = 0; n < kDimTiles; n += 2) {
-                uint32_t w[4];   // positions 0-7, 8-15 of dim tile n, then of n + 1
-                ptx::ldmatrix_x4_trans(unit_addr(v_tile, j, r, warp * kDimTiles + n + (mat >> 1)),
-                                       w[0], w[1], w[2], w[3]);
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const uint32_t a = __byte_perm(w[2 * q] & mask[0], 0u, 0x3120);
-                    const uint32_t b = __byte_perm(w[2 * q + 1] & mask[1], 0u, 0x3120);
-                    const uint32_t a0 = ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(a));
-                    const uint32_t a1 = ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(a >> 16));
-                    const uint32_t a2 = ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(b));
-                    const uint32_t a3 = ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(b >> 16));
-                    ptx::mma_f16_16816(acc[n + q], a0, a1, a2, a3, hi[j][0], hi[j][1]);
-                    if (!Pol::kSplitCols)
-                        ptx::mma_f16_16816(acc[n + q], a0, a1, a2, a3, lo[j][0], lo[j][1]);
-                }
-            }
-        }
-    }
-
-    // The piece's result: the output (slot < 0; the piece is the whole segment) or the partial
-    // (acc, m, l) at workspace slot `slot`.
-    __device__ __forceinline__ void store(const DecodeParams& p, size_t out_base, int slot, int warp,
-                                          int lane) {
-        const int g = lane >> 2, t = lane & 3;
-        float ls = l;
-        ls += __shfl_xor_sync(0xffffffffu, ls, 1);
-        ls += __shfl_xor_sync(0xffffffffu, ls, 2);
         if (Pol::kSplitCols) {
-            // columns G .. 2 G - 1 (the next t for G = 2) hold the lo parts' products
-            static_assert(!Pol::kSplitCols || G == 2, "lo columns are the next lane's");
 #pragma unroll
-            for (int i = 0; i < kDimTiles; ++i)
+            for (int i = 0; i < kUnits; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc[i][j] += __shfl_xor_sync(0xffffffffu, acc[i][j], 1);
         }
-        const float inv = 1.0f / ls;
-        const float inv0 = __shfl_sync(0xffffffffu, inv, 8 * t);
-        const float inv1 = __shfl_sync(0xffffffffu, inv, 8 * t + 4);
-        if (2 * t < G) {
+        // this thread's two outputs of each round: head h, dims d and d + 1 of the round
+        const int h = tid / (W / 2), d = 2 * (tid % (W / 2));
+        static_assert(G * W == 2 * kThreads, "two outputs per thread and round");
+        float top = -INFINITY, ls = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kDimTiles; ++i) {
-                const int dim = (warp * kDimTiles + i) * 16 + 2 * g;
+        for (int w = 0; w < Pol::NC; ++w) top = fmaxf(top, sm.wm[w][h]);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int at = (2 * t + j) * D + dim;
-                    if (slot < 0) {
-                        const float f = j ? inv1 : inv0;
-                        store_out2(p, out_base + at, acc[i][j] * f, acc[i][j + 2] * f);
-                    } else {
-                        *reinterpret_cast<float2*>(p.ws_acc + static_cast<size_t>(slot) * G * D + at) =
-                            make_float2(acc[i][j], acc[i][j + 2]);
-                    }
-                }
-            }
+        for (int w = 0; w < Pol::NC; ++w) {
+            const float mw = sm.wm[w][h];
+            ls += (mw == -INFINITY ? 0.0f : ptx::ex2(mw - top)) * sm.wl[w][h];
         }
-        if (slot >= 0 && warp == 0 && t == 0 && g < G) {
-            float* ml = p.ws_ml + (static_cast<size_t>(slot) * G + g) * 2;
-            ml[0] = m;
+        const float inv = 1.0f / ls;
+#pragma unroll
+        for (int r = 0; r < D / W; ++r) {
+            if (2 * t < G) {
+#pragma unroll
+                for (int i = 0; i < W / 16; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        *reinterpret_cast<float2*>(&sm.wacc[warp][2 * t + j][i * 16 + 2 * g]) =
+                            make_float2(acc[r * (W / 16) + i][j], acc[r * (W / 16) + i][j + 2]);
+            }
+            ptx::named_barrier_sync(1, kThreads);
+            float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int w = 0; w < Pol::NC; ++w) {
+                const float2 x = *reinterpret_cast<const float2*>(&sm.wacc[w][h][d]);
+                s.x += x.x;
+                s.y += x.y;
+            }
+            const size_t at = static_cast<size_t>(h) * D + r * W + d;
+            if (slot < 0)
+                store_out2(p, out_base + at, s.x * inv, s.y * inv);
+            else
+                *reinterpret_cast<float2*>(p.ws_acc + static_cast<size_t>(slot) * G * D + at) = s;
+            ptx::named_barrier_sync(1, kThreads);   // wacc is filled again
+        }
+        if (slot >= 0 && d == 0) {
+            float* ml = p.ws_ml + (static_cast<size_t>(slot) * G + h) * 2;
+            ml[0] = top;
             ml[1] = ls;
         }
     }
 };
 
 template <class Pol, bool kPaged>
-__global__ void __launch_bounds__((Pol::NC + 1) * 32, 1)
+__global__ void __launch_bounds__(kQuantThreads, 1)
     gqa_decode_quant_kernel(const __grid_constant__ CUtensorMap tm_k,
                             const __grid_constant__ CUtensorMap tm_v, const DecodeQuantParams qp) {
-    constexpr int G = Pol::G, D = Pol::D, TP = Pol::TP, STAGES = Pol::STAGES, NC = Pol::NC;
+    constexpr int G = Pol::G, D = Pol::D, TP = Pol::TP, SLOTS = Pol::SLOTS, NC = Pol::NC;
     constexpr int kBlocks = Pol::kBlocks;
     constexpr int kConsumerThreads = NC * 32;
     constexpr uint32_t kTileBytes = QuantSmem<Pol>::kTileBytes;
@@ -346,12 +383,12 @@ __global__ void __launch_bounds__((Pol::NC + 1) * 32, 1)
     PlanSmem& pl = sm.plan;
 
     if (tid == 0) {
-        for (int s = 0; s < STAGES; ++s) {
+        for (int s = 0; s < SLOTS; ++s) {
             ptx::mbar_init(ptx::smem_addr(&sm.full[s]), 2);   // the tiles' bytes, the scales
-            ptx::mbar_init(ptx::smem_addr(&sm.empty[s]), NC);
+            ptx::mbar_init(ptx::smem_addr(&sm.empty[s]), 1);
         }
-        ptx::mbar_init(ptx::smem_addr(&sm.q_empty[0]), NC);
-        ptx::mbar_init(ptx::smem_addr(&sm.q_empty[1]), NC);
+        ptx::mbar_init(ptx::smem_addr(&sm.q_full), 1);
+        ptx::mbar_init(ptx::smem_addr(&sm.q_empty), 1);
         ptx::mbar_init(ptx::smem_addr(&sm.stall_bar), 1);
         ptx::fence_mbar_init();
         sm.abort_flag = 0;
@@ -395,31 +432,39 @@ __global__ void __launch_bounds__((Pol::NC + 1) * 32, 1)
     if (!has_work) return;
 
     const uint32_t kv_base = ptx::smem_addr(&sm.kv[0][0][0]);
+    const uint32_t q_full = ptx::smem_addr(&sm.q_full), q_empty = ptx::smem_addr(&sm.q_empty);
 
-    if (warp == NC) {
+    if (warp >= NC) {
+        ptx::regs_dec<kQuantProducerRegs>();
+        if (warp > NC || lane != 0) return;
         // ================= producer: one thread walks the schedule =================
-        if (lane != 0) return;
         const uint64_t policy = ptx::policy_evict_first();
-        uint32_t t_idx = 0;
-        bool ok = true;
+        uint32_t t_idx = 0;   // slots filled
+        uint32_t q_n = 0;     // pieces published
         const bool dynamic = pl.n_dyn > 0;
         int claimed = -1;
-        uint32_t q_n = 0;
         constexpr uint32_t kQBytes = G * D * 2;
 
         auto emit_piece = [&](const Piece& pc) -> bool {
-            const uint32_t qb = q_n & 1u;
-            if (!wait_bounded(ptx::smem_addr(&sm.q_empty[qb]), ((q_n >> 1) & 1u) ^ 1u,
-                              &sm.abort_flag, p.ws_flags))
-                return false;
+            // q and the piece's description: free once the consumers began the piece before
+            if (!wait_bounded(q_empty, (q_n & 1u) ^ 1u, &sm.abort_flag, p.ws_flags)) return false;
             ++q_n;
             const int b = pc.b, kvh = pc.kvh, L = sm.len[b];
-            const int first_pos = p.window > 0 && L > p.window ? L - p.window : 0;
+            sm.piece.b = b;
+            sm.piece.kvh = kvh;
+            sm.piece.p0 = pc.p0;
+            sm.piece.p1 = pc.p1;
+            sm.piece.lo = p.window > 0 && L > p.window ? L - p.window : 0;
+            sm.piece.hi = L;
+            sm.piece.slot = pc.slot;
+            sm.piece.done = 0;
+            ptx::mbar_arrive_expect_tx(q_full, kQBytes);
+            ptx::bulk_copy_g2s(ptx::smem_addr(&sm.q[0]),
+                               p.q + (static_cast<size_t>(b) * H + kvh * G) * D, kQBytes, q_full);
             const int chunk0 = kvh * (D / 128);
             const int32_t* bt_row =
                 kPaged ? p.block_table + static_cast<size_t>(b) * p.max_pages : nullptr;
             for (int t = pc.p0; t < pc.p1; t += TP) {
-                const bool first = t == pc.p0, last = t + TP >= pc.p1;
                 const int nbox = min(pc.p1 - t, TP) / kQuantBlock;
                 int page[kBlocks], bad = 0;
                 if (kPaged) {
@@ -433,28 +478,18 @@ __global__ void __launch_bounds__((Pol::NC + 1) * 32, 1)
                             bad |= 1 << j;
                         }
                 }
-                if (dynamic && pc.unit_end && last)
+                if (dynamic && pc.unit_end && t + TP >= pc.p1)
                     claimed = static_cast<int>(atomicAdd(p.ws_claim, 1u));
-                const int s = t_idx % STAGES;
-                const uint32_t ph = (t_idx / STAGES) & 1u;
+                const int s = t_idx % SLOTS;
+                const uint32_t ph = (t_idx / SLOTS) & 1u;
                 if (!wait_bounded(ptx::smem_addr(&sm.empty[s]), ph ^ 1u, &sm.abort_flag, p.ws_flags))
                     return false;
-                QuantTile& d = sm.tile[s];
-                d.b = b;
-                d.kvh = kvh;
-                d.vlo = max(first_pos - t, 0);
-                d.vhi = min(min(L, pc.p1) - t, TP);
-                d.slot = pc.slot;
-                d.bad = bad;
-                d.flags = (first ? kDescFirst : 0) | (last ? kDescLast : 0);
-                if (bad) atomicOr(p.ws_flags, kFlagBadPage);
+                if (kPaged) {
+                    sm.bad[s] = bad;
+                    if (bad) atomicOr(p.ws_flags, kFlagBadPage);
+                }
                 const uint32_t full_bar = ptx::smem_addr(&sm.full[s]);
-                ptx::mbar_arrive_expect_tx(full_bar, static_cast<uint32_t>(nbox) * 2 * kBoxBytes +
-                                                         (first ? kQBytes : 0u));
-                if (first)
-                    ptx::bulk_copy_g2s(ptx::smem_addr(&sm.q[qb][0]),
-                                       p.q + (static_cast<size_t>(b) * H + kvh * G) * D, kQBytes,
-                                       full_bar);
+                ptx::mbar_arrive_expect_tx(full_bar, static_cast<uint32_t>(nbox) * 2 * kBoxBytes);
                 const uint32_t k_dst = kv_base + s * 2 * kTileBytes;
                 const uint32_t v_dst = k_dst + kTileBytes;
                 const uint32_t sc_dst = ptx::smem_addr(&sm.scales[s][0][0]);
@@ -483,21 +518,20 @@ __global__ void __launch_bounds__((Pol::NC + 1) * 32, 1)
 
         long long x = static_unit_begin(pl, cta);
         const long long stop = static_unit_begin(pl, cta + 1);
+        bool ok = true;
         Piece pc;
         while (ok && next_piece(pl, p, cta, TP, dynamic, x, stop, claimed, pc)) ok = emit_piece(pc);
         if (ok) {
-            const int s = t_idx % STAGES;
-            const uint32_t ph = (t_idx / STAGES) & 1u;
-            if (wait_bounded(ptx::smem_addr(&sm.empty[s]), ph ^ 1u, &sm.abort_flag, p.ws_flags)) {
-                sm.tile[s].flags = kDescDone;
-                ptx::mbar_arrive(ptx::smem_addr(&sm.full[s]));
-                ptx::mbar_arrive(ptx::smem_addr(&sm.full[s]));
+            if (wait_bounded(q_empty, (q_n & 1u) ^ 1u, &sm.abort_flag, p.ws_flags)) {
+                sm.piece.done = 1;
+                ptx::mbar_arrive(q_full);
             }
         } else {
             // let every copy already issued land before the CTA exits
-            const uint32_t first = t_idx > static_cast<uint32_t>(STAGES) ? t_idx - STAGES : 0u;
+            const uint32_t first = t_idx > static_cast<uint32_t>(SLOTS) ? t_idx - SLOTS : 0u;
             for (uint32_t tt = first; tt < t_idx; ++tt)
-                wait_drain(ptx::smem_addr(&sm.full[tt % STAGES]), (tt / STAGES) & 1u);
+                wait_drain(ptx::smem_addr(&sm.full[tt % SLOTS]), (tt / SLOTS) & 1u);
+            if (q_n > 0) wait_drain(q_full, (q_n - 1u) & 1u);
         }
         if (Pol::kMergeInKernel && dynamic) {
             if (ptx::atom_add_acq_rel_gpu(p.ws_done, 1u) == static_cast<uint32_t>(pl.g_eff - 1)) {
@@ -508,51 +542,71 @@ __global__ void __launch_bounds__((Pol::NC + 1) * 32, 1)
         return;
     }
 
-    // ===================== consumers: follow the tiles =====================
+    // ===================== consumers =====================
+    ptx::regs_inc<kQuantConsumerRegs>();
+    // Every warp passes the same barriers for every piece, whatever its waits return; a warp
+    // whose wait gave up (or which saw the end) makes all of them leave at the next one.
     QuantConsumer<Pol> c;
-    uint32_t q_n = 0;
-    for (uint32_t t_idx = 0;; ++t_idx) {
-        const int s = t_idx % STAGES;
-        const uint32_t ph = (t_idx / STAGES) & 1u;
-        // (one decision per warp: the tile's work is warp-wide)
-        const bool ok = __all_sync(0xffffffffu, wait_bounded(ptx::smem_addr(&sm.full[s]), ph,
-                                                             &sm.abort_flag, p.ws_flags));
-        QuantTile d;
-        d.flags = kDescDone;
-        if (ok) d = sm.tile[s];
-        const uint32_t k_tile = kv_base + s * 2 * kTileBytes;
-        float(*S)[G][Pol::kSStride] = sm.S[t_idx & 1];
-        if (!(d.flags & kDescDone)) {
-            if (d.flags & kDescFirst) {
-                // q arrived with this tile; release the buffer once every lane has read it
-                const uint32_t qb = q_n & 1u;
-                c.begin(&sm.q[qb][0], warp, lane);
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&sm.q_empty[qb]));
-                ++q_n;
-            }
-            c.scores(k_tile, sm.scales[s][0], S, warp, lane);
-        }
-        // the scores of every warp are there; and all take the same exit decision (the end, or
-        // a wait that gave up)
-        if (ptx::named_barrier_or(1, kConsumerThreads, (d.flags & kDescDone) != 0)) break;
-        c.softmax_pv(S, k_tile + kTileBytes, sm.scales[s][1], d, warp, lane);
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&sm.empty[s]));
-        if (!(d.flags & kDescLast)) continue;
+    const uint32_t q_frag = ptx::smem_addr(&sm.q_frag[0][0]);
+    uint32_t t0 = 0;   // slots of the pieces before
+    for (uint32_t n = 0;; ++n) {
+        const bool there = __all_sync(0xffffffffu, wait_bounded(q_full, n & 1u, &sm.abort_flag, p.ws_flags));
+        QuantPiece pc;
+        pc.done = 1;
+        if (there) pc = sm.piece;
+        if (!pc.done) c.begin(&sm.q[0], sm.q_frag, warp, lane);
+        if (ptx::named_barrier_or(1, kConsumerThreads, pc.done != 0)) break;
+        if (tid == 0) ptx::mbar_arrive(q_empty);   // every warp has read q and the piece
 
-        const SegmentParts sp(pl, d.b, d.kvh, p.dyn_slot_base);
+        const uint32_t slots = static_cast<uint32_t>((pc.p1 - pc.p0 + TP - 1) / TP);
+        bool gone = false;
+        // the slots of the whole call go round the warps, so that short pieces follow one
+        // another on different warps
+        for (uint32_t t_idx = t0 + ((static_cast<uint32_t>(warp) - t0) & (NC - 1)); t_idx < t0 + slots; t_idx += NC) {
+            const int s = t_idx % SLOTS;
+            const uint32_t ph = (t_idx / SLOTS) & 1u;
+            gone = !__all_sync(0xffffffffu, wait_bounded(ptx::smem_addr(&sm.full[s]), ph, &sm.abort_flag, p.ws_flags));
+            if (gone) break;
+            const int pos = pc.p0 + static_cast<int>(t_idx - t0) * TP;
+            const uint32_t k_tile = kv_base + s * 2 * kTileBytes;
+            const int bad = kPaged ? sm.bad[s] : 0;
+#pragma unroll 1
+            for (int j = 0; j < kBlocks; ++j) {
+                if (pos + j * kQuantBlock >= pc.p1) break;
+                c.block(k_tile + j * kBoxBytes, k_tile + kTileBytes + j * kBoxBytes,
+                        sm.scales[s][0][j], sm.scales[s][1][j], pc.lo - pos - j * kQuantBlock,
+                        pc.hi - pos - j * kQuantBlock, (bad >> j) & 1, q_frag, lane);
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&sm.empty[s]));
+        }
+        t0 += slots;
+
+        // normalisers of this warp's columns
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            float ls = c.l[j];
+            ls += __shfl_xor_sync(0xffffffffu, ls, 4);
+            ls += __shfl_xor_sync(0xffffffffu, ls, 8);
+            ls += __shfl_xor_sync(0xffffffffu, ls, 16);
+            if (lane < 4) {
+                sm.wm[warp][2 * lane + j] = c.m[j];
+                sm.wl[warp][2 * lane + j] = ls;
+            }
+        }
+        if (ptx::named_barrier_or(1, kConsumerThreads, gone)) break;
+        const SegmentParts sp(pl, pc.b, pc.kvh, p.dyn_slot_base);
         const int nparts = sp.count();
-        const size_t out_base = (static_cast<size_t>(d.b) * H + d.kvh * G) * D;
-        c.store(p, out_base, nparts == 1 ? -1 : d.slot, warp, lane);
+        const size_t out_base = (static_cast<size_t>(pc.b) * H + pc.kvh * G) * D;
+        c.merge(sm, p, out_base, nparts == 1 ? -1 : pc.slot, warp, lane);
         if constexpr (Pol::kMergeInKernel)
             if (nparts > 1)
-                count_and_merge<G, D, kConsumerThreads>(p, sp, d.b * KVH + d.kvh, out_base, tid,
+                count_and_merge<G, D, kConsumerThreads>(p, sp, pc.b * KVH + pc.kvh, out_base, tid,
                                                         &sm.merge_last);
     }
 }
 
-using QuantSliding = QuantPolicy<2, 256, 128, 3, true>;    // slidingDecodeGQA
-using QuantGlobal = QuantPolicy<8, 512, 64, 3, false>;     // decodeGQA
+using QuantSliding = QuantPolicy<2, 256, 2, 12, true>;    // slidingDecodeGQA
+using QuantGlobal = QuantPolicy<8, 512, 1, 11, false>;     // decodeGQA
 
 }  // namespace gqa
