@@ -32,9 +32,11 @@
 // instructions per warp and 128 positions at g = 2 against ~300 here.)
 //
 // Work split, timeouts and merging between CTAs are those of decode_kernel.cuh: a
-// persistent CTA per SM, a plan built from seq_lens on the device, one producer thread that
-// streams K and V with TMA through a ring of 16 KB slots, which the 8 consumer warps take in
-// turn.  Pieces start and end on blocks.
+// persistent CTA per SM, a plan built from seq_lens on the device.  Pieces start and end on
+// blocks.  One thread walks the schedule and publishes pieces; three threads stream K and V
+// with TMA, one slot per block; block i of a piece goes to consumer warp i % NC, into that
+// warp's own ring of slots.  (A ring shared by the warps would let a warp wait on a slot's
+// barrier two fills ahead of its last completion, which a parity cannot tell apart.)
 #pragma once
 
 #include "decode_kernel.cuh"
@@ -49,28 +51,16 @@ struct DecodeQuantParams {
     int blocks;              // blocks per sequence (contiguous)
 };
 
-// Registers: 12 warps (three warpgroups, the last one's first thread the producer) start
-// with 168 each; the producer's warpgroup gives up what the consumers' two take.
-constexpr int kQuantThreads = 384;
-constexpr int kQuantLaunchRegs = 168;
-constexpr int kQuantConsumerRegs = 224;
-constexpr int kQuantProducerRegs = 56;
-static_assert(2 * kQuantConsumerRegs + kQuantProducerRegs <= 3 * kQuantLaunchRegs, "register split");
-
-template <int kG, int kD, int kBlocksPerSlot, int kSlots, bool kMerge>
+template <int kG, int kD, int kWarps, int kRing, bool kMerge>
 struct QuantPolicy {
-    static constexpr int G = kG, D = kD, NC = 8;
-    static constexpr int kBlocks = kBlocksPerSlot;       // blocks of 16 positions per slot
-    static constexpr int TP = kBlocks * kQuantBlock;     // positions per slot
-    static constexpr int SLOTS = kSlots;
+    static constexpr int G = kG, D = kD, NC = kWarps, RING = kRing;
+    static constexpr int SLOTS = NC * RING;              // one block of K and V each
     static constexpr bool kMergeInKernel = kMerge;
+    static constexpr int kThreads = (NC + 4) * 32;       // consumers, scheduler, three loaders
     static constexpr int kUnits = D / 16;                // 16-dim steps
     static constexpr bool kSplitCols = G == 2;           // hi and lo parts of P in one mma
-    // q's B fragments: in registers (G = 2: 32), or in shared memory where the D x 8
-    // accumulators (128 registers) leave no room
-    static constexpr bool kQInSmem = D > 256;
     static constexpr int kMergeDims = G == 2 ? 256 : 64;   // dims merged per round
-    static constexpr int kMergeStride = kMergeDims + 4;    // conflict-free float2 stores
+    static constexpr int kMergeStride = kMergeDims + 4;  // conflict-free float2 stores
     static_assert((G == 2 || G == 8) && kUnits % 4 == 0 && D % kMergeDims == 0, "shape");
 };
 
@@ -85,19 +75,19 @@ struct QuantPiece {
 
 template <class Pol>
 struct alignas(1024) QuantSmem {
-    static constexpr int kTileBytes = Pol::TP * Pol::D;
-    uint8_t kv[Pol::SLOTS][2][kTileBytes];   // [slot][K, V][block][chunk][16 rows][128 B]
+    static constexpr int kTileBytes = kQuantBlock * Pol::D;
+    uint8_t kv[Pol::SLOTS][2][kTileBytes];   // [slot][K, V][chunk][16 rows][128 B]
     alignas(8) uint64_t full[Pol::SLOTS];
     alignas(8) uint64_t empty[Pol::SLOTS];
     alignas(8) uint64_t q_full, q_empty;
     alignas(8) uint64_t stall_bar;           // kTestStall: a barrier nothing completes
-    float scales[Pol::SLOTS][2][Pol::kBlocks];
-    int bad[Pol::SLOTS];                     // blocks whose page id is out of range, one bit each
+    float scales[Pol::SLOTS][2];
+    int bad[Pol::SLOTS];                     // the block's page id is out of range
     QuantPiece piece;
     PlanSmem plan;
     int len[kMaxBatch];                      // clamped lengths
     alignas(128) __nv_bfloat16 q[Pol::G * Pol::D];
-    alignas(16) uint2 q_frag[Pol::kQInSmem ? Pol::kUnits : 1][32];
+    alignas(16) uint2 q_frag[Pol::kUnits][32];   // B fragments of q (column g = head g % G)
     float wm[Pol::NC][8], wl[Pol::NC][8];    // each warp's M and l per column
     alignas(16) float wacc[Pol::NC][Pol::G][Pol::kMergeStride];
     int abort_flag;
@@ -110,7 +100,6 @@ struct QuantConsumer {
     static constexpr float kTop = 15.0f;    // largest exponent of a weight (f16 ends at 2^16)
     static constexpr float kRoom = 3.0f;    // binades left above the maximum when M is set
 
-    uint2 qb[Pol::kQInSmem ? 1 : kUnits];   // B fragments of q (column g = head g % G)
     float q_factor[2];           // undo q's scaling for columns 2t and 2t + 1, times log2(e)
     float acc[kUnits][4];        // rows: dims 2g (0, 1) and 2g + 1 (2, 3); columns 2t, 2t + 1
     float m[2];                  // M of columns 2t, 2t + 1
@@ -121,8 +110,8 @@ struct QuantConsumer {
         return block + (unit >> 3) * 2048 + r * 128 + (((unit & 7) ^ (r & 7)) << 4);
     }
 
-    // q_heads: [G][D] bf16 in shared memory.  With q in shared memory each warp makes its
-    // share of the fragments (a barrier follows).
+    // q_heads: [G][D] bf16 in shared memory.  Each warp makes its share of the fragments (a
+    // barrier follows).
     __device__ __forceinline__ void begin(const __nv_bfloat16* q_heads, uint2 (*frag)[32], int warp,
                                           int lane) {
         const int g = lane >> 2, t = lane & 3;
@@ -138,20 +127,12 @@ struct QuantConsumer {
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int e = max(static_cast<int>(top >> 7) - 127, -100);   // |q| < 2^(e + 1)
         const float f = pow2f(14 - e);
-        auto widen = [&](int u) {
+#pragma unroll
+        for (int i = 0; i < kUnits / Pol::NC; ++i) {
+            const int u = warp * (kUnits / Pol::NC) + i;
             const uint2 w = *reinterpret_cast<const uint2*>(row + u * 16);
-            return make_uint2(ptx::f16x2_pack(bf16lo(w.x) * f, bf16hi(w.x) * f),
-                              ptx::f16x2_pack(bf16lo(w.y) * f, bf16hi(w.y) * f));
-        };
-        if constexpr (Pol::kQInSmem) {
-#pragma unroll
-            for (int i = 0; i < kUnits / Pol::NC; ++i) {
-                const int u = warp * (kUnits / Pol::NC) + i;
-                frag[u][lane] = widen(u);
-            }
-        } else {
-#pragma unroll
-            for (int u = 0; u < kUnits; ++u) qb[u] = widen(u);
+            frag[u][lane] = make_uint2(ptx::f16x2_pack(bf16lo(w.x) * f, bf16hi(w.x) * f),
+                                       ptx::f16x2_pack(bf16lo(w.y) * f, bf16hi(w.y) * f));
         }
         const float undo = pow2f(e - 14) * kLog2e;
         q_factor[0] = __shfl_sync(0xffffffffu, undo, 8 * t);
@@ -183,12 +164,11 @@ struct QuantConsumer {
             ptx::ldmatrix_x4(unit_addr(k_blk, r, u + (mat >> 1)), a[0], a[1], a[2], a[3]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const uint2 q = Pol::kQInSmem ? ptx::lds64(q_frag + (u + i) * 256 + lane * 8) : qb[Pol::kQInSmem ? 0 : u + i];
-                const uint32_t lo = a[2 * i], hi = a[2 * i + 1];
-                ptx::mma_f16_16816(c[(u + i) & 3], ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(lo)),
-                                   ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(hi)),
-                                   ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(lo >> 16)),
-                                   ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(hi >> 16)), q.x, q.y);
+                const uint2 q = ptx::lds64(q_frag + (u + i) * 256 + lane * 8);
+                uint32_t a0, a1, a2, a3;
+                ptx::e4m3x4_to_f16x2(a[2 * i], a0, a2);
+                ptx::e4m3x4_to_f16x2(a[2 * i + 1], a1, a3);
+                ptx::mma_f16_16816(c[(u + i) & 3], a0, a1, a2, a3, q.x, q.y);
             }
         }
         // log2 of the weights: y = log2(e) score + ev - M, rows g (0, 1) and g + 8 (2, 3)
@@ -269,12 +249,9 @@ struct QuantConsumer {
             ptx::ldmatrix_x4_trans(unit_addr(v_blk, r, u + (mat >> 1)), w[0], w[1], w[2], w[3]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const uint32_t a = __byte_perm(w[2 * i] & mask[0], 0u, 0x3120);
-                const uint32_t b = __byte_perm(w[2 * i + 1] & mask[1], 0u, 0x3120);
-                const uint32_t a0 = ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(a));
-                const uint32_t a1 = ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(a >> 16));
-                const uint32_t a2 = ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(b));
-                const uint32_t a3 = ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(b >> 16));
+                uint32_t a0, a1, a2, a3;
+                ptx::e4m3x4_to_f16x2(__byte_perm(w[2 * i] & mask[0], 0u, 0x3120), a0, a1);
+                ptx::e4m3x4_to_f16x2(__byte_perm(w[2 * i + 1] & mask[1], 0u, 0x3120), a2, a3);
                 float d[4];
                 if (Pol::kSplitCols) {
                     ptx::mma_f16_16816_zero(d, a0, a1, a2, a3, hi[0], hi[1]);
@@ -288,7 +265,7 @@ struct QuantConsumer {
         }
     }
 
-    // Merge of the 8 warps' states: the output (slot < 0; the piece is the whole segment) or
+    // Merge of the warps' states: the output (slot < 0; the piece is the whole segment) or
     // the partial (acc, m, l) at workspace slot `slot`.  The M are whole numbers, so the
     // factors 2^(M_w - M) are exact.  Called by all consumer warps, after a barrier that
     // follows the stores of wm and wl.
@@ -297,6 +274,9 @@ struct QuantConsumer {
         const int g = lane >> 2, t = lane & 3, tid = warp * 32 + lane;
         constexpr int kThreads = Pol::NC * 32;
         constexpr int W = Pol::kMergeDims;
+        // a round merges G heads x W dims; a thread takes two dims of every kHeadStep-th head
+        constexpr int kHeadStep = kThreads / (W / 2) < G ? kThreads / (W / 2) : G;
+        static_assert(kHeadStep * (W / 2) == kThreads && G % kHeadStep == 0, "two dims per thread");
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             float top = -INFINITY;
@@ -316,18 +296,20 @@ struct QuantConsumer {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc[i][j] += __shfl_xor_sync(0xffffffffu, acc[i][j], 1);
         }
-        // this thread's two outputs of each round: head h, dims d and d + 1 of the round
-        const int h = tid / (W / 2), d = 2 * (tid % (W / 2));
-        static_assert(G * W == 2 * kThreads, "two outputs per thread and round");
-        float top = -INFINITY, ls = 0.0f;
+        float top[G / kHeadStep], ls[G / kHeadStep];   // of this thread's heads
 #pragma unroll
-        for (int w = 0; w < Pol::NC; ++w) top = fmaxf(top, sm.wm[w][h]);
+        for (int k = 0; k < G / kHeadStep; ++k) {
+            const int h = k * kHeadStep + tid / (W / 2);
+            top[k] = -INFINITY;
+            ls[k] = 0.0f;
 #pragma unroll
-        for (int w = 0; w < Pol::NC; ++w) {
-            const float mw = sm.wm[w][h];
-            ls += (mw == -INFINITY ? 0.0f : ptx::ex2(mw - top)) * sm.wl[w][h];
+            for (int w = 0; w < Pol::NC; ++w) top[k] = fmaxf(top[k], sm.wm[w][h]);
+#pragma unroll
+            for (int w = 0; w < Pol::NC; ++w) {
+                const float mw = sm.wm[w][h];
+                ls[k] += (mw == -INFINITY ? 0.0f : ptx::ex2(mw - top[k])) * sm.wl[w][h];
+            }
         }
-        const float inv = 1.0f / ls;
 #pragma unroll
         for (int r = 0; r < D / W; ++r) {
             if (2 * t < G) {
@@ -339,37 +321,43 @@ struct QuantConsumer {
                             make_float2(acc[r * (W / 16) + i][j], acc[r * (W / 16) + i][j + 2]);
             }
             ptx::named_barrier_sync(1, kThreads);
-            float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int w = 0; w < Pol::NC; ++w) {
-                const float2 x = *reinterpret_cast<const float2*>(&sm.wacc[w][h][d]);
-                s.x += x.x;
-                s.y += x.y;
+            for (int k = 0; k < G / kHeadStep; ++k) {
+                const int h = k * kHeadStep + tid / (W / 2), d = 2 * (tid % (W / 2));
+                float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int w = 0; w < Pol::NC; ++w) {
+                    const float2 x = *reinterpret_cast<const float2*>(&sm.wacc[w][h][d]);
+                    s.x += x.x;
+                    s.y += x.y;
+                }
+                const size_t at = static_cast<size_t>(h) * D + r * W + d;
+                if (slot < 0) {
+                    const float inv = 1.0f / ls[k];
+                    store_out2(p, out_base + at, s.x * inv, s.y * inv);
+                } else {
+                    *reinterpret_cast<float2*>(p.ws_acc + static_cast<size_t>(slot) * G * D + at) = s;
+                    if (r == 0 && d == 0) {
+                        float* ml = p.ws_ml + (static_cast<size_t>(slot) * G + h) * 2;
+                        ml[0] = top[k];
+                        ml[1] = ls[k];
+                    }
+                }
             }
-            const size_t at = static_cast<size_t>(h) * D + r * W + d;
-            if (slot < 0)
-                store_out2(p, out_base + at, s.x * inv, s.y * inv);
-            else
-                *reinterpret_cast<float2*>(p.ws_acc + static_cast<size_t>(slot) * G * D + at) = s;
             ptx::named_barrier_sync(1, kThreads);   // wacc is filled again
-        }
-        if (slot >= 0 && d == 0) {
-            float* ml = p.ws_ml + (static_cast<size_t>(slot) * G + h) * 2;
-            ml[0] = top;
-            ml[1] = ls;
         }
     }
 };
 
 template <class Pol, bool kPaged>
-__global__ void __launch_bounds__(kQuantThreads, 1)
+__global__ void __launch_bounds__(Pol::kThreads, 1)
     gqa_decode_quant_kernel(const __grid_constant__ CUtensorMap tm_k,
                             const __grid_constant__ CUtensorMap tm_v, const DecodeQuantParams qp) {
-    constexpr int G = Pol::G, D = Pol::D, TP = Pol::TP, SLOTS = Pol::SLOTS, NC = Pol::NC;
-    constexpr int kBlocks = Pol::kBlocks;
+    constexpr int G = Pol::G, D = Pol::D, SLOTS = Pol::SLOTS, NC = Pol::NC, RING = Pol::RING;
+    constexpr int kLoaders = 3;
+    constexpr int kLoads = (NC + kLoaders - 1) / kLoaders;   // consumer warps a loader serves
     constexpr int kConsumerThreads = NC * 32;
     constexpr uint32_t kTileBytes = QuantSmem<Pol>::kTileBytes;
-    constexpr uint32_t kBoxBytes = kQuantBlock * D;   // one block of one KV head
     const DecodeParams& p = qp.d;
 
     extern __shared__ uint8_t smem_raw[];
@@ -388,7 +376,7 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
             ptx::mbar_init(ptx::smem_addr(&sm.empty[s]), 1);
         }
         ptx::mbar_init(ptx::smem_addr(&sm.q_full), 1);
-        ptx::mbar_init(ptx::smem_addr(&sm.q_empty), 1);
+        ptx::mbar_init(ptx::smem_addr(&sm.q_empty), 1 + kLoaders);   // consumers, loaders
         ptx::mbar_init(ptx::smem_addr(&sm.stall_bar), 1);
         ptx::fence_mbar_init();
         sm.abort_flag = 0;
@@ -403,7 +391,7 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
     // (the plan's barriers make the lengths visible)
     for (int b = tid; b < B; b += blockDim.x)
         sm.len[b] = min(max(__ldg(p.seq_lens + b), 0), p.capacity);
-    build_plan<kQuantBlock>(pl, p, gridDim.x, warp, lane, cta, TP,
+    build_plan<kQuantBlock>(pl, p, gridDim.x, warp, lane, cta, kQuantBlock,
                             reinterpret_cast<uint32_t*>(&sm.kv[0][0][0]));
 
     // zeros for empty sequences and the segments' partial lists, as in decode_kernel.cuh
@@ -435,120 +423,133 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
     const uint32_t q_full = ptx::smem_addr(&sm.q_full), q_empty = ptx::smem_addr(&sm.q_empty);
 
     if (warp >= NC) {
-        ptx::regs_dec<kQuantProducerRegs>();
-        if (warp > NC || lane != 0) return;
-        // ================= producer: one thread walks the schedule =================
-        const uint64_t policy = ptx::policy_evict_first();
-        uint32_t t_idx = 0;   // slots filled
-        uint32_t q_n = 0;     // pieces published
-        const bool dynamic = pl.n_dyn > 0;
-        int claimed = -1;
-        constexpr uint32_t kQBytes = G * D * 2;
-
-        auto emit_piece = [&](const Piece& pc) -> bool {
-            // q and the piece's description: free once the consumers began the piece before
-            if (!wait_bounded(q_empty, (q_n & 1u) ^ 1u, &sm.abort_flag, p.ws_flags)) return false;
-            ++q_n;
-            const int b = pc.b, kvh = pc.kvh, L = sm.len[b];
-            sm.piece.b = b;
-            sm.piece.kvh = kvh;
-            sm.piece.p0 = pc.p0;
-            sm.piece.p1 = pc.p1;
-            sm.piece.lo = p.window > 0 && L > p.window ? L - p.window : 0;
-            sm.piece.hi = L;
-            sm.piece.slot = pc.slot;
-            sm.piece.done = 0;
-            ptx::mbar_arrive_expect_tx(q_full, kQBytes);
-            ptx::bulk_copy_g2s(ptx::smem_addr(&sm.q[0]),
-                               p.q + (static_cast<size_t>(b) * H + kvh * G) * D, kQBytes, q_full);
-            const int chunk0 = kvh * (D / 128);
-            const int32_t* bt_row =
-                kPaged ? p.block_table + static_cast<size_t>(b) * p.max_pages : nullptr;
-            for (int t = pc.p0; t < pc.p1; t += TP) {
-                const int nbox = min(pc.p1 - t, TP) / kQuantBlock;
-                int page[kBlocks], bad = 0;
-                if (kPaged) {
-#pragma unroll
-                    for (int j = 0; j < kBlocks; ++j)
-                        page[j] = j < nbox ? __ldg(bt_row + t / kQuantBlock + j) : 0;
-#pragma unroll
-                    for (int j = 0; j < kBlocks; ++j)
-                        if (page[j] < 0 || page[j] >= p.num_pages) {
-                            page[j] = 0;   // (loaded, and masked by the consumers)
-                            bad |= 1 << j;
-                        }
+        if (lane != 0) return;
+        if (warp == NC) {
+            // ======== scheduler: one thread walks the schedule, publishes pieces and q ========
+            const bool dynamic = pl.n_dyn > 0;
+            constexpr uint32_t kQBytes = G * D * 2;
+            long long x = static_unit_begin(pl, cta);
+            const long long stop = static_unit_begin(pl, cta + 1);
+            uint32_t n = 0;   // pieces published
+            bool ended = false;
+            // the description and q are free once the consumers began the piece before and
+            // the loaders have read it
+            while (wait_bounded(q_empty, (n & 1u) ^ 1u, &sm.abort_flag, p.ws_flags)) {
+                int claimed = -1;
+                Piece pc;
+                if (!next_piece(pl, p, cta, kQuantBlock, dynamic, x, stop, claimed, pc)) {
+                    sm.piece.done = 1;
+                    ptx::mbar_arrive(q_full);
+                    ended = true;
+                    break;
                 }
-                if (dynamic && pc.unit_end && t + TP >= pc.p1)
-                    claimed = static_cast<int>(atomicAdd(p.ws_claim, 1u));
-                const int s = t_idx % SLOTS;
-                const uint32_t ph = (t_idx / SLOTS) & 1u;
-                if (!wait_bounded(ptx::smem_addr(&sm.empty[s]), ph ^ 1u, &sm.abort_flag, p.ws_flags))
-                    return false;
-                if (kPaged) {
-                    sm.bad[s] = bad;
-                    if (bad) atomicOr(p.ws_flags, kFlagBadPage);
-                }
-                const uint32_t full_bar = ptx::smem_addr(&sm.full[s]);
-                ptx::mbar_arrive_expect_tx(full_bar, static_cast<uint32_t>(nbox) * 2 * kBoxBytes);
-                const uint32_t k_dst = kv_base + s * 2 * kTileBytes;
-                const uint32_t v_dst = k_dst + kTileBytes;
-                const uint32_t sc_dst = ptx::smem_addr(&sm.scales[s][0][0]);
-#pragma unroll
-                for (int j = 0; j < kBlocks; ++j) {
-                    if (j >= nbox) break;
-                    const int row = kPaged ? 0 : t + j * kQuantBlock;
-                    const int outer = kPaged ? page[j] : b;
-                    ptx::tma_load_4d(k_dst + j * kBoxBytes, &tm_k, full_bar, 0, row, chunk0, outer, policy);
-                    ptx::tma_load_4d(v_dst + j * kBoxBytes, &tm_v, full_bar, 0, row, chunk0, outer, policy);
-                    const size_t at =
-                        (kPaged ? static_cast<size_t>(page[j])
-                                : static_cast<size_t>(b) * qp.blocks + t / kQuantBlock + j) * KVH + kvh;
-                    ptx::cp_async4(sc_dst + j * 4, qp.k_scales + at);
-                    ptx::cp_async4(sc_dst + (kBlocks + j) * 4, qp.v_scales + at);
-                }
-                ptx::cp_async_mbar_arrive(full_bar);
-                ++t_idx;
-                if ((p.test_flags & kTestStall) && t_idx == 1 &&
-                    !wait_bounded(ptx::smem_addr(&sm.stall_bar), 0u, &sm.abort_flag, p.ws_flags,
-                                  kTestStallNs))
-                    return false;
+                ++n;
+                const int L = sm.len[pc.b];
+                sm.piece.b = pc.b;
+                sm.piece.kvh = pc.kvh;
+                sm.piece.p0 = pc.p0;
+                sm.piece.p1 = pc.p1;
+                sm.piece.lo = p.window > 0 && L > p.window ? L - p.window : 0;
+                sm.piece.hi = L;
+                sm.piece.slot = pc.slot;
+                sm.piece.done = 0;
+                ptx::mbar_arrive_expect_tx(q_full, kQBytes);
+                ptx::bulk_copy_g2s(ptx::smem_addr(&sm.q[0]),
+                                   p.q + (static_cast<size_t>(pc.b) * H + pc.kvh * G) * D, kQBytes,
+                                   q_full);
             }
-            return true;
-        };
-
-        long long x = static_unit_begin(pl, cta);
-        const long long stop = static_unit_begin(pl, cta + 1);
-        bool ok = true;
-        Piece pc;
-        while (ok && next_piece(pl, p, cta, TP, dynamic, x, stop, claimed, pc)) ok = emit_piece(pc);
-        if (ok) {
-            if (wait_bounded(q_empty, (q_n & 1u) ^ 1u, &sm.abort_flag, p.ws_flags)) {
-                sm.piece.done = 1;
-                ptx::mbar_arrive(q_full);
+            // (a q copy in flight when a wait gave up lands before the CTA exits)
+            if (!ended && n > 0) wait_drain(q_full, (n - 1u) & 1u);
+            if (Pol::kMergeInKernel && dynamic) {
+                // no combine kernel follows: the last scheduler to finish claiming zeroes the
+                // claim counter for the next call
+                if (ptx::atom_add_acq_rel_gpu(p.ws_done, 1u) == static_cast<uint32_t>(pl.g_eff - 1)) {
+                    atomicExch(p.ws_claim, 0u);
+                    atomicExch(p.ws_done, 0u);
+                }
             }
-        } else {
-            // let every copy already issued land before the CTA exits
-            const uint32_t first = t_idx > static_cast<uint32_t>(SLOTS) ? t_idx - SLOTS : 0u;
-            for (uint32_t tt = first; tt < t_idx; ++tt)
-                wait_drain(ptx::smem_addr(&sm.full[tt % SLOTS]), (tt / SLOTS) & 1u);
-            if (q_n > 0) wait_drain(q_full, (q_n - 1u) & 1u);
+            return;
         }
-        if (Pol::kMergeInKernel && dynamic) {
-            if (ptx::atom_add_acq_rel_gpu(p.ws_done, 1u) == static_cast<uint32_t>(pl.g_eff - 1)) {
-                atomicExch(p.ws_claim, 0u);
-                atomicExch(p.ws_done, 0u);
+        // ======== loaders: three threads, each for every third consumer warp ========
+        // (one thread spends ~700 cycles on 16 KB -- its TMA instructions, the scales, its
+        // barriers -- which is the time HBM takes to deliver them)
+        const uint64_t policy = ptx::policy_evict_first();
+        const int me = warp - NC - 1;
+        uint32_t filled[kLoads];   // blocks sent to warps me, me + 3, ...
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) filled[k] = 0;
+        bool ok = true;
+        for (uint32_t n = 0; ok; ++n) {
+            ok = wait_bounded(q_full, n & 1u, &sm.abort_flag, p.ws_flags);
+            if (!ok) break;
+            const QuantPiece pc = sm.piece;
+            if (pc.done) break;
+            ptx::mbar_arrive(q_empty);
+            const int32_t* bt_row =
+                kPaged ? p.block_table + static_cast<size_t>(pc.b) * p.max_pages : nullptr;
+            const int blk1 = pc.p1 / kQuantBlock;
+            const int chunk0 = pc.kvh * (D / 128);
+            int page[kLoads];   // page ids of the next round, loaded one round ahead
+            if (kPaged) {
+#pragma unroll
+                for (int k = 0; k < kLoads; ++k) {
+                    const int blk = pc.p0 / kQuantBlock + me + k * kLoaders;
+                    page[k] = me + k * kLoaders < NC && blk < blk1 ? __ldg(bt_row + blk) : 0;
+                }
             }
+            for (int round = pc.p0 / kQuantBlock; ok && round < blk1; round += NC) {
+#pragma unroll
+                for (int k = 0; k < kLoads; ++k) {
+                    const int w = me + k * kLoaders, blk = round + w;
+                    if (w >= NC || blk >= blk1) break;
+                    const int s = w * RING + static_cast<int>(filled[k] % RING);
+                    const uint32_t ph = (filled[k] / RING) & 1u;
+                    ok = wait_bounded(ptx::smem_addr(&sm.empty[s]), ph ^ 1u, &sm.abort_flag, p.ws_flags);
+                    if (!ok) break;
+                    int outer = pc.b;
+                    if (kPaged) {
+                        const bool bad = page[k] < 0 || page[k] >= p.num_pages;
+                        outer = bad ? 0 : page[k];   // (loaded, and masked by the consumer)
+                        sm.bad[s] = bad;
+                        if (bad) atomicOr(p.ws_flags, kFlagBadPage);
+                        if (blk + NC < blk1) page[k] = __ldg(bt_row + blk + NC);
+                    }
+                    const uint32_t full_bar = ptx::smem_addr(&sm.full[s]);
+                    ptx::mbar_arrive_expect_tx(full_bar, 2 * kTileBytes);
+                    const uint32_t k_dst = kv_base + s * 2 * kTileBytes;
+                    const int row = kPaged ? 0 : blk * kQuantBlock;
+                    ptx::tma_load_4d(k_dst, &tm_k, full_bar, 0, row, chunk0, outer, policy);
+                    ptx::tma_load_4d(k_dst + kTileBytes, &tm_v, full_bar, 0, row, chunk0, outer, policy);
+                    const size_t at = (kPaged ? static_cast<size_t>(outer)
+                                              : static_cast<size_t>(pc.b) * qp.blocks + blk) * KVH + pc.kvh;
+                    const uint32_t sc_dst = ptx::smem_addr(&sm.scales[s][0]);
+                    ptx::cp_async4(sc_dst, qp.k_scales + at);
+                    ptx::cp_async4(sc_dst + 4, qp.v_scales + at);
+                    ptx::cp_async_mbar_arrive(full_bar);
+                    ++filled[k];
+                    if ((p.test_flags & kTestStall) && me == 0 && filled[0] == 1 && k == 0)
+                        ok = wait_bounded(ptx::smem_addr(&sm.stall_bar), 0u, &sm.abort_flag,
+                                          p.ws_flags, kTestStallNs);
+                    if (!ok) break;
+                }
+            }
+        }
+        if (!ok) {
+            // let every copy already issued land before the CTA exits
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k)
+                for (uint32_t f = filled[k] > RING ? filled[k] - RING : 0u; f < filled[k]; ++f)
+                    wait_drain(ptx::smem_addr(&sm.full[(me + k * kLoaders) * RING + f % RING]), (f / RING) & 1u);
         }
         return;
     }
 
     // ===================== consumers =====================
-    ptx::regs_inc<kQuantConsumerRegs>();
     // Every warp passes the same barriers for every piece, whatever its waits return; a warp
     // whose wait gave up (or which saw the end) makes all of them leave at the next one.
     QuantConsumer<Pol> c;
     const uint32_t q_frag = ptx::smem_addr(&sm.q_frag[0][0]);
-    uint32_t t0 = 0;   // slots of the pieces before
+    uint32_t taken = 0;   // blocks this warp has processed (its ring's fills, in order)
     for (uint32_t n = 0;; ++n) {
         const bool there = __all_sync(0xffffffffu, wait_bounded(q_full, n & 1u, &sm.abort_flag, p.ws_flags));
         QuantPiece pc;
@@ -558,29 +559,21 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
         if (ptx::named_barrier_or(1, kConsumerThreads, pc.done != 0)) break;
         if (tid == 0) ptx::mbar_arrive(q_empty);   // every warp has read q and the piece
 
-        const uint32_t slots = static_cast<uint32_t>((pc.p1 - pc.p0 + TP - 1) / TP);
         bool gone = false;
-        // the slots of the whole call go round the warps, so that short pieces follow one
-        // another on different warps
-        for (uint32_t t_idx = t0 + ((static_cast<uint32_t>(warp) - t0) & (NC - 1)); t_idx < t0 + slots; t_idx += NC) {
-            const int s = t_idx % SLOTS;
-            const uint32_t ph = (t_idx / SLOTS) & 1u;
+        // (counted from the piece's first block: which warp takes a block, and so the order of
+        // the sums, does not depend on the pieces before)
+        for (int pos = pc.p0 + warp * kQuantBlock; pos < pc.p1; pos += NC * kQuantBlock) {
+            const int s = warp * RING + static_cast<int>(taken % RING);
+            const uint32_t ph = (taken / RING) & 1u;
             gone = !__all_sync(0xffffffffu, wait_bounded(ptx::smem_addr(&sm.full[s]), ph, &sm.abort_flag, p.ws_flags));
             if (gone) break;
-            const int pos = pc.p0 + static_cast<int>(t_idx - t0) * TP;
             const uint32_t k_tile = kv_base + s * 2 * kTileBytes;
-            const int bad = kPaged ? sm.bad[s] : 0;
-#pragma unroll 1
-            for (int j = 0; j < kBlocks; ++j) {
-                if (pos + j * kQuantBlock >= pc.p1) break;
-                c.block(k_tile + j * kBoxBytes, k_tile + kTileBytes + j * kBoxBytes,
-                        sm.scales[s][0][j], sm.scales[s][1][j], pc.lo - pos - j * kQuantBlock,
-                        pc.hi - pos - j * kQuantBlock, (bad >> j) & 1, q_frag, lane);
-            }
+            c.block(k_tile, k_tile + kTileBytes, sm.scales[s][0], sm.scales[s][1], pc.lo - pos,
+                    pc.hi - pos, kPaged && sm.bad[s] != 0, q_frag, lane);
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&sm.empty[s]));
+            ++taken;
         }
-        t0 += slots;
 
         // normalisers of this warp's columns
 #pragma unroll
@@ -606,7 +599,7 @@ __global__ void __launch_bounds__(kQuantThreads, 1)
     }
 }
 
-using QuantSliding = QuantPolicy<2, 256, 2, 12, true>;    // slidingDecodeGQA
-using QuantGlobal = QuantPolicy<8, 512, 1, 11, false>;     // decodeGQA
+using QuantSliding = QuantPolicy<2, 256, 8, 3, true>;    // slidingDecodeGQA
+using QuantGlobal = QuantPolicy<8, 512, 4, 3, false>;    // decodeGQA
 
 }  // namespace gqa

@@ -100,19 +100,6 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
     return t;
 }
 
-// ---- registers per warpgroup ----------------------------------------------------------
-
-// Give registers back, or take them from what the block was launched with; executed by all
-// four warps of a warpgroup.  An increase waits until enough were given back.
-template <int n>
-__device__ __forceinline__ void regs_dec() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(n));
-}
-template <int n>
-__device__ __forceinline__ void regs_inc() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(n));
-}
-
 // ---- programmatic dependent launch ------------------------------------------------
 
 // Wait until the grids this one depends on have completed and their memory is
@@ -314,6 +301,13 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v) {
     uint32_t r;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(v));
     return r;
+}
+// Four codes (a word, low byte first) as two packed f16 pairs.
+__device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
 }
 __device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t v) {
     return f16x2_unpack(e4m3x2_to_f16x2(v));

@@ -38,12 +38,6 @@ cudaError_t launch(const LaunchArgs& a, const DecodeQuantParams& p) {
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     std::call_once(once[dev], [&] {
-        // the kernel's register split counts on what it is launched with
-        cudaFuncAttributes attr;
-        attr_err[dev] = cudaFuncGetAttributes(&attr, gqa_decode_quant_kernel<Pol, kPaged>);
-        if (attr_err[dev] == cudaSuccess && attr.numRegs != kQuantLaunchRegs)
-            attr_err[dev] = cudaErrorInvalidKernelImage;
-        if (attr_err[dev] != cudaSuccess) return;
         attr_err[dev] = cudaFuncSetAttribute(gqa_decode_quant_kernel<Pol, kPaged>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(kSmem));
@@ -59,7 +53,7 @@ cudaError_t launch(const LaunchArgs& a, const DecodeQuantParams& p) {
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.grid));
-    cfg.blockDim = dim3(kQuantThreads);
+    cfg.blockDim = dim3(Pol::kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = a.stream;
     cfg.attrs = pdl;
