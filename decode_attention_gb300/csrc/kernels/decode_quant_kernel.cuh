@@ -33,9 +33,12 @@
 //
 // Work split, timeouts and merging between CTAs are those of decode_kernel.cuh: a
 // persistent CTA per SM, a plan built from seq_lens on the device.  Pieces start and end on
-// blocks.  One thread walks the schedule and publishes pieces; three threads stream K and V
-// with TMA, one slot per block; block i of a piece goes to consumer warp i % NC, into that
-// warp's own ring of slots.  (A ring shared by the warps would let a warp wait on a slot's
+// blocks.  The consumer warps form groups of NC; each group is a unit of the plan with a
+// schedule of its own, so that one group computes while another merges its piece (g = 2:
+// two groups of 4; g = 8, whose accumulators take twice the registers: one).  A group has two
+// producer threads: the first walks its schedule and publishes pieces, both stream K and V
+// with TMA, one slot per block.  Block i of a piece goes to warp i % NC of the group, into
+// that warp's own ring of slots.  (A ring shared by the warps would let a warp wait on a slot's
 // barrier two fills ahead of its last completion, which a parity cannot tell apart.)
 #pragma once
 
@@ -51,12 +54,15 @@ struct DecodeQuantParams {
     int blocks;              // blocks per sequence (contiguous)
 };
 
-template <int kG, int kD, int kWarps, int kRing, bool kMerge>
+template <int kG, int kD, int kGroups, int kRing, bool kMerge>
 struct QuantPolicy {
-    static constexpr int G = kG, D = kD, NC = kWarps, RING = kRing;
-    static constexpr int SLOTS = NC * RING;              // one block of K and V each
+    static constexpr int G = kG, D = kD, GROUPS = kGroups, RING = kRing;
+    static constexpr int NC = 4;                         // consumer warps per group
+    static constexpr int SLOTS = NC * RING;              // of a group: one block of K and V each
     static constexpr bool kMergeInKernel = kMerge;
-    static constexpr int kThreads = (NC + 4) * 32;       // consumers, scheduler, three loaders
+    static constexpr int kConsumers = GROUPS * NC;
+    static constexpr int kWarps = kConsumers + 2 * GROUPS;
+    static constexpr int kThreads = (kWarps < kPlanWarps ? kPlanWarps : kWarps) * 32;
     static constexpr int kUnits = D / 16;                // 16-dim steps
     static constexpr bool kSplitCols = G == 2;           // hi and lo parts of P in one mma
     static constexpr int kMergeDims = G == 2 ? 256 : 64;   // dims merged per round
@@ -76,22 +82,29 @@ struct QuantPiece {
 template <class Pol>
 struct alignas(1024) QuantSmem {
     static constexpr int kTileBytes = kQuantBlock * Pol::D;
-    uint8_t kv[Pol::SLOTS][2][kTileBytes];   // [slot][K, V][chunk][16 rows][128 B]
-    alignas(8) uint64_t full[Pol::SLOTS];
-    alignas(8) uint64_t empty[Pol::SLOTS];
-    alignas(8) uint64_t q_full, q_empty;
-    alignas(8) uint64_t stall_bar;           // kTestStall: a barrier nothing completes
-    float scales[Pol::SLOTS][2];
-    int bad[Pol::SLOTS];                     // the block's page id is out of range
-    QuantPiece piece;
+    struct Group {
+        alignas(8) uint64_t full[Pol::SLOTS];
+        alignas(8) uint64_t empty[Pol::SLOTS];
+        alignas(8) uint64_t q_full, q_empty;
+        float scales[Pol::SLOTS][2];
+        int bad[Pol::SLOTS];                     // the block's page id is out of range
+        QuantPiece piece;
+        // a piece's q fragments are last read before its merge, whose last barrier precedes the
+        // next piece's
+        union alignas(16) {
+            uint2 q_frag[Pol::kUnits][32];                      // B fragments of q (column g = head g % G)
+            float wacc[Pol::NC][Pol::G][Pol::kMergeStride];     // dims being merged
+        };
+        alignas(128) __nv_bfloat16 q[Pol::G * Pol::D];
+        float wm[Pol::NC][8], wl[Pol::NC][8];    // each warp's M and l per column
+        int merge_last;
+    };
+    uint8_t kv[Pol::GROUPS][Pol::SLOTS][2][kTileBytes];   // [slot][K, V][chunk][16 rows][128 B]
+    Group group[Pol::GROUPS];
+    alignas(8) uint64_t stall_bar;               // kTestStall: a barrier nothing completes
     PlanSmem plan;
-    int len[kMaxBatch];                      // clamped lengths
-    alignas(128) __nv_bfloat16 q[Pol::G * Pol::D];
-    alignas(16) uint2 q_frag[Pol::kUnits][32];   // B fragments of q (column g = head g % G)
-    float wm[Pol::NC][8], wl[Pol::NC][8];    // each warp's M and l per column
-    alignas(16) float wacc[Pol::NC][Pol::G][Pol::kMergeStride];
+    int len[kMaxBatch];                          // clamped lengths
     int abort_flag;
-    int merge_last;
 };
 
 template <class Pol>
@@ -145,14 +158,14 @@ struct QuantConsumer {
         l[0] = l[1] = 0.0f;
     }
 
-    // One block: rows [first, last) are attended (all of them at first <= 0, last >= 16).
+    // One block.  whole: every row is attended; else rows [first, last) are, and none is on
+    // a bad page.
+    template <bool whole>
     __device__ __forceinline__ void block(uint32_t k_blk, uint32_t v_blk, float k_scale,
                                           float v_scale, int first, int last, bool bad,
                                           uint32_t q_frag, int lane) {
         const int g = lane >> 2, t = lane & 3;
         const int mat = lane >> 3, r = (mat & 1) * 8 + (lane & 7);
-        const bool whole = first <= 0 && last >= kQuantBlock && !bad;
-
         float c[4][4];   // four independent chains
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -190,7 +203,7 @@ struct QuantConsumer {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             c[0][i] = (c[0][i] + c[1][i]) + (c[2][i] + c[3][i]);
-            if (bad) c[0][i] = __uint_as_float(0x7fc00000u);
+            if (!whole && bad) c[0][i] = __uint_as_float(0x7fc00000u);
             y[i] = level(i, evf - m[i & 1]);
         }
         // M moves only when a weight would pass 2^kTop (and on the first block, M = -inf)
@@ -250,8 +263,10 @@ struct QuantConsumer {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 uint32_t a0, a1, a2, a3;
-                ptx::e4m3x4_to_f16x2(__byte_perm(w[2 * i] & mask[0], 0u, 0x3120), a0, a1);
-                ptx::e4m3x4_to_f16x2(__byte_perm(w[2 * i + 1] & mask[1], 0u, 0x3120), a2, a3);
+                const uint32_t w0 = whole ? w[2 * i] : w[2 * i] & mask[0];
+                const uint32_t w1 = whole ? w[2 * i + 1] : w[2 * i + 1] & mask[1];
+                ptx::e4m3x4_to_f16x2(__byte_perm(w0, 0u, 0x3120), a0, a1);
+                ptx::e4m3x4_to_f16x2(__byte_perm(w1, 0u, 0x3120), a2, a3);
                 float d[4];
                 if (Pol::kSplitCols) {
                     ptx::mma_f16_16816_zero(d, a0, a1, a2, a3, hi[0], hi[1]);
@@ -269,8 +284,8 @@ struct QuantConsumer {
     // the partial (acc, m, l) at workspace slot `slot`.  The M are whole numbers, so the
     // factors 2^(M_w - M) are exact.  Called by all consumer warps, after a barrier that
     // follows the stores of wm and wl.
-    __device__ __forceinline__ void merge(QuantSmem<Pol>& sm, const DecodeParams& p, size_t out_base,
-                                          int slot, int warp, int lane) {
+    __device__ __forceinline__ void merge(typename QuantSmem<Pol>::Group& sm, const DecodeParams& p,
+                                          size_t out_base, int slot, int bar, int warp, int lane) {
         const int g = lane >> 2, t = lane & 3, tid = warp * 32 + lane;
         constexpr int kThreads = Pol::NC * 32;
         constexpr int W = Pol::kMergeDims;
@@ -320,7 +335,7 @@ struct QuantConsumer {
                         *reinterpret_cast<float2*>(&sm.wacc[warp][2 * t + j][i * 16 + 2 * g]) =
                             make_float2(acc[r * (W / 16) + i][j], acc[r * (W / 16) + i][j + 2]);
             }
-            ptx::named_barrier_sync(1, kThreads);
+            ptx::named_barrier_sync(bar, kThreads);
 #pragma unroll
             for (int k = 0; k < G / kHeadStep; ++k) {
                 const int h = k * kHeadStep + tid / (W / 2), d = 2 * (tid % (W / 2));
@@ -344,7 +359,7 @@ struct QuantConsumer {
                     }
                 }
             }
-            ptx::named_barrier_sync(1, kThreads);   // wacc is filled again
+            ptx::named_barrier_sync(bar, kThreads);   // wacc is filled again
         }
     }
 };
@@ -354,10 +369,11 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
     gqa_decode_quant_kernel(const __grid_constant__ CUtensorMap tm_k,
                             const __grid_constant__ CUtensorMap tm_v, const DecodeQuantParams qp) {
     constexpr int G = Pol::G, D = Pol::D, SLOTS = Pol::SLOTS, NC = Pol::NC, RING = Pol::RING;
-    constexpr int kLoaders = 3;
-    constexpr int kLoads = (NC + kLoaders - 1) / kLoaders;   // consumer warps a loader serves
-    constexpr int kConsumerThreads = NC * 32;
+    constexpr int GROUPS = Pol::GROUPS;
+    constexpr int kLoads = NC / 2;             // consumer warps a producer serves
+    constexpr int kGroupThreads = NC * 32;     // consumers of a group
     constexpr uint32_t kTileBytes = QuantSmem<Pol>::kTileBytes;
+    constexpr uint32_t kQBytes = G * D * 2;
     const DecodeParams& p = qp.d;
 
     extern __shared__ uint8_t smem_raw[];
@@ -368,20 +384,23 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
     const int warp = tid >> 5, lane = tid & 31;
     const int B = p.B, KVH = p.KVH, H = p.H;
     const int cta = blockIdx.x;
+    const int units = static_cast<int>(gridDim.x) * GROUPS;   // units of the plan
     PlanSmem& pl = sm.plan;
 
     if (tid == 0) {
-        for (int s = 0; s < SLOTS; ++s) {
-            ptx::mbar_init(ptx::smem_addr(&sm.full[s]), 2);   // the tiles' bytes, the scales
-            ptx::mbar_init(ptx::smem_addr(&sm.empty[s]), 1);
+        for (int g = 0; g < GROUPS; ++g) {
+            for (int s = 0; s < SLOTS; ++s) {
+                ptx::mbar_init(ptx::smem_addr(&sm.group[g].full[s]), 2);   // the tiles' bytes, the scales
+                ptx::mbar_init(ptx::smem_addr(&sm.group[g].empty[s]), 1);
+            }
+            ptx::mbar_init(ptx::smem_addr(&sm.group[g].q_full), 1);
+            ptx::mbar_init(ptx::smem_addr(&sm.group[g].q_empty), 2);   // consumers, second producer
         }
-        ptx::mbar_init(ptx::smem_addr(&sm.q_full), 1);
-        ptx::mbar_init(ptx::smem_addr(&sm.q_empty), 1 + kLoaders);   // consumers, loaders
         ptx::mbar_init(ptx::smem_addr(&sm.stall_bar), 1);
         ptx::fence_mbar_init();
         sm.abort_flag = 0;
     }
-    if (warp == NC && lane == 0) {
+    if (warp == Pol::kConsumers && lane == 0) {
         ptx::prefetch_tensormap(&tm_k);
         ptx::prefetch_tensormap(&tm_v);
     }
@@ -391,13 +410,13 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
     // (the plan's barriers make the lengths visible)
     for (int b = tid; b < B; b += blockDim.x)
         sm.len[b] = min(max(__ldg(p.seq_lens + b), 0), p.capacity);
-    build_plan<kQuantBlock>(pl, p, gridDim.x, warp, lane, cta, kQuantBlock,
-                            reinterpret_cast<uint32_t*>(&sm.kv[0][0][0]));
+    build_plan<kQuantBlock>(pl, p, units, warp, lane, cta, kQuantBlock,
+                            reinterpret_cast<uint32_t*>(&sm.kv[0][0][0][0]));
 
     // zeros for empty sequences and the segments' partial lists, as in decode_kernel.cuh
-    const bool has_work = cta < pl.g_eff;
-    if (!has_work || warp < NC) {
-        const int nt = has_work ? kConsumerThreads : static_cast<int>(blockDim.x);
+    const bool has_work = cta * GROUPS < pl.g_eff;
+    if (!has_work || warp < Pol::kConsumers) {
+        const int nt = has_work ? Pol::kConsumers * 32 : static_cast<int>(blockDim.x);
         for (int b = cta; b < B; b += gridDim.x) {
             if (pl.n[b] != 0) continue;
             const size_t base = static_cast<size_t>(b) * H * D;
@@ -417,74 +436,69 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
             }
         }
     }
-    if (!has_work) return;
+    // this warp's group and its unit (a group without a unit has nothing to do)
+    const int group = warp < Pol::kConsumers ? warp / NC : (warp - Pol::kConsumers) / 2;
+    if (warp >= Pol::kWarps) return;
+    const int unit = cta * GROUPS + group;
+    if (unit >= pl.g_eff) return;
 
-    const uint32_t kv_base = ptx::smem_addr(&sm.kv[0][0][0]);
-    const uint32_t q_full = ptx::smem_addr(&sm.q_full), q_empty = ptx::smem_addr(&sm.q_empty);
+    typename QuantSmem<Pol>::Group& gr = sm.group[group];
+    const uint32_t kv_base = ptx::smem_addr(&sm.kv[group][0][0][0]);
+    const uint32_t q_full = ptx::smem_addr(&gr.q_full), q_empty = ptx::smem_addr(&gr.q_empty);
 
-    if (warp >= NC) {
+    if (warp >= Pol::kConsumers) {
+        // ================= producers: two threads per group =================
+        // The first walks the schedule and publishes each piece with its q; both fill the
+        // slots of every second warp.  (One thread spends ~700 cycles on 16 KB -- its TMA
+        // instructions, the scales, its barriers -- which is the time HBM takes to deliver
+        // them.)
         if (lane != 0) return;
-        if (warp == NC) {
-            // ======== scheduler: one thread walks the schedule, publishes pieces and q ========
-            const bool dynamic = pl.n_dyn > 0;
-            constexpr uint32_t kQBytes = G * D * 2;
-            long long x = static_unit_begin(pl, cta);
-            const long long stop = static_unit_begin(pl, cta + 1);
-            uint32_t n = 0;   // pieces published
-            bool ended = false;
-            // the description and q are free once the consumers began the piece before and
-            // the loaders have read it
-            while (wait_bounded(q_empty, (n & 1u) ^ 1u, &sm.abort_flag, p.ws_flags)) {
-                int claimed = -1;
-                Piece pc;
-                if (!next_piece(pl, p, cta, kQuantBlock, dynamic, x, stop, claimed, pc)) {
-                    sm.piece.done = 1;
-                    ptx::mbar_arrive(q_full);
-                    ended = true;
-                    break;
-                }
-                ++n;
-                const int L = sm.len[pc.b];
-                sm.piece.b = pc.b;
-                sm.piece.kvh = pc.kvh;
-                sm.piece.p0 = pc.p0;
-                sm.piece.p1 = pc.p1;
-                sm.piece.lo = p.window > 0 && L > p.window ? L - p.window : 0;
-                sm.piece.hi = L;
-                sm.piece.slot = pc.slot;
-                sm.piece.done = 0;
-                ptx::mbar_arrive_expect_tx(q_full, kQBytes);
-                ptx::bulk_copy_g2s(ptx::smem_addr(&sm.q[0]),
-                                   p.q + (static_cast<size_t>(pc.b) * H + pc.kvh * G) * D, kQBytes,
-                                   q_full);
-            }
-            // (a q copy in flight when a wait gave up lands before the CTA exits)
-            if (!ended && n > 0) wait_drain(q_full, (n - 1u) & 1u);
-            if (Pol::kMergeInKernel && dynamic) {
-                // no combine kernel follows: the last scheduler to finish claiming zeroes the
-                // claim counter for the next call
-                if (ptx::atom_add_acq_rel_gpu(p.ws_done, 1u) == static_cast<uint32_t>(pl.g_eff - 1)) {
-                    atomicExch(p.ws_claim, 0u);
-                    atomicExch(p.ws_done, 0u);
-                }
-            }
-            return;
-        }
-        // ======== loaders: three threads, each for every third consumer warp ========
-        // (one thread spends ~700 cycles on 16 KB -- its TMA instructions, the scales, its
-        // barriers -- which is the time HBM takes to deliver them)
+        const int me = (warp - Pol::kConsumers) & 1;
         const uint64_t policy = ptx::policy_evict_first();
-        const int me = warp - NC - 1;
-        uint32_t filled[kLoads];   // blocks sent to warps me, me + 3, ...
+        const bool dynamic = pl.n_dyn > 0;
+        long long x = static_unit_begin(pl, unit);
+        const long long stop = static_unit_begin(pl, unit + 1);
+        uint32_t filled[kLoads];   // blocks sent to warps me, me + 2, ...
 #pragma unroll
         for (int k = 0; k < kLoads; ++k) filled[k] = 0;
+        uint32_t n = 0;            // pieces published
         bool ok = true;
-        for (uint32_t n = 0; ok; ++n) {
-            ok = wait_bounded(q_full, n & 1u, &sm.abort_flag, p.ws_flags);
-            if (!ok) break;
-            const QuantPiece pc = sm.piece;
-            if (pc.done) break;
-            ptx::mbar_arrive(q_empty);
+        while (true) {
+            QuantPiece pc;
+            if (me == 0) {
+                // the description and q are free once the consumers began the piece before and
+                // the other producer has read it
+                ok = wait_bounded(q_empty, (n & 1u) ^ 1u, &sm.abort_flag, p.ws_flags);
+                if (!ok) break;
+                int claimed = -1;
+                Piece w;
+                if (!next_piece(pl, p, unit, kQuantBlock, dynamic, x, stop, claimed, w)) {
+                    gr.piece.done = 1;
+                    ptx::mbar_arrive(q_full);
+                    break;
+                }
+                const int L = sm.len[w.b];
+                pc.b = w.b;
+                pc.kvh = w.kvh;
+                pc.p0 = w.p0;
+                pc.p1 = w.p1;
+                pc.lo = p.window > 0 && L > p.window ? L - p.window : 0;
+                pc.hi = L;
+                pc.slot = w.slot;
+                pc.done = 0;
+                gr.piece = pc;
+                ptx::mbar_arrive_expect_tx(q_full, kQBytes);
+                ptx::bulk_copy_g2s(ptx::smem_addr(&gr.q[0]),
+                                   p.q + (static_cast<size_t>(pc.b) * H + pc.kvh * G) * D, kQBytes,
+                                   q_full);
+            } else {
+                ok = wait_bounded(q_full, n & 1u, &sm.abort_flag, p.ws_flags);
+                if (!ok) break;
+                pc = gr.piece;
+                if (pc.done) break;
+                ptx::mbar_arrive(q_empty);
+            }
+            ++n;
             const int32_t* bt_row =
                 kPaged ? p.block_table + static_cast<size_t>(pc.b) * p.max_pages : nullptr;
             const int blk1 = pc.p1 / kQuantBlock;
@@ -493,28 +507,28 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
             if (kPaged) {
 #pragma unroll
                 for (int k = 0; k < kLoads; ++k) {
-                    const int blk = pc.p0 / kQuantBlock + me + k * kLoaders;
-                    page[k] = me + k * kLoaders < NC && blk < blk1 ? __ldg(bt_row + blk) : 0;
+                    const int blk = pc.p0 / kQuantBlock + me + 2 * k;
+                    page[k] = blk < blk1 ? __ldg(bt_row + blk) : 0;
                 }
             }
             for (int round = pc.p0 / kQuantBlock; ok && round < blk1; round += NC) {
 #pragma unroll
                 for (int k = 0; k < kLoads; ++k) {
-                    const int w = me + k * kLoaders, blk = round + w;
-                    if (w >= NC || blk >= blk1) break;
+                    const int w = me + 2 * k, blk = round + w;
+                    if (blk >= blk1) break;
                     const int s = w * RING + static_cast<int>(filled[k] % RING);
                     const uint32_t ph = (filled[k] / RING) & 1u;
-                    ok = wait_bounded(ptx::smem_addr(&sm.empty[s]), ph ^ 1u, &sm.abort_flag, p.ws_flags);
+                    ok = wait_bounded(ptx::smem_addr(&gr.empty[s]), ph ^ 1u, &sm.abort_flag, p.ws_flags);
                     if (!ok) break;
                     int outer = pc.b;
                     if (kPaged) {
                         const bool bad = page[k] < 0 || page[k] >= p.num_pages;
                         outer = bad ? 0 : page[k];   // (loaded, and masked by the consumer)
-                        sm.bad[s] = bad;
+                        gr.bad[s] = bad;
                         if (bad) atomicOr(p.ws_flags, kFlagBadPage);
                         if (blk + NC < blk1) page[k] = __ldg(bt_row + blk + NC);
                     }
-                    const uint32_t full_bar = ptx::smem_addr(&sm.full[s]);
+                    const uint32_t full_bar = ptx::smem_addr(&gr.full[s]);
                     ptx::mbar_arrive_expect_tx(full_bar, 2 * kTileBytes);
                     const uint32_t k_dst = kv_base + s * 2 * kTileBytes;
                     const int row = kPaged ? 0 : blk * kQuantBlock;
@@ -522,56 +536,73 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
                     ptx::tma_load_4d(k_dst + kTileBytes, &tm_v, full_bar, 0, row, chunk0, outer, policy);
                     const size_t at = (kPaged ? static_cast<size_t>(outer)
                                               : static_cast<size_t>(pc.b) * qp.blocks + blk) * KVH + pc.kvh;
-                    const uint32_t sc_dst = ptx::smem_addr(&sm.scales[s][0]);
+                    const uint32_t sc_dst = ptx::smem_addr(&gr.scales[s][0]);
                     ptx::cp_async4(sc_dst, qp.k_scales + at);
                     ptx::cp_async4(sc_dst + 4, qp.v_scales + at);
                     ptx::cp_async_mbar_arrive(full_bar);
                     ++filled[k];
-                    if ((p.test_flags & kTestStall) && me == 0 && filled[0] == 1 && k == 0)
+                    if ((p.test_flags & kTestStall) && me == 0 && k == 0 && filled[0] == 1)
                         ok = wait_bounded(ptx::smem_addr(&sm.stall_bar), 0u, &sm.abort_flag,
                                           p.ws_flags, kTestStallNs);
                     if (!ok) break;
                 }
             }
+            if (!ok) break;
         }
         if (!ok) {
             // let every copy already issued land before the CTA exits
 #pragma unroll
             for (int k = 0; k < kLoads; ++k)
                 for (uint32_t f = filled[k] > RING ? filled[k] - RING : 0u; f < filled[k]; ++f)
-                    wait_drain(ptx::smem_addr(&sm.full[(me + k * kLoaders) * RING + f % RING]), (f / RING) & 1u);
+                    wait_drain(ptx::smem_addr(&gr.full[(me + 2 * k) * RING + f % RING]), (f / RING) & 1u);
+            if (me == 0 && n > 0) wait_drain(q_full, (n - 1u) & 1u);
+        }
+        if (Pol::kMergeInKernel && me == 0 && dynamic) {
+            // no combine kernel follows: the last producer to finish claiming zeroes the claim
+            // counter for the next call
+            if (ptx::atom_add_acq_rel_gpu(p.ws_done, 1u) == static_cast<uint32_t>(pl.g_eff - 1)) {
+                atomicExch(p.ws_claim, 0u);
+                atomicExch(p.ws_done, 0u);
+            }
         }
         return;
     }
 
     // ===================== consumers =====================
-    // Every warp passes the same barriers for every piece, whatever its waits return; a warp
-    // whose wait gave up (or which saw the end) makes all of them leave at the next one.
+    // Every warp of a group passes the same barriers for every piece, whatever its waits
+    // return; a warp whose wait gave up (or which saw the end) makes all of them leave at the
+    // next one.
     QuantConsumer<Pol> c;
-    const uint32_t q_frag = ptx::smem_addr(&sm.q_frag[0][0]);
+    const int gwarp = warp - group * NC, gtid = gwarp * 32 + lane, bar = 1 + group;
+    const uint32_t q_frag = ptx::smem_addr(&gr.q_frag[0][0]);
     uint32_t taken = 0;   // blocks this warp has processed (its ring's fills, in order)
     for (uint32_t n = 0;; ++n) {
         const bool there = __all_sync(0xffffffffu, wait_bounded(q_full, n & 1u, &sm.abort_flag, p.ws_flags));
         QuantPiece pc;
         pc.done = 1;
-        if (there) pc = sm.piece;
-        if (!pc.done) c.begin(&sm.q[0], sm.q_frag, warp, lane);
-        if (ptx::named_barrier_or(1, kConsumerThreads, pc.done != 0)) break;
-        if (tid == 0) ptx::mbar_arrive(q_empty);   // every warp has read q and the piece
+        if (there) pc = gr.piece;
+        if (!pc.done) c.begin(&gr.q[0], gr.q_frag, gwarp, lane);
+        if (ptx::named_barrier_or(bar, kGroupThreads, pc.done != 0)) break;
+        if (gtid == 0) ptx::mbar_arrive(q_empty);   // every warp has read q and the piece
 
         bool gone = false;
         // (counted from the piece's first block: which warp takes a block, and so the order of
         // the sums, does not depend on the pieces before)
-        for (int pos = pc.p0 + warp * kQuantBlock; pos < pc.p1; pos += NC * kQuantBlock) {
-            const int s = warp * RING + static_cast<int>(taken % RING);
+        for (int pos = pc.p0 + gwarp * kQuantBlock; pos < pc.p1; pos += NC * kQuantBlock) {
+            const int s = gwarp * RING + static_cast<int>(taken % RING);
             const uint32_t ph = (taken / RING) & 1u;
-            gone = !__all_sync(0xffffffffu, wait_bounded(ptx::smem_addr(&sm.full[s]), ph, &sm.abort_flag, p.ws_flags));
+            gone = !__all_sync(0xffffffffu, wait_bounded(ptx::smem_addr(&gr.full[s]), ph, &sm.abort_flag, p.ws_flags));
             if (gone) break;
             const uint32_t k_tile = kv_base + s * 2 * kTileBytes;
-            c.block(k_tile, k_tile + kTileBytes, sm.scales[s][0], sm.scales[s][1], pc.lo - pos,
-                    pc.hi - pos, kPaged && sm.bad[s] != 0, q_frag, lane);
+            const float ks = gr.scales[s][0], vs = gr.scales[s][1];
+            const bool bad = kPaged && gr.bad[s] != 0;
+            const int first = pc.lo - pos, last = pc.hi - pos;
+            if (first <= 0 && last >= kQuantBlock && !bad)
+                c.template block<true>(k_tile, k_tile + kTileBytes, ks, vs, 0, kQuantBlock, false, q_frag, lane);
+            else
+                c.template block<false>(k_tile, k_tile + kTileBytes, ks, vs, first, last, bad, q_frag, lane);
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&sm.empty[s]));
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&gr.empty[s]));
             ++taken;
         }
 
@@ -583,23 +614,23 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
             ls += __shfl_xor_sync(0xffffffffu, ls, 8);
             ls += __shfl_xor_sync(0xffffffffu, ls, 16);
             if (lane < 4) {
-                sm.wm[warp][2 * lane + j] = c.m[j];
-                sm.wl[warp][2 * lane + j] = ls;
+                gr.wm[gwarp][2 * lane + j] = c.m[j];
+                gr.wl[gwarp][2 * lane + j] = ls;
             }
         }
-        if (ptx::named_barrier_or(1, kConsumerThreads, gone)) break;
+        if (ptx::named_barrier_or(bar, kGroupThreads, gone)) break;
         const SegmentParts sp(pl, pc.b, pc.kvh, p.dyn_slot_base);
         const int nparts = sp.count();
         const size_t out_base = (static_cast<size_t>(pc.b) * H + pc.kvh * G) * D;
-        c.merge(sm, p, out_base, nparts == 1 ? -1 : pc.slot, warp, lane);
+        c.merge(gr, p, out_base, nparts == 1 ? -1 : pc.slot, bar, gwarp, lane);
         if constexpr (Pol::kMergeInKernel)
             if (nparts > 1)
-                count_and_merge<G, D, kConsumerThreads>(p, sp, pc.b * KVH + pc.kvh, out_base, tid,
-                                                        &sm.merge_last);
+                count_and_merge<G, D, kGroupThreads>(p, sp, pc.b * KVH + pc.kvh, out_base, gtid,
+                                                     &gr.merge_last, bar);
     }
 }
 
-using QuantSliding = QuantPolicy<2, 256, 8, 3, true>;    // slidingDecodeGQA
-using QuantGlobal = QuantPolicy<8, 512, 4, 3, false>;    // decodeGQA
+using QuantSliding = QuantPolicy<2, 256, 2, 3, true>;    // slidingDecodeGQA
+using QuantGlobal = QuantPolicy<8, 512, 1, 3, false>;    // decodeGQA
 
 }  // namespace gqa
