@@ -659,25 +659,22 @@ __device__ __forceinline__ void merge_segment(const DecodeParams& p, const Segme
 
 // After this CTA's consumers stored a partial of segment u: count it, and if it was
 // the segment's last, merge all of them into the output.  Every consumer thread
-// calls this; `last` is a shared-memory flag, `bar` the threads' named barrier.  One thread counts, with release
+// calls this; `last` is a shared-memory flag.  One thread counts, with release
 // semantics (the CTA's partial stores, ordered before it by the barrier, are
 // visible to the merging CTA) and acquire semantics (if it completes the count, the
 // other CTAs' partials are visible here; the barrier after it passes that on).
 template <int G, int D, int kThreads>
 __device__ __forceinline__ void count_and_merge(const DecodeParams& p, const SegmentParts& sp,
-                                                int u, size_t out_base, int tid, volatile int* last,
-                                                int bar = 1) {
-    ptx::named_barrier_sync(bar, kThreads);
+                                                int u, size_t out_base, int tid, volatile int* last) {
+    ptx::named_barrier_sync(1, kThreads);
     if (tid == 0)
         *last = ptx::atom_add_acq_rel_gpu(p.ws_seg_count + u, 1u) ==
                         static_cast<uint32_t>(sp.count() - 1)
                     ? 1
                     : 0;
-    ptx::named_barrier_sync(bar, kThreads);
+    ptx::named_barrier_sync(1, kThreads);
     if (!*last) return;
-#pragma unroll
-    for (int i = 0; i < G * D / 2; i += kThreads)   // two outputs per thread and turn
-        merge_segment<G, D, G * D / 2>(p, sp, u, out_base, i + tid);
+    merge_segment<G, D, kThreads>(p, sp, u, out_base, tid);
     if (tid == 0) p.ws_seg_count[u] = 0u;
 }
 

@@ -65,8 +65,10 @@ struct QuantPolicy {
     static constexpr int kThreads = (kWarps < kPlanWarps ? kPlanWarps : kWarps) * 32;
     static constexpr int kUnits = D / 16;                // 16-dim steps
     static constexpr bool kSplitCols = G == 2;           // hi and lo parts of P in one mma
-    static constexpr int kMergeDims = G == 2 ? 256 : 64;   // dims merged per round
+    static constexpr int kMergeDims = 128;               // dims merged per round
     static constexpr int kMergeStride = kMergeDims + 4;  // conflict-free float2 stores
+    static constexpr int kMergeCols = kSplitCols ? 2 * G : G;
+    static constexpr int kQStride = D + 16;              // padded row of q: conflict-free 8-byte loads
     static_assert((G == 2 || G == 8) && kUnits % 4 == 0 && D % kMergeDims == 0, "shape");
 };
 
@@ -76,6 +78,7 @@ struct QuantPiece {
     int p0, p1;     // positions, whole blocks
     int lo, hi;     // attended positions of the sequence
     int slot;       // workspace slot of the partial
+    int parts;      // partials of the segment (1: the piece is the whole segment)
     int done;       // no more pieces
 };
 
@@ -93,9 +96,9 @@ struct alignas(1024) QuantSmem {
         // next piece's
         union alignas(16) {
             uint2 q_frag[Pol::kUnits][32];                      // B fragments of q (column g = head g % G)
-            float wacc[Pol::NC][Pol::G][Pol::kMergeStride];     // dims being merged
+            float wacc[Pol::NC][Pol::kMergeCols][Pol::kMergeStride];   // dims being merged
         };
-        alignas(128) __nv_bfloat16 q[Pol::G * Pol::D];
+        alignas(128) __nv_bfloat16 q[Pol::G][Pol::kQStride];
         float wm[Pol::NC][8], wl[Pol::NC][8];    // each warp's M and l per column
         int merge_last;
     };
@@ -123,12 +126,12 @@ struct QuantConsumer {
         return block + (unit >> 3) * 2048 + r * 128 + (((unit & 7) ^ (r & 7)) << 4);
     }
 
-    // q_heads: [G][D] bf16 in shared memory.  Each warp makes its share of the fragments (a
+    // q_heads: [G][kQStride] bf16 in shared memory.  Each warp makes its share of the fragments (a
     // barrier follows).
     __device__ __forceinline__ void begin(const __nv_bfloat16* q_heads, uint2 (*frag)[32], int warp,
                                           int lane) {
         const int g = lane >> 2, t = lane & 3;
-        const __nv_bfloat16* row = q_heads + (g % G) * D + 4 * t;
+        const __nv_bfloat16* row = q_heads + (g % G) * Pol::kQStride + 4 * t;
         uint32_t top = 0;   // largest |q|: the bits of |bf16| order like the values
 #pragma unroll 8
         for (int u = 0; u < kUnits; ++u) {
@@ -290,7 +293,7 @@ struct QuantConsumer {
         constexpr int kThreads = Pol::NC * 32;
         constexpr int W = Pol::kMergeDims;
         // a round merges G heads x W dims; a thread takes two dims of every kHeadStep-th head
-        constexpr int kHeadStep = kThreads / (W / 2) < G ? kThreads / (W / 2) : G;
+        constexpr int kHeadStep = kThreads / (W / 2);
         static_assert(kHeadStep * (W / 2) == kThreads && G % kHeadStep == 0, "two dims per thread");
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -304,12 +307,6 @@ struct QuantConsumer {
                 acc[i][j] *= f;
                 acc[i][j + 2] *= f;
             }
-        }
-        if (Pol::kSplitCols) {
-#pragma unroll
-            for (int i = 0; i < kUnits; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] += __shfl_xor_sync(0xffffffffu, acc[i][j], 1);
         }
         float top[G / kHeadStep], ls[G / kHeadStep];   // of this thread's heads
 #pragma unroll
@@ -327,7 +324,7 @@ struct QuantConsumer {
         }
 #pragma unroll
         for (int r = 0; r < D / W; ++r) {
-            if (2 * t < G) {
+            if (2 * t < Pol::kMergeCols) {   // (at kSplitCols t = 1 holds the lo parts' products)
 #pragma unroll
                 for (int i = 0; i < W / 16; ++i)
 #pragma unroll
@@ -341,11 +338,13 @@ struct QuantConsumer {
                 const int h = k * kHeadStep + tid / (W / 2), d = 2 * (tid % (W / 2));
                 float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
-                for (int w = 0; w < Pol::NC; ++w) {
-                    const float2 x = *reinterpret_cast<const float2*>(&sm.wacc[w][h][d]);
-                    s.x += x.x;
-                    s.y += x.y;
-                }
+                for (int w = 0; w < Pol::NC; ++w)
+#pragma unroll
+                    for (int c = 0; c < Pol::kMergeCols; c += G) {
+                        const float2 x = *reinterpret_cast<const float2*>(&sm.wacc[w][c + h][d]);
+                        s.x += x.x;
+                        s.y += x.y;
+                    }
                 const size_t at = static_cast<size_t>(h) * D + r * W + d;
                 if (slot < 0) {
                     const float inv = 1.0f / ls[k];
@@ -485,12 +484,15 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
                 pc.lo = p.window > 0 && L > p.window ? L - p.window : 0;
                 pc.hi = L;
                 pc.slot = w.slot;
+                pc.parts = SegmentParts(pl, w.b, w.kvh, p.dyn_slot_base).count();
                 pc.done = 0;
                 gr.piece = pc;
                 ptx::mbar_arrive_expect_tx(q_full, kQBytes);
-                ptx::bulk_copy_g2s(ptx::smem_addr(&gr.q[0]),
-                                   p.q + (static_cast<size_t>(pc.b) * H + pc.kvh * G) * D, kQBytes,
-                                   q_full);
+#pragma unroll
+                for (int h = 0; h < G; ++h)
+                    ptx::bulk_copy_g2s(ptx::smem_addr(&gr.q[h][0]),
+                                       p.q + (static_cast<size_t>(pc.b) * H + pc.kvh * G + h) * D,
+                                       D * 2, q_full);
             } else {
                 ok = wait_bounded(q_full, n & 1u, &sm.abort_flag, p.ws_flags);
                 if (!ok) break;
@@ -576,13 +578,31 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
     const int gwarp = warp - group * NC, gtid = gwarp * 32 + lane, bar = 1 + group;
     const uint32_t q_frag = ptx::smem_addr(&gr.q_frag[0][0]);
     uint32_t taken = 0;   // blocks this warp has processed (its ring's fills, in order)
+    // In-kernel merge of a segment's partials: the group whose partial completes the count
+    // merges them.  The count's round trip is not waited for: its result is used one piece
+    // later.
+    bool counted = false, arrived = false;
+    int counted_b = 0, counted_kvh = 0;
+    auto merge_counted = [&]() {   // every thread of the group, after the barrier that follows the flag
+        if (!counted || !gr.merge_last) return;
+        const SegmentParts sp(pl, counted_b, counted_kvh, p.dyn_slot_base);
+        const int u = counted_b * KVH + counted_kvh;
+#pragma unroll
+        for (int i = 0; i < G * D / 2; i += kGroupThreads)   // two outputs per thread and turn
+            merge_segment<G, D, G * D / 2>(p, sp, u, static_cast<size_t>(u) * G * D, i + gtid);
+        if (gtid == 0) p.ws_seg_count[u] = 0u;
+    };
     for (uint32_t n = 0;; ++n) {
         const bool there = __all_sync(0xffffffffu, wait_bounded(q_full, n & 1u, &sm.abort_flag, p.ws_flags));
         QuantPiece pc;
         pc.done = 1;
         if (there) pc = gr.piece;
-        if (!pc.done) c.begin(&gr.q[0], gr.q_frag, gwarp, lane);
-        if (ptx::named_barrier_or(bar, kGroupThreads, pc.done != 0)) break;
+        if (!pc.done) c.begin(&gr.q[0][0], gr.q_frag, gwarp, lane);
+        if (Pol::kMergeInKernel && pc.done && gtid == 0) gr.merge_last = arrived;
+        if (ptx::named_barrier_or(bar, kGroupThreads, pc.done != 0)) {
+            if constexpr (Pol::kMergeInKernel) merge_counted();
+            break;
+        }
         if (gtid == 0) ptx::mbar_arrive(q_empty);   // every warp has read q and the piece
 
         bool gone = false;
@@ -618,19 +638,27 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
                 gr.wl[gwarp][2 * lane + j] = ls;
             }
         }
+        if (Pol::kMergeInKernel && gtid == 0) gr.merge_last = arrived;
         if (ptx::named_barrier_or(bar, kGroupThreads, gone)) break;
-        const SegmentParts sp(pl, pc.b, pc.kvh, p.dyn_slot_base);
-        const int nparts = sp.count();
         const size_t out_base = (static_cast<size_t>(pc.b) * H + pc.kvh * G) * D;
-        c.merge(gr, p, out_base, nparts == 1 ? -1 : pc.slot, bar, gwarp, lane);
-        if constexpr (Pol::kMergeInKernel)
-            if (nparts > 1)
-                count_and_merge<G, D, kGroupThreads>(p, sp, pc.b * KVH + pc.kvh, out_base, gtid,
-                                                     &gr.merge_last, bar);
+        c.merge(gr, p, out_base, pc.parts == 1 ? -1 : pc.slot, bar, gwarp, lane);
+        if constexpr (Pol::kMergeInKernel) {
+            // count the partial (the merge's last barrier is behind its stores); whether it was
+            // the segment's last is looked at when the next piece ends
+            merge_counted();
+            counted = pc.parts > 1;
+            counted_b = pc.b;
+            counted_kvh = pc.kvh;
+            arrived = false;
+            if (counted && gtid == 0)
+                arrived = ptx::atom_add_acq_rel_gpu(p.ws_seg_count + pc.b * KVH + pc.kvh, 1u) + 1u ==
+                          static_cast<uint32_t>(pc.parts);
+        }
     }
 }
 
-using QuantSliding = QuantPolicy<2, 256, 2, 3, true>;    // slidingDecodeGQA
-using QuantGlobal = QuantPolicy<8, 512, 1, 3, false>;    // decodeGQA
+using QuantSliding = QuantPolicy<2, 256, 2, 3, false>;       // slidingDecodeGQA, many segments
+using QuantSlidingFew = QuantPolicy<2, 256, 2, 3, true>;     // slidingDecodeGQA, few segments
+using QuantGlobal = QuantPolicy<8, 512, 1, 3, false>;        // decodeGQA
 
 }  // namespace gqa

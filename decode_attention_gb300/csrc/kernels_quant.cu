@@ -80,7 +80,11 @@ cudaError_t launch_quant(const LaunchArgs& a, bool sliding, bool paged) {
     p.k_scales = a.k_scales;
     p.v_scales = a.v_scales;
     p.blocks = static_cast<int>((a.rows + kQuantBlock - 1) / kQuantBlock);
-    if (sliding) return paged ? launch<QuantSliding, true>(a, p) : launch<QuantSliding, false>(a, p);
+    if (sliding) {
+        if (a.p.B * a.p.KVH <= a.grid)
+            return paged ? launch<QuantSlidingFew, true>(a, p) : launch<QuantSlidingFew, false>(a, p);
+        return paged ? launch<QuantSliding, true>(a, p) : launch<QuantSliding, false>(a, p);
+    }
     return paged ? launch<QuantGlobal, true>(a, p) : launch<QuantGlobal, false>(a, p);
 }
 
