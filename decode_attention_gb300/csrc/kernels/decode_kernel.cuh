@@ -47,6 +47,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -184,9 +185,11 @@ __device__ __forceinline__ long long div_floor(long long a, long long b) {
     return a / b;
 }
 
-// Static tiles of each segment of sequence b.
+// Static tiles of each segment of sequence b.  kExtra > 0 counts that many more in front of
+// the real ones, which stand for the cost of a piece and hold no positions.
+template <int kExtra = 0>
 __device__ __forceinline__ int static_tiles(const PlanSmem& pl, int b) {
-    return (pl.sn[b] + pl.unit - 1) / pl.unit;
+    return kExtra + (pl.sn[b] + pl.unit - 1) / pl.unit;
 }
 // First static tile of unit j.  The static heads of all segments, concatenated in
 // (b, kvh) order and counted in tiles, are split evenly over the units: a unit
@@ -203,11 +206,13 @@ __device__ __forceinline__ int static_unit_of(const PlanSmem& pl, long long x) {
 // then dynamic chunks dk0..dk0+nd_parts-1.
 struct SegmentParts {
     int first_s, ns_parts, dk0, nd_parts, dyn_base;
-    __device__ __forceinline__ SegmentParts(const PlanSmem& pl, int b, int kvh, int dyn_slot_base)
+    template <int kExtra = 0>
+    __device__ __forceinline__ SegmentParts(const PlanSmem& pl, int b, int kvh, int dyn_slot_base,
+                                            std::integral_constant<int, kExtra> = {})
         : dyn_base(dyn_slot_base) {
-        const int st = static_tiles(pl, b);
+        const int st = static_tiles<kExtra>(pl, b);
         const long long ss = pl.spref[b] + static_cast<long long>(kvh) * st;
-        first_s = static_unit_of(pl, ss);
+        first_s = static_unit_of(pl, ss + kExtra);
         ns_parts = static_unit_of(pl, ss + st - 1) - first_s + 1;
         // the dynamic slots of a segment are contiguous: its long chunks, then its
         // short ones (whatever order they are claimed in)
@@ -234,22 +239,24 @@ struct Piece {
 // counter (a claim may already be in flight in `claimed`, -1 when not).  Fills `pc` and
 // returns true, or returns false when no piece is left.  One call site per producer
 // keeps the producer's code (and its instruction-cache footprint) small.
+template <int kExtra = 0>
 __device__ __forceinline__ bool next_piece(const PlanSmem& pl, const DecodeParams& p, int cta,
                                            int tile, bool dynamic, long long& x, long long stop,
                                            int& claimed, Piece& pc) {
     const int B = p.B, KVH = p.KVH;
-    if (x < stop) {
+    while (x < stop) {
         const int b = upper_seq(pl.spref, B, x);
-        const int st = static_tiles(pl, b);
+        const int st = static_tiles<kExtra>(pl, b);
         const long long rel = x - pl.spref[b];
         const int kvh = static_cast<int>(div_floor(rel, st));
         const int k0 = static_cast<int>(rel - static_cast<long long>(kvh) * st);
         const int take = static_cast<int>(stop - x < st - k0 ? stop - x : st - k0);
         x += take;
-        const int e = k0 + take == st ? pl.sn[b] : (k0 + take) * tile;
+        if (kExtra > 0 && k0 + take <= kExtra) continue;   // no positions among them
+        const int e = k0 + take == st ? pl.sn[b] : (k0 + take - kExtra) * tile;
         pc.b = b;
         pc.kvh = kvh;
-        pc.p0 = pl.lo[b] + k0 * tile;
+        pc.p0 = pl.lo[b] + (k0 > kExtra ? k0 - kExtra : 0) * tile;
         pc.p1 = pl.lo[b] + e;
         pc.slot = cta + b * KVH + kvh;
         pc.unit_end = x >= stop;
@@ -414,11 +421,11 @@ __device__ __forceinline__ void store_out4(const DecodeParams& p, size_t idx, fl
 //
 // kAlign: ranges are widened to whole blocks of kAlign positions, which makes every piece
 // start and end on a block when `unit` is whole blocks too; the caller masks the
-// positions outside the attended range.
+// positions outside the attended range.  kExtra: see static_tiles.
 // ---------------------------------------------------------------------------
 constexpr int kPlanWarps = kMaxBatch / 32;   // 8
 
-template <int kAlign = 1>
+template <int kAlign = 1, int kExtra = 0>
 __device__ __forceinline__ void build_plan(PlanSmem& pl, const DecodeParams& p, int grid, int warp,
                                            int lane, int cta, int unit, uint32_t* xsum) {
     const int B = p.B, KVH = p.KVH;
@@ -539,7 +546,7 @@ __device__ __forceinline__ void build_plan(PlanSmem& pl, const DecodeParams& p, 
             pl.dn[b] = static_cast<uint16_t>(d);
             pl.dn1[b] = static_cast<uint16_t>(d1);
         }
-        st_own = ((sn + unit - 1) / unit) * KVH;
+        st_own = sn > 0 ? (kExtra + (sn + unit - 1) / unit) * KVH : 0;
         d_own = d * KVH;
         d1_own = d1 * KVH;
         st_incl = static_cast<uint32_t>(st_own);

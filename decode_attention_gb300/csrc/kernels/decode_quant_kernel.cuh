@@ -35,7 +35,9 @@
 // persistent CTA per SM, a plan built from seq_lens on the device.  Pieces start and end on
 // blocks.  The consumer warps form groups of NC; each group is a unit of the plan with a
 // schedule of its own, so that one group computes while another merges its piece (g = 2:
-// two groups of 4; g = 8, whose accumulators take twice the registers: one).  A group has two
+// two groups of 4).  At g = 8 the D x 8 accumulators of a block would take 128 registers and
+// leave one warp per scheduler; there two warps share a block, half of D each, and add their
+// halves of the scores (one group of 4 pairs).  A group has two
 // producer threads: the first walks its schedule and publishes pieces, both stream K and V
 // with TMA, one slot per block.  Block i of a piece goes to warp i % NC of the group, into
 // that warp's own ring of slots.  (A ring shared by the warps would let a warp wait on a slot's
@@ -54,22 +56,28 @@ struct DecodeQuantParams {
     int blocks;              // blocks per sequence (contiguous)
 };
 
-template <int kG, int kD, int kGroups, int kRing, bool kMerge>
+template <int kG, int kD, int kGroups, int kSplitD, int kRing, bool kMerge>
 struct QuantPolicy {
     static constexpr int G = kG, D = kD, GROUPS = kGroups, RING = kRing;
-    static constexpr int NC = 4;                         // consumer warps per group
+    static constexpr int NC = 4;                         // blocks a group works on at a time
+    static constexpr int SPLIT = kSplitD;                // warps per block, D / SPLIT dims each
+    static constexpr int GW = NC * SPLIT;                // consumer warps per group
     static constexpr int SLOTS = NC * RING;              // of a group: one block of K and V each
     static constexpr bool kMergeInKernel = kMerge;
-    static constexpr int kConsumers = GROUPS * NC;
+    static constexpr int kConsumers = GROUPS * GW;
     static constexpr int kWarps = kConsumers + 2 * GROUPS;
     static constexpr int kThreads = (kWarps < kPlanWarps ? kPlanWarps : kWarps) * 32;
     static constexpr int kUnits = D / 16;                // 16-dim steps
+    static constexpr int kOwnUnits = kUnits / SPLIT;     // those of one warp
+    // Cost of a piece (q, merge, barriers: 2-3 us of a group) in blocks, for the plan's balance
+    static constexpr int kExtra = 4;
     static constexpr bool kSplitCols = G == 2;           // hi and lo parts of P in one mma
-    static constexpr int kMergeDims = 128;               // dims merged per round
+    static constexpr int kMergeDims = 128 / SPLIT;       // dims of a warp merged per round
     static constexpr int kMergeStride = kMergeDims + 4;  // conflict-free float2 stores
     static constexpr int kMergeCols = kSplitCols ? 2 * G : G;
     static constexpr int kQStride = D + 16;              // padded row of q: conflict-free 8-byte loads
-    static_assert((G == 2 || G == 8) && kUnits % 4 == 0 && D % kMergeDims == 0, "shape");
+    static_assert((G == 2 || G == 8) && kOwnUnits % 4 == 0 && (D / SPLIT) % kMergeDims == 0, "shape");
+    static_assert(SPLIT == 1 || SPLIT == 2, "a block is one warp's or two's");
 };
 
 // One piece of work, published with its q.
@@ -96,10 +104,10 @@ struct alignas(1024) QuantSmem {
         // next piece's
         union alignas(16) {
             uint2 q_frag[Pol::kUnits][32];                      // B fragments of q (column g = head g % G)
-            float wacc[Pol::NC][Pol::kMergeCols][Pol::kMergeStride];   // dims being merged
+            float wacc[Pol::SPLIT][Pol::NC][Pol::kMergeCols][Pol::kMergeStride];   // dims being merged
         };
         alignas(128) __nv_bfloat16 q[Pol::G][Pol::kQStride];
-        float wm[Pol::NC][8], wl[Pol::NC][8];    // each warp's M and l per column
+        float wm[Pol::NC][8], wl[Pol::NC][8];    // M and l per column of each warp (pair)
         int merge_last;
     };
     uint8_t kv[Pol::GROUPS][Pol::SLOTS][2][kTileBytes];   // [slot][K, V][chunk][16 rows][128 B]
@@ -112,12 +120,12 @@ struct alignas(1024) QuantSmem {
 
 template <class Pol>
 struct QuantConsumer {
-    static constexpr int G = Pol::G, D = Pol::D, kUnits = Pol::kUnits;
+    static constexpr int G = Pol::G, D = Pol::D, kUnits = Pol::kUnits, kOwnUnits = Pol::kOwnUnits;
     static constexpr float kTop = 15.0f;    // largest exponent of a weight (f16 ends at 2^16)
     static constexpr float kRoom = 3.0f;    // binades left above the maximum when M is set
 
     float q_factor[2];           // undo q's scaling for columns 2t and 2t + 1, times log2(e)
-    float acc[kUnits][4];        // rows: dims 2g (0, 1) and 2g + 1 (2, 3); columns 2t, 2t + 1
+    float acc[kOwnUnits][4];     // rows: dims 2g (0, 1) and 2g + 1 (2, 3); columns 2t, 2t + 1
     float m[2];                  // M of columns 2t, 2t + 1
     float l[2];                  // this lane's share of their normalisers
 
@@ -144,8 +152,8 @@ struct QuantConsumer {
         const int e = max(static_cast<int>(top >> 7) - 127, -100);   // |q| < 2^(e + 1)
         const float f = pow2f(14 - e);
 #pragma unroll
-        for (int i = 0; i < kUnits / Pol::NC; ++i) {
-            const int u = warp * (kUnits / Pol::NC) + i;
+        for (int i = 0; i < kUnits / Pol::GW; ++i) {
+            const int u = warp * (kUnits / Pol::GW) + i;
             const uint2 w = *reinterpret_cast<const uint2*>(row + u * 16);
             frag[u][lane] = make_uint2(ptx::f16x2_pack(bf16lo(w.x) * f, bf16hi(w.x) * f),
                                        ptx::f16x2_pack(bf16lo(w.y) * f, bf16hi(w.y) * f));
@@ -154,39 +162,51 @@ struct QuantConsumer {
         q_factor[0] = __shfl_sync(0xffffffffu, undo, 8 * t);
         q_factor[1] = __shfl_sync(0xffffffffu, undo, 8 * t + 4);
 #pragma unroll
-        for (int i = 0; i < kUnits; ++i)
+        for (int i = 0; i < kOwnUnits; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
         m[0] = m[1] = -INFINITY;
         l[0] = l[1] = 0.0f;
     }
 
-    // One block.  whole: every row is attended; else rows [first, last) are, and none is on
-    // a bad page.
-    template <bool whole>
-    __device__ __forceinline__ void block(uint32_t k_blk, uint32_t v_blk, float k_scale,
-                                          float v_scale, int first, int last, bool bad,
-                                          uint32_t q_frag, int lane) {
-        const int g = lane >> 2, t = lane & 3;
+    // This warp's share (`half` of D) of a block's scores, c[i]: rows g (0, 1) and g + 8 (2, 3),
+    // columns 2t, 2t + 1.
+    __device__ __forceinline__ void scores(uint32_t k_blk, uint32_t q_frag, int half, float (&z)[4],
+                                           int lane) {
         const int mat = lane >> 3, r = (mat & 1) * 8 + (lane & 7);
         float c[4][4];   // four independent chains
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) c[i][j] = 0.0f;
+        // (unit_addr's chunks: kOwnUnits is a multiple of 8 units or the whole of D)
+        const uint32_t k_half = k_blk + half * (kOwnUnits / 8) * 2048;
+        const uint32_t q_half = q_frag + half * kOwnUnits * 256;
 #pragma unroll
-        for (int u = 0; u < kUnits; u += 2) {
+        for (int u = 0; u < kOwnUnits; u += 2) {
             uint32_t a[4];   // rows g, g + 8 of unit u, then of unit u + 1
-            ptx::ldmatrix_x4(unit_addr(k_blk, r, u + (mat >> 1)), a[0], a[1], a[2], a[3]);
+            ptx::ldmatrix_x4(unit_addr(k_half, r, u + (mat >> 1)), a[0], a[1], a[2], a[3]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const uint2 q = ptx::lds64(q_frag + (u + i) * 256 + lane * 8);
+                const uint2 q = ptx::lds64(q_half + (u + i) * 256 + lane * 8);
                 uint32_t a0, a1, a2, a3;
                 ptx::e4m3x4_to_f16x2(a[2 * i], a0, a2);
                 ptx::e4m3x4_to_f16x2(a[2 * i + 1], a1, a3);
                 ptx::mma_f16_16816(c[(u + i) & 3], a0, a1, a2, a3, q.x, q.y);
             }
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = (c[0][i] + c[1][i]) + (c[2][i] + c[3][i]);
+    }
+
+    // The rest of a block, from its scores z: weights, M, l, and P.V for this warp's dims.  whole:
+    // every row is attended; else rows [first, last) are, and none of them on a bad page.
+    template <bool whole>
+    __device__ __forceinline__ void weigh(const float (&z)[4], uint32_t v_blk, float k_scale,
+                                          float v_scale, int first, int last, bool bad, int half,
+                                          int lane) {
+        const int g = lane >> 2, t = lane & 3;
+        const int mat = lane >> 3, r = (mat & 1) * 8 + (lane & 7);
         // log2 of the weights: y = log2(e) score + ev - M, rows g (0, 1) and g + 8 (2, 3)
         const float fk = pow2f(scale_exponent(k_scale));
         const int ev = scale_exponent(v_scale);
@@ -199,14 +219,12 @@ struct QuantConsumer {
             row_ok[1] = g + 8 >= first && g + 8 < last;
         }
         auto level = [&](int i, float shift) {
-            const float v = fmaf(c[0][i], f[i & 1], shift);
+            const float v = fmaf(z[i], f[i & 1], !whole && bad ? __uint_as_float(0x7fc00000u) : shift);
             return row_ok[i >> 1] ? v : -INFINITY;
         };
         float y[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            c[0][i] = (c[0][i] + c[1][i]) + (c[2][i] + c[3][i]);
-            if (!whole && bad) c[0][i] = __uint_as_float(0x7fc00000u);
             y[i] = level(i, evf - m[i & 1]);
         }
         // M moves only when a weight would pass 2^kTop (and on the first block, M = -inf)
@@ -222,7 +240,7 @@ struct QuantConsumer {
                 const float alpha = mn == m[j] ? 1.0f : ptx::ex2(m[j] - mn);
                 l[j] *= alpha;
 #pragma unroll
-                for (int i = 0; i < kUnits; ++i) {
+                for (int i = 0; i < kOwnUnits; ++i) {
                     acc[i][j] *= alpha;
                     acc[i][j + 2] *= alpha;
                 }
@@ -259,10 +277,11 @@ struct QuantConsumer {
                 if (bad) mask[i] = 0u;
             }
         }
+        const uint32_t v_half = v_blk + half * (kOwnUnits / 8) * 2048;
 #pragma unroll
-        for (int u = 0; u < kUnits; u += 2) {
+        for (int u = 0; u < kOwnUnits; u += 2) {
             uint32_t w[4];   // positions 0-7, 8-15 of unit u, then of unit u + 1
-            ptx::ldmatrix_x4_trans(unit_addr(v_blk, r, u + (mat >> 1)), w[0], w[1], w[2], w[3]);
+            ptx::ldmatrix_x4_trans(unit_addr(v_half, r, u + (mat >> 1)), w[0], w[1], w[2], w[3]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 uint32_t a0, a1, a2, a3;
@@ -288,9 +307,10 @@ struct QuantConsumer {
     // factors 2^(M_w - M) are exact.  Called by all consumer warps, after a barrier that
     // follows the stores of wm and wl.
     __device__ __forceinline__ void merge(typename QuantSmem<Pol>::Group& sm, const DecodeParams& p,
-                                          size_t out_base, int slot, int bar, int warp, int lane) {
-        const int g = lane >> 2, t = lane & 3, tid = warp * 32 + lane;
-        constexpr int kThreads = Pol::NC * 32;
+                                          size_t out_base, int slot, int bar, int own, int half,
+                                          int lane) {
+        const int g = lane >> 2, t = lane & 3, tid = own * 32 + lane;
+        constexpr int kThreads = Pol::NC * 32;          // of each half of D
         constexpr int W = Pol::kMergeDims;
         // a round merges G heads x W dims; a thread takes two dims of every kHeadStep-th head
         constexpr int kHeadStep = kThreads / (W / 2);
@@ -303,7 +323,7 @@ struct QuantConsumer {
             // (a warp without a finite score weighs 0; its NaN stay)
             const float f = m[j] == -INFINITY ? 0.0f : ptx::ex2(m[j] - top);
 #pragma unroll
-            for (int i = 0; i < kUnits; ++i) {
+            for (int i = 0; i < kOwnUnits; ++i) {
                 acc[i][j] *= f;
                 acc[i][j + 2] *= f;
             }
@@ -323,16 +343,16 @@ struct QuantConsumer {
             }
         }
 #pragma unroll
-        for (int r = 0; r < D / W; ++r) {
+        for (int r = 0; r < D / Pol::SPLIT / W; ++r) {
             if (2 * t < Pol::kMergeCols) {   // (at kSplitCols t = 1 holds the lo parts' products)
 #pragma unroll
                 for (int i = 0; i < W / 16; ++i)
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
-                        *reinterpret_cast<float2*>(&sm.wacc[warp][2 * t + j][i * 16 + 2 * g]) =
+                        *reinterpret_cast<float2*>(&sm.wacc[half][own][2 * t + j][i * 16 + 2 * g]) =
                             make_float2(acc[r * (W / 16) + i][j], acc[r * (W / 16) + i][j + 2]);
             }
-            ptx::named_barrier_sync(bar, kThreads);
+            ptx::named_barrier_sync(bar, Pol::GW * 32);
 #pragma unroll
             for (int k = 0; k < G / kHeadStep; ++k) {
                 const int h = k * kHeadStep + tid / (W / 2), d = 2 * (tid % (W / 2));
@@ -341,24 +361,24 @@ struct QuantConsumer {
                 for (int w = 0; w < Pol::NC; ++w)
 #pragma unroll
                     for (int c = 0; c < Pol::kMergeCols; c += G) {
-                        const float2 x = *reinterpret_cast<const float2*>(&sm.wacc[w][c + h][d]);
+                        const float2 x = *reinterpret_cast<const float2*>(&sm.wacc[half][w][c + h][d]);
                         s.x += x.x;
                         s.y += x.y;
                     }
-                const size_t at = static_cast<size_t>(h) * D + r * W + d;
+                const size_t at = static_cast<size_t>(h) * D + half * (D / Pol::SPLIT) + r * W + d;
                 if (slot < 0) {
                     const float inv = 1.0f / ls[k];
                     store_out2(p, out_base + at, s.x * inv, s.y * inv);
                 } else {
                     *reinterpret_cast<float2*>(p.ws_acc + static_cast<size_t>(slot) * G * D + at) = s;
-                    if (r == 0 && d == 0) {
+                    if (half == 0 && r == 0 && d == 0) {
                         float* ml = p.ws_ml + (static_cast<size_t>(slot) * G + h) * 2;
                         ml[0] = top[k];
                         ml[1] = ls[k];
                     }
                 }
             }
-            ptx::named_barrier_sync(bar, kThreads);   // wacc is filled again
+            ptx::named_barrier_sync(bar, Pol::GW * 32);   // wacc is filled again
         }
     }
 };
@@ -369,8 +389,10 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
                             const __grid_constant__ CUtensorMap tm_v, const DecodeQuantParams qp) {
     constexpr int G = Pol::G, D = Pol::D, SLOTS = Pol::SLOTS, NC = Pol::NC, RING = Pol::RING;
     constexpr int GROUPS = Pol::GROUPS;
-    constexpr int kLoads = NC / 2;             // consumer warps a producer serves
-    constexpr int kGroupThreads = NC * 32;     // consumers of a group
+    constexpr int SPLIT = Pol::SPLIT;
+    constexpr int kLoads = NC / 2;             // rings a producer fills
+    constexpr int kGroupThreads = Pol::GW * 32;   // consumers of a group
+    constexpr std::integral_constant<int, Pol::kExtra> kExtra{};
     constexpr uint32_t kTileBytes = QuantSmem<Pol>::kTileBytes;
     constexpr uint32_t kQBytes = G * D * 2;
     const DecodeParams& p = qp.d;
@@ -390,7 +412,7 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
         for (int g = 0; g < GROUPS; ++g) {
             for (int s = 0; s < SLOTS; ++s) {
                 ptx::mbar_init(ptx::smem_addr(&sm.group[g].full[s]), 2);   // the tiles' bytes, the scales
-                ptx::mbar_init(ptx::smem_addr(&sm.group[g].empty[s]), 1);
+                ptx::mbar_init(ptx::smem_addr(&sm.group[g].empty[s]), SPLIT);
             }
             ptx::mbar_init(ptx::smem_addr(&sm.group[g].q_full), 1);
             ptx::mbar_init(ptx::smem_addr(&sm.group[g].q_empty), 2);   // consumers, second producer
@@ -409,7 +431,7 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
     // (the plan's barriers make the lengths visible)
     for (int b = tid; b < B; b += blockDim.x)
         sm.len[b] = min(max(__ldg(p.seq_lens + b), 0), p.capacity);
-    build_plan<kQuantBlock>(pl, p, units, warp, lane, cta, kQuantBlock,
+    build_plan<kQuantBlock, Pol::kExtra>(pl, p, units, warp, lane, cta, kQuantBlock,
                             reinterpret_cast<uint32_t*>(&sm.kv[0][0][0][0]));
 
     // zeros for empty sequences and the segments' partial lists, as in decode_kernel.cuh
@@ -428,7 +450,7 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
                 const int b = u / KVH, kvh = u - b * KVH;
                 int4 e = make_int4(0, 0, 0, 0);
                 if (pl.n[b] != 0 && pl.g_eff > 0) {
-                    const SegmentParts sp(pl, b, kvh, p.dyn_slot_base);
+                    const SegmentParts sp(pl, b, kvh, p.dyn_slot_base, kExtra);
                     e = make_int4(sp.first_s, sp.ns_parts, sp.dk0, sp.nd_parts);
                 }
                 p.ws_segs[u] = e;
@@ -436,7 +458,7 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
         }
     }
     // this warp's group and its unit (a group without a unit has nothing to do)
-    const int group = warp < Pol::kConsumers ? warp / NC : (warp - Pol::kConsumers) / 2;
+    const int group = warp < Pol::kConsumers ? warp / Pol::GW : (warp - Pol::kConsumers) / 2;
     if (warp >= Pol::kWarps) return;
     const int unit = cta * GROUPS + group;
     if (unit >= pl.g_eff) return;
@@ -471,7 +493,7 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
                 if (!ok) break;
                 int claimed = -1;
                 Piece w;
-                if (!next_piece(pl, p, unit, kQuantBlock, dynamic, x, stop, claimed, w)) {
+                if (!next_piece<Pol::kExtra>(pl, p, unit, kQuantBlock, dynamic, x, stop, claimed, w)) {
                     gr.piece.done = 1;
                     ptx::mbar_arrive(q_full);
                     break;
@@ -484,7 +506,7 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
                 pc.lo = p.window > 0 && L > p.window ? L - p.window : 0;
                 pc.hi = L;
                 pc.slot = w.slot;
-                pc.parts = SegmentParts(pl, w.b, w.kvh, p.dyn_slot_base).count();
+                pc.parts = SegmentParts(pl, w.b, w.kvh, p.dyn_slot_base, kExtra).count();
                 pc.done = 0;
                 gr.piece = pc;
                 ptx::mbar_arrive_expect_tx(q_full, kQBytes);
@@ -575,7 +597,8 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
     // return; a warp whose wait gave up (or which saw the end) makes all of them leave at the
     // next one.
     QuantConsumer<Pol> c;
-    const int gwarp = warp - group * NC, gtid = gwarp * 32 + lane, bar = 1 + group;
+    const int gwarp = warp - group * Pol::GW, gtid = gwarp * 32 + lane, bar = 1 + group;
+    const int own = gwarp % NC, half = gwarp / NC;   // ring, part of D
     const uint32_t q_frag = ptx::smem_addr(&gr.q_frag[0][0]);
     uint32_t taken = 0;   // blocks this warp has processed (its ring's fills, in order)
     // In-kernel merge of a segment's partials: the group whose partial completes the count
@@ -585,7 +608,7 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
     int counted_b = 0, counted_kvh = 0;
     auto merge_counted = [&]() {   // every thread of the group, after the barrier that follows the flag
         if (!counted || !gr.merge_last) return;
-        const SegmentParts sp(pl, counted_b, counted_kvh, p.dyn_slot_base);
+        const SegmentParts sp(pl, counted_b, counted_kvh, p.dyn_slot_base, kExtra);
         const int u = counted_b * KVH + counted_kvh;
 #pragma unroll
         for (int i = 0; i < G * D / 2; i += kGroupThreads)   // two outputs per thread and turn
@@ -608,19 +631,42 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
         bool gone = false;
         // (counted from the piece's first block: which warp takes a block, and so the order of
         // the sums, does not depend on the pieces before)
-        for (int pos = pc.p0 + gwarp * kQuantBlock; pos < pc.p1; pos += NC * kQuantBlock) {
-            const int s = gwarp * RING + static_cast<int>(taken % RING);
+        for (int pos = pc.p0 + own * kQuantBlock; pos < pc.p1; pos += NC * kQuantBlock) {
+            const int s = own * RING + static_cast<int>(taken % RING);
             const uint32_t ph = (taken / RING) & 1u;
             gone = !__all_sync(0xffffffffu, wait_bounded(ptx::smem_addr(&gr.full[s]), ph, &sm.abort_flag, p.ws_flags));
-            if (gone) break;
             const uint32_t k_tile = kv_base + s * 2 * kTileBytes;
+            float z[4];
+            if (SPLIT == 1) {
+                if (gone) break;
+                c.scores(k_tile, q_frag, 0, z, lane);
+            } else {
+                // the halves of the scores cross over through this warp's part of the K tile,
+                // which it has read
+                const uint32_t mine = k_tile + half * (kTileBytes / SPLIT) + lane * 16;
+                const uint32_t other = k_tile + (1 - half) * (kTileBytes / SPLIT) + lane * 16;
+                if (!gone) {
+                    c.scores(k_tile, q_frag, half, z, lane);
+                    __syncwarp();
+                    ptx::sts128(mine, __float_as_uint(z[0]), __float_as_uint(z[1]),
+                                __float_as_uint(z[2]), __float_as_uint(z[3]));
+                }
+                gone = ptx::named_barrier_or(1 + Pol::GROUPS + group * NC + own, 2 * 32, gone);
+                if (gone) break;
+                const uint4 o = ptx::lds128(other);
+                z[0] += __uint_as_float(o.x);
+                z[1] += __uint_as_float(o.y);
+                z[2] += __uint_as_float(o.z);
+                z[3] += __uint_as_float(o.w);
+            }
             const float ks = gr.scales[s][0], vs = gr.scales[s][1];
             const bool bad = kPaged && gr.bad[s] != 0;
             const int first = pc.lo - pos, last = pc.hi - pos;
             if (first <= 0 && last >= kQuantBlock && !bad)
-                c.template block<true>(k_tile, k_tile + kTileBytes, ks, vs, 0, kQuantBlock, false, q_frag, lane);
+                c.template weigh<true>(z, k_tile + kTileBytes, ks, vs, 0, kQuantBlock, false, half, lane);
             else
-                c.template block<false>(k_tile, k_tile + kTileBytes, ks, vs, first, last, bad, q_frag, lane);
+                c.template weigh<false>(z, k_tile + kTileBytes, ks, vs, first, last, bad, half, lane);
+            if (SPLIT > 1) ptx::fence_proxy_async_smem();   // the scores, before the next copy
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&gr.empty[s]));
             ++taken;
@@ -633,15 +679,15 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
             ls += __shfl_xor_sync(0xffffffffu, ls, 4);
             ls += __shfl_xor_sync(0xffffffffu, ls, 8);
             ls += __shfl_xor_sync(0xffffffffu, ls, 16);
-            if (lane < 4) {
-                gr.wm[gwarp][2 * lane + j] = c.m[j];
-                gr.wl[gwarp][2 * lane + j] = ls;
+            if (half == 0 && lane < 4) {   // (the halves hold the same)
+                gr.wm[own][2 * lane + j] = c.m[j];
+                gr.wl[own][2 * lane + j] = ls;
             }
         }
         if (Pol::kMergeInKernel && gtid == 0) gr.merge_last = arrived;
         if (ptx::named_barrier_or(bar, kGroupThreads, gone)) break;
         const size_t out_base = (static_cast<size_t>(pc.b) * H + pc.kvh * G) * D;
-        c.merge(gr, p, out_base, pc.parts == 1 ? -1 : pc.slot, bar, gwarp, lane);
+        c.merge(gr, p, out_base, pc.parts == 1 ? -1 : pc.slot, bar, own, half, lane);
         if constexpr (Pol::kMergeInKernel) {
             // count the partial (the merge's last barrier is behind its stores); whether it was
             // the segment's last is looked at when the next piece ends
@@ -657,8 +703,8 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
     }
 }
 
-using QuantSliding = QuantPolicy<2, 256, 2, 3, false>;       // slidingDecodeGQA, many segments
-using QuantSlidingFew = QuantPolicy<2, 256, 2, 3, true>;     // slidingDecodeGQA, few segments
-using QuantGlobal = QuantPolicy<8, 512, 1, 3, false>;        // decodeGQA
+using QuantSliding = QuantPolicy<2, 256, 2, 1, 3, false>;       // slidingDecodeGQA, many segments
+using QuantSlidingFew = QuantPolicy<2, 256, 2, 1, 3, true>;     // slidingDecodeGQA, few segments
+using QuantGlobal = QuantPolicy<8, 512, 1, 2, 3, false>;        // decodeGQA
 
 }  // namespace gqa
