@@ -501,51 +501,94 @@ def gqa_prepare_decode_paged(q_raw: torch.Tensor, k_raw: torch.Tensor, v_raw, w_
     _check("gqa_prepare_decode_paged", st)
 
 
-def _check_quant_cache(k, v, k_scales, v_scales, B: int, block_table):
-    """Codes and scales of an 8-bit cache, contiguous (block_table None) or paged; returns
-    (KVH, D)."""
-    names = ("k", "v") if block_table is None else ("k_pages", "v_pages")
-    _check_tensor(names[0], k, torch.float8_e4m3fn, 4)
-    _check_tensor(names[1], v, torch.float8_e4m3fn, 4)
-    _require(v.shape == k.shape, f"{names[0]} and {names[1]} must have the same shape")
-    n, rows, KVH, D = k.shape
-    if block_table is None:
-        _require(n == B, f"{names[0]} must hold B sequences")
-        shape = (n, (rows + PAGE_SIZE - 1) // PAGE_SIZE, KVH)
+# The 8-bit cache calls are made once per layer and token, so their checks are written for
+# few attribute reads per tensor; whatever they do not pass is looked at again by
+# _check_tensor, whose error says what is wrong.
+
+def _check_args(ref, *specs) -> int:
+    """Check (name, tensor, dtype, ndim) specs against the device of the first tensor, `ref`;
+    returns that device's index."""
+    try:
+        dev = ref.get_device()
+        if dev >= 0:
+            for _, t, dtype, ndim in specs:
+                if not (t.dtype is dtype and t.get_device() == dev and t.dim() == ndim
+                        and t.is_contiguous()):
+                    break
+            else:
+                return dev
+    except AttributeError:
+        pass
+    for name, t, dtype, ndim in specs:
+        _check_tensor(name, t, dtype, ndim)
+    _same_device(ref, **{name: t for name, t, _, _ in specs})
+    raise ValueError("tensor arguments were refused")
+
+
+def _call_on(dev: int, stream, name: str, *args) -> None:
+    """lib.name(*args, stream) with device `dev` current; raises GQAError when it fails."""
+    fn = getattr(_lib or load_library(), name)
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(dev)
     else:
-        _check_tensor("block_table", block_table, torch.int32, 2)
+        handle = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, handle)
+    if st != GQA_OK:
+        raise GQAError(name, st)
+
+
+_E4M3 = torch.float8_e4m3fn
+_BF16 = torch.bfloat16
+
+
+def _cache_specs(k, v, k_scales, v_scales, block_table):
+    if block_table is None:
+        return (("k", k, _E4M3, 4), ("v", v, _E4M3, 4), ("k_scales", k_scales, torch.float32, 3),
+                ("v_scales", v_scales, torch.float32, 3))
+    return (("k_pages", k, _E4M3, 4), ("v_pages", v, _E4M3, 4),
+            ("k_scales", k_scales, torch.float32, 2), ("v_scales", v_scales, torch.float32, 2),
+            ("block_table", block_table, torch.int32, 2))
+
+
+def _cache_shape(k, v, k_scales, v_scales, B: int, block_table):
+    """(sequences or pages, rows, KVH, D) of an 8-bit cache whose tensors passed _check_args."""
+    n, rows, KVH, D = shape = k.shape
+    _require(v.shape == shape, "k and v must have the same shape")
+    if block_table is None:
+        _require(n == B, "the cache must hold B sequences")
+        want = (n, (rows + PAGE_SIZE - 1) // PAGE_SIZE, KVH)
+    else:
         _require(block_table.shape[0] == B, "block_table must have B rows")
-        shape = (n, KVH)
-    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
-        _check_tensor(name, t, torch.float32, len(shape))
-        _require(tuple(t.shape) == shape, f"{name} must be {list(shape)}")
-    return KVH, D
+        want = (n, KVH)
+    if k_scales.shape != want or v_scales.shape != want:
+        raise ValueError(f"k_scales and v_scales must be {list(want)}")
+    return n, rows, KVH, D
 
 
-def _append_quant(fn, k_new, v_new, token_offsets, block_table, seq_lens, k, v, k_scales, v_scales,
+def _append_quant(k_new, v_new, token_offsets, block_table, seq_lens, k, v, k_scales, v_scales,
                   stream):
-    _check_tensor("k_new", k_new, torch.bfloat16, 3)
-    _check_tensor("v_new", v_new, torch.bfloat16, 3)
-    _check_tensor("token_offsets", token_offsets, torch.int32, 1)
-    _check_tensor("seq_lens", seq_lens, torch.int32, 1)
+    dev = _check_args(k_new, ("k_new", k_new, _BF16, 3), ("v_new", v_new, _BF16, 3),
+                      ("token_offsets", token_offsets, torch.int32, 1),
+                      ("seq_lens", seq_lens, torch.int32, 1),
+                      *_cache_specs(k, v, k_scales, v_scales, block_table))
     B = seq_lens.shape[0]
-    KVH, D = _check_quant_cache(k, v, k_scales, v_scales, B, block_table)
+    n, rows, KVH, D = _cache_shape(k, v, k_scales, v_scales, B, block_table)
     _require(token_offsets.shape[0] == B + 1, "token_offsets must have B + 1 entries")
-    _require(v_new.shape == k_new.shape and tuple(k_new.shape[1:]) == (KVH, D),
+    N = k_new.shape[0]
+    _require(k_new.shape == (N, KVH, D) and v_new.shape == (N, KVH, D),
              "k_new / v_new must be [N, KVH, D]")
-    _same_device(k_new, v_new=v_new, token_offsets=token_offsets, block_table=block_table,
-                 seq_lens=seq_lens, k=k, v=v, k_scales=k_scales, v_scales=v_scales)
-    lib, N, n, rows = _lib_on(k_new.device), k_new.shape[0], k.shape[0], k.shape[1]
-    s = _stream_handle(stream, k_new.device)
-    cache = (_ptr(k), _ptr(v), _ptr(k_scales), _ptr(v_scales))
+    cache = (k.data_ptr(), v.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr())
     if block_table is None:
-        st = lib.gqa_append_quant(_ptr(k_new), _ptr(v_new), _ptr(token_offsets), _ptr(seq_lens), B,
-                                  N, rows, KVH, D, *cache, s)
+        _call_on(dev, stream, "gqa_append_quant", k_new.data_ptr(), v_new.data_ptr(),
+                 token_offsets.data_ptr(), seq_lens.data_ptr(), B, N, rows, KVH, D, *cache)
     else:
-        st = lib.gqa_append_quant_paged(_ptr(k_new), _ptr(v_new), _ptr(token_offsets),
-                                        _ptr(block_table), _ptr(seq_lens), B, N, n,
-                                        block_table.shape[1], rows, KVH, D, *cache, s)
-    _check(fn, st)
+        _call_on(dev, stream, "gqa_append_quant_paged", k_new.data_ptr(), v_new.data_ptr(),
+                 token_offsets.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), B, N, n,
+                 block_table.shape[1], rows, KVH, D, *cache)
 
 
 def gqa_append_quant(k_new: torch.Tensor, v_new: torch.Tensor, token_offsets: torch.Tensor,
@@ -554,8 +597,7 @@ def gqa_append_quant(k_new: torch.Tensor, v_new: torch.Tensor, token_offsets: to
     """Quantised append to a contiguous 8-bit cache: rows token_offsets[b] .. token_offsets[b+1]
     of k_new, v_new [N,KVH,D] (bf16) go to the last positions before seq_lens[b] of k, v
     [B,S,KVH,D] (float8_e4m3fn) with scales [B,ceil(S/16),KVH] (fp32)."""
-    _append_quant("gqa_append_quant", k_new, v_new, token_offsets, None, seq_lens, k, v, k_scales,
-                  v_scales, stream)
+    _append_quant(k_new, v_new, token_offsets, None, seq_lens, k, v, k_scales, v_scales, stream)
 
 
 def gqa_append_quant_paged(k_new: torch.Tensor, v_new: torch.Tensor, token_offsets: torch.Tensor,
@@ -564,37 +606,34 @@ def gqa_append_quant_paged(k_new: torch.Tensor, v_new: torch.Tensor, token_offse
                            v_scales: torch.Tensor, stream=None) -> None:
     """gqa_append_quant into page pools [P,16,KVH,D] with scales [P,KVH]."""
     _require(block_table is not None, "block_table is required")
-    _append_quant("gqa_append_quant_paged", k_new, v_new, token_offsets, block_table, seq_lens,
-                  k_pages, v_pages, k_scales, v_scales, stream)
+    _append_quant(k_new, v_new, token_offsets, block_table, seq_lens, k_pages, v_pages, k_scales,
+                  v_scales, stream)
 
 
-def _read_quant(fn, k, v, k_scales, v_scales, block_table, seq_lens, window, k_out, v_out,
-                out_rows, out_dtype, stream):
-    _check_tensor("seq_lens", seq_lens, torch.int32, 1)
+def _read_quant(k, v, k_scales, v_scales, block_table, seq_lens, window, k_out, v_out, out_rows,
+                out_dtype, stream):
+    dev = _check_args(k, ("seq_lens", seq_lens, torch.int32, 1),
+                      *_cache_specs(k, v, k_scales, v_scales, block_table))
     B = seq_lens.shape[0]
-    KVH, D = _check_quant_cache(k, v, k_scales, v_scales, B, block_table)
-    n, rows = k.shape[0], k.shape[1]
+    n, rows, KVH, D = _cache_shape(k, v, k_scales, v_scales, B, block_table)
     _require((k_out is None) == (v_out is None), "give both k_out and v_out, or neither")
     if k_out is None:
         if out_rows is None:
             out_rows = rows if block_table is None else block_table.shape[1] * rows
         k_out = torch.zeros((B, out_rows, KVH, D), dtype=out_dtype, device=k.device)
         v_out = torch.zeros_like(k_out)
-    _check_tensor("k_out", k_out, k_out.dtype, 4)
-    _check_tensor("v_out", v_out, k_out.dtype, 4)
-    _require(v_out.shape == k_out.shape and k_out.shape[0] == B and
-             tuple(k_out.shape[2:]) == (KVH, D), "k_out / v_out must be [B, rows, KVH, D]")
-    _same_device(k, v=v, k_scales=k_scales, v_scales=v_scales, block_table=block_table,
-                 seq_lens=seq_lens, k_out=k_out, v_out=v_out)
-    lib, s = _lib_on(k.device), _stream_handle(stream, k.device)
-    cache = (_ptr(k), _ptr(v), _ptr(k_scales), _ptr(v_scales))
-    tail = (int(window), _ptr(k_out), _ptr(v_out), k_out.shape[1], _out_code(k_out), s)
+    dtype = getattr(k_out, "dtype", None)
+    _check_args(k, ("k_out", k_out, dtype, 4), ("v_out", v_out, dtype, 4))
+    R = k_out.shape[1]
+    _require(k_out.shape == (B, R, KVH, D) and v_out.shape == (B, R, KVH, D),
+             "k_out / v_out must be [B, rows, KVH, D]")
+    cache = (k.data_ptr(), v.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr())
+    tail = (int(window), k_out.data_ptr(), v_out.data_ptr(), R, _out_code(k_out))
     if block_table is None:
-        st = lib.gqa_read_quant(*cache, _ptr(seq_lens), B, rows, KVH, D, *tail)
+        _call_on(dev, stream, "gqa_read_quant", *cache, seq_lens.data_ptr(), B, rows, KVH, D, *tail)
     else:
-        st = lib.gqa_read_quant_paged(*cache, _ptr(block_table), _ptr(seq_lens), B, n,
-                                      block_table.shape[1], rows, KVH, D, *tail)
-    _check(fn, st)
+        _call_on(dev, stream, "gqa_read_quant_paged", *cache, block_table.data_ptr(),
+                 seq_lens.data_ptr(), B, n, block_table.shape[1], rows, KVH, D, *tail)
     return k_out, v_out
 
 
@@ -606,8 +645,8 @@ def gqa_read_quant(k: torch.Tensor, v: torch.Tensor, k_scales: torch.Tensor,
     with row s = position s for the last `window` positions (0: all) of each sequence.  Other
     rows of given outputs are left as they are; new outputs (out_rows rows, default S) start
     at zero."""
-    return _read_quant("gqa_read_quant", k, v, k_scales, v_scales, None, seq_lens, window, k_out,
-                       v_out, out_rows, out_dtype, stream)
+    return _read_quant(k, v, k_scales, v_scales, None, seq_lens, window, k_out, v_out, out_rows,
+                       out_dtype, stream)
 
 
 def gqa_read_quant_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales: torch.Tensor,
@@ -617,39 +656,32 @@ def gqa_read_quant_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales:
                          out_dtype=torch.bfloat16, stream=None):
     """gqa_read_quant from page pools [P,16,KVH,D] with scales [P,KVH]."""
     _require(block_table is not None, "block_table is required")
-    return _read_quant("gqa_read_quant_paged", k_pages, v_pages, k_scales, v_scales, block_table,
-                       seq_lens, window, k_out, v_out, out_rows, out_dtype, stream)
+    return _read_quant(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, window, k_out,
+                       v_out, out_rows, out_dtype, stream)
 
 
-def _prepare_quant(fn, q_raw, k_raw, v_raw, w_q, w_k, block_table, seq_lens, q_out, k, v, k_scales,
+def _prepare_quant(q_raw, k_raw, v_raw, w_q, w_k, block_table, seq_lens, q_out, k, v, k_scales,
                    v_scales, stream):
-    _check_tensor("q_raw", q_raw, torch.bfloat16, 3)
-    _check_tensor("k_raw", k_raw, torch.bfloat16, 3)
-    _check_tensor("v_raw", v_raw, torch.bfloat16, 3)
-    _check_tensor("w_q", w_q, torch.bfloat16, 1)
-    _check_tensor("w_k", w_k, torch.bfloat16, 1)
-    _check_tensor("seq_lens", seq_lens, torch.int32, 1)
-    _check_tensor("q_out", q_out, torch.bfloat16, 3)
-    B, H, D = q_raw.shape
-    KVH, Dc = _check_quant_cache(k, v, k_scales, v_scales, B, block_table)
-    _require(Dc == D and tuple(k_raw.shape) == (B, KVH, D) and v_raw.shape == k_raw.shape,
+    dev = _check_args(q_raw, ("q_raw", q_raw, _BF16, 3), ("k_raw", k_raw, _BF16, 3),
+                      ("v_raw", v_raw, _BF16, 3), ("w_q", w_q, _BF16, 1), ("w_k", w_k, _BF16, 1),
+                      ("seq_lens", seq_lens, torch.int32, 1), ("q_out", q_out, _BF16, 3),
+                      *_cache_specs(k, v, k_scales, v_scales, block_table))
+    B, H, D = shape = q_raw.shape
+    n, rows, KVH, Dc = _cache_shape(k, v, k_scales, v_scales, B, block_table)
+    _require(Dc == D and k_raw.shape == (B, KVH, D) and v_raw.shape == (B, KVH, D),
              "k_raw / v_raw must be [B, KVH, D]")
-    _require(q_out.shape == q_raw.shape, "q_out must match q_raw")
+    _require(q_out.shape == shape, "q_out must match q_raw")
     _require(w_q.shape[0] == D and w_k.shape[0] == D, "w_q / w_k must be [D]")
     _require(seq_lens.shape[0] == B, "seq_lens must have B entries")
-    _same_device(q_raw, k_raw=k_raw, v_raw=v_raw, w_q=w_q, w_k=w_k, block_table=block_table,
-                 seq_lens=seq_lens, q_out=q_out, k=k, v=v, k_scales=k_scales, v_scales=v_scales)
-    lib, s = _lib_on(q_raw.device), _stream_handle(stream, q_raw.device)
-    head = (_ptr(q_raw), _ptr(k_raw), _ptr(v_raw), _ptr(w_q), _ptr(w_k))
-    cache = (_ptr(k), _ptr(v), _ptr(k_scales), _ptr(v_scales))
+    head = (q_raw.data_ptr(), k_raw.data_ptr(), v_raw.data_ptr(), w_q.data_ptr(), w_k.data_ptr())
+    cache = (k.data_ptr(), v.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr())
     if block_table is None:
-        st = lib.gqa_prepare_decode_quant(*head, _ptr(seq_lens), B, H, KVH, D, _ptr(q_out), *cache,
-                                          k.shape[1], s)
+        _call_on(dev, stream, "gqa_prepare_decode_quant", *head, seq_lens.data_ptr(), B, H, KVH, D,
+                 q_out.data_ptr(), *cache, rows)
     else:
-        st = lib.gqa_prepare_decode_quant_paged(*head, _ptr(block_table), _ptr(seq_lens), B,
-                                                k.shape[0], block_table.shape[1], k.shape[1], H,
-                                                KVH, D, _ptr(q_out), *cache, s)
-    _check(fn, st)
+        _call_on(dev, stream, "gqa_prepare_decode_quant_paged", *head, block_table.data_ptr(),
+                 seq_lens.data_ptr(), B, n, block_table.shape[1], rows, H, KVH, D,
+                 q_out.data_ptr(), *cache)
 
 
 def gqa_prepare_decode_quant(q_raw: torch.Tensor, k_raw: torch.Tensor, v_raw: torch.Tensor,
@@ -658,8 +690,8 @@ def gqa_prepare_decode_quant(q_raw: torch.Tensor, k_raw: torch.Tensor, v_raw: to
                              k_scales: torch.Tensor, v_scales: torch.Tensor, stream=None) -> None:
     """gqa_prepare_decode into a contiguous 8-bit cache k, v [B,S,KVH,D] (float8_e4m3fn) with
     scales [B,ceil(S/16),KVH]: position seq_lens[b] - 1."""
-    _prepare_quant("gqa_prepare_decode_quant", q_raw, k_raw, v_raw, w_q, w_k, None, seq_lens, q_out,
-                   k, v, k_scales, v_scales, stream)
+    _prepare_quant(q_raw, k_raw, v_raw, w_q, w_k, None, seq_lens, q_out, k, v, k_scales, v_scales,
+                   stream)
 
 
 def gqa_prepare_decode_quant_paged(q_raw: torch.Tensor, k_raw: torch.Tensor, v_raw: torch.Tensor,
@@ -670,34 +702,34 @@ def gqa_prepare_decode_quant_paged(q_raw: torch.Tensor, k_raw: torch.Tensor, v_r
                                    stream=None) -> None:
     """gqa_prepare_decode_quant into page pools [P,16,KVH,D] with scales [P,KVH]."""
     _require(block_table is not None, "block_table is required")
-    _prepare_quant("gqa_prepare_decode_quant_paged", q_raw, k_raw, v_raw, w_q, w_k, block_table,
-                   seq_lens, q_out, k_pages, v_pages, k_scales, v_scales, stream)
+    _prepare_quant(q_raw, k_raw, v_raw, w_q, w_k, block_table, seq_lens, q_out, k_pages, v_pages,
+                   k_scales, v_scales, stream)
 
 
-def _decode_quant(fn, q, k, v, k_scales, v_scales, block_table, seq_lens, window, out, out_dtype,
+def _decode_quant(q, k, v, k_scales, v_scales, block_table, seq_lens, window, out, out_dtype,
                   workspace, stream):
-    _check_tensor("q", q, torch.bfloat16, 3)
-    _check_tensor("seq_lens", seq_lens, torch.int32, 1)
-    B, H, D = q.shape
-    KVH, Dc = _check_quant_cache(k, v, k_scales, v_scales, B, block_table)
+    dev = _check_args(q, ("q", q, _BF16, 3), ("seq_lens", seq_lens, torch.int32, 1),
+                      *_cache_specs(k, v, k_scales, v_scales, block_table))
+    B, H, D = shape = q.shape
+    n, rows, KVH, Dc = _cache_shape(k, v, k_scales, v_scales, B, block_table)
     _require(Dc == D, "q and the cache must have the same head size")
     _require(seq_lens.shape[0] == B, "seq_lens must have B entries")
     if out is None:
-        out = torch.empty((B, H, D), dtype=out_dtype, device=q.device)
-    _check_tensor("out", out, out.dtype, 3)
-    _require(tuple(out.shape) == (B, H, D), "out must be [B, H, D]")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _same_device(q, k=k, v=v, k_scales=k_scales, v_scales=v_scales, block_table=block_table,
-                 seq_lens=seq_lens, out=out, workspace=workspace)
-    lib, s = _lib_on(q.device), _stream_handle(stream, q.device)
-    head = (_ptr(q), _ptr(k), _ptr(v), _ptr(k_scales), _ptr(v_scales))
-    tail = (H, KVH, D, int(window), _ptr(out), _out_code(out), _ptr(workspace), ws_bytes, s)
-    if block_table is None:
-        st = lib.gqa_decode_quant(*head, _ptr(seq_lens), B, k.shape[1], *tail)
+        out = torch.empty(shape, dtype=out_dtype, device=q.device)
     else:
-        st = lib.gqa_decode_quant_paged(*head, _ptr(block_table), _ptr(seq_lens), B, k.shape[0],
-                                        block_table.shape[1], k.shape[1], *tail)
-    _check(fn, st)
+        _check_args(q, ("out", out, getattr(out, "dtype", None), 3))
+        _require(out.shape == shape, "out must be [B, H, D]")
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        _same_device(q, workspace=workspace)
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    head = (q.data_ptr(), k.data_ptr(), v.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr())
+    tail = (H, KVH, D, int(window), out.data_ptr(), _out_code(out), ws, ws_bytes)
+    if block_table is None:
+        _call_on(dev, stream, "gqa_decode_quant", *head, seq_lens.data_ptr(), B, rows, *tail)
+    else:
+        _call_on(dev, stream, "gqa_decode_quant_paged", *head, block_table.data_ptr(),
+                 seq_lens.data_ptr(), B, n, block_table.shape[1], rows, *tail)
     return out
 
 
@@ -707,8 +739,8 @@ def gqa_decode_quant(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_scales
                      workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """gqa_decode over a contiguous 8-bit cache: q [B,H,D] (bf16), k/v [B,S,KVH,D]
     (float8_e4m3fn), scales [B,ceil(S/16),KVH] (fp32), seq_lens int32 [B]."""
-    return _decode_quant("gqa_decode_quant", q, k, v, k_scales, v_scales, None, seq_lens, window,
-                         out, out_dtype, workspace, stream)
+    return _decode_quant(q, k, v, k_scales, v_scales, None, seq_lens, window, out, out_dtype,
+                         workspace, stream)
 
 
 def gqa_decode_quant_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -718,8 +750,8 @@ def gqa_decode_quant_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torc
                            workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """gqa_decode_quant over page pools [P,16,KVH,D] with scales [P,KVH]."""
     _require(block_table is not None, "block_table is required")
-    return _decode_quant("gqa_decode_quant_paged", q, k_pages, v_pages, k_scales, v_scales,
-                         block_table, seq_lens, window, out, out_dtype, workspace, stream)
+    return _decode_quant(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, window,
+                         out, out_dtype, workspace, stream)
 
 
 def gqa_decode_noalloc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_lens: torch.Tensor,
