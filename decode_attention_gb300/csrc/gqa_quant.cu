@@ -109,8 +109,9 @@ gqa_status_t run_append(const void* k_new, const void* v_new, const int32_t* tok
     p.N = N;
     // n tokens touch at most (n + 14) / 16 + 1 blocks
     const uint64_t blocks = static_cast<uint64_t>(N) / gqa::kQuantBlock + 2u * static_cast<uint64_t>(B);
-    const uint64_t warps = blocks * 2 * static_cast<uint64_t>(cache.KVH);
-    const dim3 grid(clamp_grid((warps + 7) / 8, 2, sms));
+    const uint64_t items = blocks * 2 * static_cast<uint64_t>(cache.KVH);
+    const uint64_t per_cta = gqa::kAppendThreads / 32 / (D / 256);
+    const dim3 grid(clamp_grid((items + per_cta - 1) / per_cta, 2, sms));
     return D == 256 ? launch(gqa::gqa_append_quant_kernel<256>, p, grid, gqa::kAppendThreads, stream)
                     : launch(gqa::gqa_append_quant_kernel<512>, p, grid, gqa::kAppendThreads, stream);
 }
@@ -148,8 +149,8 @@ gqa_status_t run_read(const gqa::QuantCache& cache, const int32_t* seq_lens, int
     p.out_rows = out_rows;
     int most = cache.capacity() < out_rows ? cache.capacity() : out_rows;
     if (window > 0 && window < most) most = window;
-    const uint64_t blocks = static_cast<uint64_t>(B) * (most / gqa::kQuantBlock + 2) * 2;
-    const dim3 grid(clamp_grid(blocks, 8, sms));
+    const uint64_t items = static_cast<uint64_t>(B) * (most / gqa::kQuantBlock + 2) * 2 * 4;
+    const dim3 grid(clamp_grid(items, 8, sms));
     const bool f32 = out_dtype == GQA_OUT_F32;
     if (cache.KVH == 16)
         return f32 ? launch(gqa::gqa_read_quant_kernel<16, 256, true>, p, grid, gqa::kReadThreads, stream)

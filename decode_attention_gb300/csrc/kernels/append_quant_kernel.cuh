@@ -1,11 +1,14 @@
 // Quantising K/V rows into the 8-bit cache (quant_cache.cuh) as they are written.
 //
 // The new rows of sequence b are the packed tokens [off_b, off_{b+1}); they go to the
-// positions [L_b - n_b, L_b).  A warp takes one block of 16 positions of one KV head of K
-// or V: it loads the block's new rows once (each lane 16 bytes of a row at a time), takes
-// the largest magnitude, and writes the codes and the scale.  In a block that holds
-// earlier rows of the sequence the scale never shrinks; when it grows the earlier rows
-// are re-coded.  Rows behind the last new one are left as they are.
+// positions [L_b - n_b, L_b).  One item is a block of 16 positions of one KV head of K or V:
+// its new rows are loaded once into registers (16 bytes of a row per lane), the largest
+// magnitude is taken, and the codes and the scale are written.  D / 256 warps share an
+// item, 16 / (D / 256) rows each, so that a lane holds 64 registers of data at both head
+// sizes and 16 warps fit an SM (one warp per item at D = 512 needs 171 registers and left 8
+// warps: append_chunks_b32_paged 97.6 us).  In a block that holds earlier rows of the
+// sequence the scale never shrinks; when it grows the earlier rows are re-coded.  Rows
+// behind the last new one are left as they are.
 #pragma once
 
 #include "quant_cache.cuh"
@@ -24,16 +27,21 @@ struct AppendQuantParams {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kAppendThreads)
+__global__ void __launch_bounds__(kAppendThreads, 2)
     gqa_append_quant_kernel(const AppendQuantParams p) {
-    constexpr int kVec = D / 256;   // 16-byte loads per lane and row
+    constexpr int kWarps = kAppendThreads / 32;
+    constexpr int kShare = D / 256;               // warps per item
+    constexpr int kRows = kQuantBlock / kShare;   // block rows per warp
+    constexpr int kItems = kWarps / kShare;       // items a CTA works on at a time
     __shared__ BlockIndex idx;
+    __shared__ uint32_t top[2][kWarps];           // [turn parity]: largest magnitude of each warp
 
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
 
     const QuantCache& c = p.cache;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int sub = warp % kShare, slot = warp / kShare;
     const int capacity = c.capacity();
     // blocks of positions that sequence b writes; 0 when its offsets or length do not fit
     idx.build(p.B, [&](int b) {
@@ -42,11 +50,25 @@ __global__ void __launch_bounds__(kAppendThreads)
         return (L - 1) / kQuantBlock - (L - (o1 - o0)) / kQuantBlock + 1;
     });
     const uint32_t per_block = 2u * c.KVH;   // K heads, then V heads
-    const uint32_t items = idx.pref[p.B];
-    const uint64_t total = static_cast<uint64_t>(items) * per_block;
+    const uint64_t total = static_cast<uint64_t>(idx.pref[p.B]) * per_block;
+    uint32_t turn = 0;
+    // the largest of the sharing warps' values (the other parity is written next, after this
+    // exchange's barrier)
+    auto share_max = [&](uint32_t m) {
+        m = __reduce_max_sync(0xffffffffu, m);
+        if constexpr (kShare > 1) {
+            uint32_t* t = top[turn & 1u];
+            ++turn;
+            if (lane == 0) t[warp] = m;
+            ptx::named_barrier_sync(1 + slot, 32 * kShare);
+#pragma unroll
+            for (int i = 0; i < kShare; ++i) m = max(m, t[slot * kShare + i]);
+        }
+        return m;
+    };
 
-    for (uint64_t it = static_cast<uint64_t>(blockIdx.x) * (kAppendThreads / 32) + warp; it < total;
-         it += static_cast<uint64_t>(gridDim.x) * (kAppendThreads / 32)) {
+    for (uint64_t it = static_cast<uint64_t>(blockIdx.x) * kItems + slot; it < total;
+         it += static_cast<uint64_t>(gridDim.x) * kItems) {
         const uint32_t x = static_cast<uint32_t>(it / per_block);
         const int th = static_cast<int>(it - static_cast<uint64_t>(x) * per_block);
         const bool is_v = th >= c.KVH;
@@ -61,61 +83,62 @@ __global__ void __launch_bounds__(kAppendThreads)
         size_t row, scale_row;
         if (!c.locate(b, blk, &row, &scale_row)) continue;
 
-        const __nv_bfloat16* src =
-            (is_v ? p.v_new : p.k_new) +
-            (static_cast<size_t>(o0 + base - start + j0) * c.KVH + kvh) * D + lane * 8;
+        // this warp's rows: sub, sub + kShare, ... of the block
+        const size_t stride = static_cast<size_t>(c.KVH) * D;
+        const __nv_bfloat16* src = (is_v ? p.v_new : p.k_new) +
+                                   (static_cast<int64_t>(o0) + base - start) * static_cast<int64_t>(stride) +
+                                   static_cast<size_t>(kvh) * D + lane * 8;
         uint8_t* dst = (is_v ? c.v : c.k) + (row * c.KVH + kvh) * D + lane * 8;
         float* scale = (is_v ? c.v_scales : c.k_scales) + scale_row * c.KVH + kvh;
-        const size_t stride = static_cast<size_t>(c.KVH) * D;
 
-        uint4 w[kQuantBlock][kVec];
+        uint4 w[kRows][kShare];
 #pragma unroll
-        for (int j = 0; j < kQuantBlock; ++j)
+        for (int i = 0; i < kRows; ++i)
 #pragma unroll
-            for (int q = 0; q < kVec; ++q) {
-                w[j][q] = make_uint4(0, 0, 0, 0);
-                if (j < j1 - j0)
-                    w[j][q] = __ldcs(reinterpret_cast<const uint4*>(src + j * stride + q * 256));
+            for (int q = 0; q < kShare; ++q) {
+                const int j = i * kShare + sub;
+                w[i][q] = make_uint4(0, 0, 0, 0);
+                if (j >= j0 && j < j1)
+                    w[i][q] = __ldcs(reinterpret_cast<const uint4*>(src + j * stride + q * 256));
             }
         const float old = j0 > 0 ? *scale : 0.0f;
         // largest magnitude: the bits of |bf16| order like the values, NaN above infinity
-        uint32_t m = 0;
+        uint32_t m2 = 0;
 #pragma unroll
-        for (int j = 0; j < kQuantBlock; ++j)
+        for (int i = 0; i < kRows; ++i)
 #pragma unroll
-            for (int q = 0; q < kVec; ++q) {
-                m = __vmaxu2(m, w[j][q].x & 0x7fff7fffu);
-                m = __vmaxu2(m, w[j][q].y & 0x7fff7fffu);
-                m = __vmaxu2(m, w[j][q].z & 0x7fff7fffu);
-                m = __vmaxu2(m, w[j][q].w & 0x7fff7fffu);
+            for (int q = 0; q < kShare; ++q) {
+                m2 = __vmaxu2(m2, w[i][q].x & 0x7fff7fffu);
+                m2 = __vmaxu2(m2, w[i][q].y & 0x7fff7fffu);
+                m2 = __vmaxu2(m2, w[i][q].z & 0x7fff7fffu);
+                m2 = __vmaxu2(m2, w[i][q].w & 0x7fff7fffu);
             }
-        m = max(m & 0xffffu, m >> 16);
-        m = __reduce_max_sync(0xffffffffu, m);
+        uint32_t m = share_max(max(m2 & 0xffffu, m2 >> 16));
         const bool non_finite = m >= 0x7f80u;
         if (non_finite) {   // the largest finite one instead
             m = 0;
 #pragma unroll
-            for (int j = 0; j < kQuantBlock; ++j)
+            for (int i = 0; i < kRows; ++i)
 #pragma unroll
-                for (int q = 0; q < kVec; ++q) {
-                    const uint32_t u[4] = {w[j][q].x, w[j][q].y, w[j][q].z, w[j][q].w};
+                for (int q = 0; q < kShare; ++q) {
+                    const uint32_t u[4] = {w[i][q].x, w[i][q].y, w[i][q].z, w[i][q].w};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t lo = u[i] & 0x7fffu, hi = (u[i] >> 16) & 0x7fffu;
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t lo = u[e] & 0x7fffu, hi = (u[e] >> 16) & 0x7fffu;
                         m = max(m, lo < 0x7f80u ? lo : 0u);
                         m = max(m, hi < 0x7f80u ? hi : 0u);
                     }
                 }
-            m = __reduce_max_sync(0xffffffffu, m);
+            m = share_max(m);
         }
         int e = quant_exponent(__uint_as_float(m << 16));
         if (j0 > 0) {
             const int eo = scale_exponent(old);
             if (e > eo) {
                 const float f = pow2f(max(eo - e, -126));
-                for (int j = 0; j < j0; ++j)
+                for (int j = sub; j < j0; j += kShare)
 #pragma unroll
-                    for (int q = 0; q < kVec; ++q) {
+                    for (int q = 0; q < kShare; ++q) {
                         uint2* r = reinterpret_cast<uint2*>(dst + j * stride + q * 256);
                         const uint2 t = *r;
                         *r = make_uint2(recode4(t.x, f), recode4(t.y, f));
@@ -126,28 +149,30 @@ __global__ void __launch_bounds__(kAppendThreads)
         }
         const float inv = pow2f(-e);
 #pragma unroll
-        for (int j = 0; j < kQuantBlock; ++j) {
-            if (j >= j1 - j0) break;
+        for (int i = 0; i < kRows; ++i) {
+            const int j = i * kShare + sub;
+            if (j < j0 || j >= j1) continue;
 #pragma unroll
-            for (int q = 0; q < kVec; ++q) {
-                const uint32_t u[4] = {w[j][q].x, w[j][q].y, w[j][q].z, w[j][q].w};
+            for (int q = 0; q < kShare; ++q) {
+                const uint32_t u[4] = {w[i][q].x, w[i][q].y, w[i][q].z, w[i][q].w};
                 uint16_t o[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float lo = __uint_as_float(u[i] << 16) * inv;
-                    float hi = __uint_as_float(u[i] & 0xffff0000u) * inv;
+                for (int k = 0; k < 4; ++k) {
+                    float lo = __uint_as_float(u[k] << 16) * inv;
+                    float hi = __uint_as_float(u[k] & 0xffff0000u) * inv;
                     if (non_finite) {
                         lo = inf_to_nan(lo);
                         hi = inf_to_nan(hi);
                     }
-                    o[i] = ptx::float2_to_e4m3x2(lo, hi);
+                    o[k] = ptx::float2_to_e4m3x2(lo, hi);
                 }
-                *reinterpret_cast<uint2*>(dst + (j0 + j) * stride + q * 256) =
-                    make_uint2(o[0] | (static_cast<uint32_t>(o[1]) << 16),
-                               o[2] | (static_cast<uint32_t>(o[3]) << 16));
+                __stcs(reinterpret_cast<uint2*>(dst + j * stride + q * 256),
+                       make_uint2(o[0] | (static_cast<uint32_t>(o[1]) << 16),
+                                  o[2] | (static_cast<uint32_t>(o[3]) << 16)));
             }
         }
-        if (lane == 0) *scale = pow2f(e);
+        // (the sharing warps have all read the old scale: each did before the exchange)
+        if (sub == 0 && lane == 0) *scale = pow2f(e);
     }
 }
 

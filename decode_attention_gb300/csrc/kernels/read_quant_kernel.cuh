@@ -2,8 +2,8 @@
 // positions s in [lo_b, min(L_b, out_rows)), in bf16 (exact: 4 significant bits, exponents
 // within range) or fp32.  Other rows of the output are left as they are.
 //
-// A CTA takes one block of 16 positions of K or V, 16 * KVH * D contiguous codes; a
-// thread converts 8 codes at a time.
+// A CTA takes a quarter of a block of 16 positions of K or V (16 * KVH * D contiguous
+// codes); a thread loads all of its codes, 8 at a time, before it converts them.
 #pragma once
 
 #include "quant_cache.cuh"
@@ -24,7 +24,8 @@ template <int KVH, int D, bool kF32>
 __global__ void __launch_bounds__(kReadThreads)
     gqa_read_quant_kernel(const ReadQuantParams p) {
     constexpr int kRow = KVH * D;                                 // codes per position
-    constexpr int kSteps = kQuantBlock * kRow / (8 * kReadThreads);
+    constexpr int kParts = 4;                                     // items per block
+    constexpr int kSteps = kQuantBlock * kRow / (8 * kReadThreads) / kParts;
     __shared__ BlockIndex idx;
 
     ptx::grid_dependency_wait();
@@ -42,11 +43,13 @@ __global__ void __launch_bounds__(kReadThreads)
         const int hi = range(b, &lo);
         return hi > lo ? (hi - 1) / kQuantBlock - lo / kQuantBlock + 1 : 0;
     });
-    const uint32_t total = 2u * idx.pref[p.B];   // <= 2 * 256 * 2^14 blocks
+    const uint32_t total = 2u * kParts * idx.pref[p.B];   // <= 2 * 4 * 256 * 2^14
 
     for (uint32_t it = blockIdx.x; it < total; it += gridDim.x) {
-        const bool is_v = it & 1u;
-        const uint32_t x = it >> 1;
+        const uint32_t x = it / (2u * kParts), sub = it % (2u * kParts);
+        const bool is_v = sub >= kParts;
+        const int at0 = static_cast<int>(sub % kParts) * (kQuantBlock * kRow / kParts) +
+                        static_cast<int>(threadIdx.x) * 8;
         const int b = idx.seq_of(p.B, x);
         int lo;
         const int hi = range(b, &lo);
@@ -57,12 +60,18 @@ __global__ void __launch_bounds__(kReadThreads)
         const uint8_t* src = (is_v ? c.v : c.k) + row * kRow;
         const float* scale = (is_v ? c.v_scales : c.k_scales) + scale_row * KVH;
         const size_t out0 = (static_cast<size_t>(b) * p.out_rows + base) * kRow;
-#pragma unroll 4
+        uint2 codes[kSteps];
+#pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-            const int at = (s * kReadThreads + static_cast<int>(threadIdx.x)) * 8;
-            const int pos = base + at / kRow;
+            const int at = at0 + s * kReadThreads * 8, pos = base + at / kRow;
+            codes[s] = make_uint2(0, 0);
+            if (pos >= lo && pos < hi) codes[s] = __ldcs(reinterpret_cast<const uint2*>(src + at));
+        }
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            const int at = at0 + s * kReadThreads * 8, pos = base + at / kRow;
             if (pos < lo || pos >= hi) continue;
-            const uint2 w = __ldcs(reinterpret_cast<const uint2*>(src + at));
+            const uint2 w = codes[s];
             const float f = pow2f(scale_exponent(__ldg(scale + (at % kRow) / D)));
             float2 v[4] = {ptx::e4m3x2_to_float2(static_cast<uint16_t>(w.x)),
                            ptx::e4m3x2_to_float2(static_cast<uint16_t>(w.x >> 16)),
