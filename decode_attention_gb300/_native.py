@@ -502,27 +502,27 @@ def gqa_prepare_decode_paged(q_raw: torch.Tensor, k_raw: torch.Tensor, v_raw, w_
 
 
 # The 8-bit cache calls are made once per layer and token, so their checks are written for
-# few attribute reads per tensor; whatever they do not pass is looked at again by
-# _check_tensor, whose error says what is wrong.
+# few attribute reads per tensor; what they do not pass is looked at again by _refuse, whose
+# error says what is wrong.
 
-def _check_args(ref, *specs) -> int:
-    """Check (name, tensor, dtype, ndim) specs against the device of the first tensor, `ref`;
-    returns that device's index."""
-    try:
-        dev = ref.get_device()
-        if dev >= 0:
-            for _, t, dtype, ndim in specs:
-                if not (t.dtype is dtype and t.get_device() == dev and t.dim() == ndim
-                        and t.is_contiguous()):
-                    break
-            else:
-                return dev
-    except AttributeError:
-        pass
+def _all_on(dev: int, dtype, *tensors) -> bool:
+    """Whether every tensor is contiguous, of this dtype and on CUDA device `dev`."""
+    for t in tensors:
+        if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+            return False
+    return True
+
+
+def _refuse(ref, *specs):
+    """Raise the error of the first (name, tensor, dtype, ndim) that is not as it should be."""
     for name, t, dtype, ndim in specs:
         _check_tensor(name, t, dtype, ndim)
     _same_device(ref, **{name: t for name, t, _, _ in specs})
-    raise ValueError("tensor arguments were refused")
+    raise ValueError("tensor shapes do not fit together")
+
+
+def _device_of(t) -> int:
+    return t.get_device() if isinstance(t, torch.Tensor) else -1
 
 
 def _call_on(dev: int, stream, name: str, *args) -> None:
@@ -554,8 +554,16 @@ def _cache_specs(k, v, k_scales, v_scales, block_table):
             ("block_table", block_table, torch.int32, 2))
 
 
+def _cache_on(dev: int, k, v, k_scales, v_scales, block_table) -> bool:
+    """Device, dtype and number of dims of an 8-bit cache's tensors."""
+    return (_all_on(dev, _E4M3, k, v) and _all_on(dev, torch.float32, k_scales, v_scales)
+            and k.dim() == 4
+            and (block_table is None
+                 or (_all_on(dev, torch.int32, block_table) and block_table.dim() == 2)))
+
+
 def _cache_shape(k, v, k_scales, v_scales, B: int, block_table):
-    """(sequences or pages, rows, KVH, D) of an 8-bit cache whose tensors passed _check_args."""
+    """(sequences or pages, rows, KVH, D) of an 8-bit cache that passed _cache_on."""
     n, rows, KVH, D = shape = k.shape
     _require(v.shape == shape, "k and v must have the same shape")
     if block_table is None:
@@ -571,16 +579,24 @@ def _cache_shape(k, v, k_scales, v_scales, B: int, block_table):
 
 def _append_quant(k_new, v_new, token_offsets, block_table, seq_lens, k, v, k_scales, v_scales,
                   stream):
-    dev = _check_args(k_new, ("k_new", k_new, _BF16, 3), ("v_new", v_new, _BF16, 3),
-                      ("token_offsets", token_offsets, torch.int32, 1),
-                      ("seq_lens", seq_lens, torch.int32, 1),
-                      *_cache_specs(k, v, k_scales, v_scales, block_table))
+    dev = _device_of(k_new)
+    try:
+        ok = (dev >= 0 and _all_on(dev, _BF16, k_new, v_new) and k_new.dim() == 3
+              and _all_on(dev, torch.int32, token_offsets, seq_lens) and seq_lens.dim() == 1
+              and _cache_on(dev, k, v, k_scales, v_scales, block_table))
+    except AttributeError:
+        ok = False
+    if not ok:
+        _refuse(k_new, ("k_new", k_new, _BF16, 3), ("v_new", v_new, _BF16, 3),
+                ("token_offsets", token_offsets, torch.int32, 1),
+                ("seq_lens", seq_lens, torch.int32, 1),
+                *_cache_specs(k, v, k_scales, v_scales, block_table))
     B = seq_lens.shape[0]
     n, rows, KVH, D = _cache_shape(k, v, k_scales, v_scales, B, block_table)
-    _require(token_offsets.shape[0] == B + 1, "token_offsets must have B + 1 entries")
-    N = k_new.shape[0]
-    _require(k_new.shape == (N, KVH, D) and v_new.shape == (N, KVH, D),
-             "k_new / v_new must be [N, KVH, D]")
+    _require(token_offsets.shape == (B + 1,), "token_offsets must have B + 1 entries")
+    shape = k_new.shape
+    N = shape[0]
+    _require(shape == (N, KVH, D) and v_new.shape == shape, "k_new / v_new must be [N, KVH, D]")
     cache = (k.data_ptr(), v.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr())
     if block_table is None:
         _call_on(dev, stream, "gqa_append_quant", k_new.data_ptr(), v_new.data_ptr(),
@@ -612,8 +628,15 @@ def gqa_append_quant_paged(k_new: torch.Tensor, v_new: torch.Tensor, token_offse
 
 def _read_quant(k, v, k_scales, v_scales, block_table, seq_lens, window, k_out, v_out, out_rows,
                 out_dtype, stream):
-    dev = _check_args(k, ("seq_lens", seq_lens, torch.int32, 1),
-                      *_cache_specs(k, v, k_scales, v_scales, block_table))
+    dev = _device_of(k)
+    try:
+        ok = (dev >= 0 and _all_on(dev, torch.int32, seq_lens) and seq_lens.dim() == 1
+              and _cache_on(dev, k, v, k_scales, v_scales, block_table))
+    except AttributeError:
+        ok = False
+    if not ok:
+        _refuse(k, ("seq_lens", seq_lens, torch.int32, 1),
+                *_cache_specs(k, v, k_scales, v_scales, block_table))
     B = seq_lens.shape[0]
     n, rows, KVH, D = _cache_shape(k, v, k_scales, v_scales, B, block_table)
     _require((k_out is None) == (v_out is None), "give both k_out and v_out, or neither")
@@ -623,9 +646,14 @@ def _read_quant(k, v, k_scales, v_scales, block_table, seq_lens, window, k_out, 
         k_out = torch.zeros((B, out_rows, KVH, D), dtype=out_dtype, device=k.device)
         v_out = torch.zeros_like(k_out)
     dtype = getattr(k_out, "dtype", None)
-    _check_args(k, ("k_out", k_out, dtype, 4), ("v_out", v_out, dtype, 4))
+    try:
+        ok = _all_on(dev, dtype, k_out, v_out) and k_out.dim() == 4
+    except AttributeError:
+        ok = False
+    if not ok:
+        _refuse(k, ("k_out", k_out, dtype, 4), ("v_out", v_out, dtype, 4))
     R = k_out.shape[1]
-    _require(k_out.shape == (B, R, KVH, D) and v_out.shape == (B, R, KVH, D),
+    _require(k_out.shape == (B, R, KVH, D) and v_out.shape == k_out.shape,
              "k_out / v_out must be [B, rows, KVH, D]")
     cache = (k.data_ptr(), v.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr())
     tail = (int(window), k_out.data_ptr(), v_out.data_ptr(), R, _out_code(k_out))
@@ -662,17 +690,25 @@ def gqa_read_quant_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales:
 
 def _prepare_quant(q_raw, k_raw, v_raw, w_q, w_k, block_table, seq_lens, q_out, k, v, k_scales,
                    v_scales, stream):
-    dev = _check_args(q_raw, ("q_raw", q_raw, _BF16, 3), ("k_raw", k_raw, _BF16, 3),
-                      ("v_raw", v_raw, _BF16, 3), ("w_q", w_q, _BF16, 1), ("w_k", w_k, _BF16, 1),
-                      ("seq_lens", seq_lens, torch.int32, 1), ("q_out", q_out, _BF16, 3),
-                      *_cache_specs(k, v, k_scales, v_scales, block_table))
+    dev = _device_of(q_raw)
+    try:
+        ok = (dev >= 0 and _all_on(dev, _BF16, q_raw, k_raw, v_raw, w_q, w_k, q_out)
+              and q_raw.dim() == 3 and _all_on(dev, torch.int32, seq_lens)
+              and _cache_on(dev, k, v, k_scales, v_scales, block_table))
+    except AttributeError:
+        ok = False
+    if not ok:
+        _refuse(q_raw, ("q_raw", q_raw, _BF16, 3), ("k_raw", k_raw, _BF16, 3),
+                ("v_raw", v_raw, _BF16, 3), ("w_q", w_q, _BF16, 1), ("w_k", w_k, _BF16, 1),
+                ("seq_lens", seq_lens, torch.int32, 1), ("q_out", q_out, _BF16, 3),
+                *_cache_specs(k, v, k_scales, v_scales, block_table))
     B, H, D = shape = q_raw.shape
     n, rows, KVH, Dc = _cache_shape(k, v, k_scales, v_scales, B, block_table)
-    _require(Dc == D and k_raw.shape == (B, KVH, D) and v_raw.shape == (B, KVH, D),
+    _require(Dc == D and k_raw.shape == (B, KVH, D) and v_raw.shape == k_raw.shape,
              "k_raw / v_raw must be [B, KVH, D]")
     _require(q_out.shape == shape, "q_out must match q_raw")
-    _require(w_q.shape[0] == D and w_k.shape[0] == D, "w_q / w_k must be [D]")
-    _require(seq_lens.shape[0] == B, "seq_lens must have B entries")
+    _require(w_q.shape == (D,) and w_k.shape == (D,), "w_q / w_k must be [D]")
+    _require(seq_lens.shape == (B,), "seq_lens must have B entries")
     head = (q_raw.data_ptr(), k_raw.data_ptr(), v_raw.data_ptr(), w_q.data_ptr(), w_k.data_ptr())
     cache = (k.data_ptr(), v.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr())
     if block_table is None:
@@ -708,17 +744,26 @@ def gqa_prepare_decode_quant_paged(q_raw: torch.Tensor, k_raw: torch.Tensor, v_r
 
 def _decode_quant(q, k, v, k_scales, v_scales, block_table, seq_lens, window, out, out_dtype,
                   workspace, stream):
-    dev = _check_args(q, ("q", q, _BF16, 3), ("seq_lens", seq_lens, torch.int32, 1),
-                      *_cache_specs(k, v, k_scales, v_scales, block_table))
+    dev = _device_of(q)
+    try:
+        ok = (dev >= 0 and _all_on(dev, _BF16, q) and q.dim() == 3
+              and _all_on(dev, torch.int32, seq_lens)
+              and _cache_on(dev, k, v, k_scales, v_scales, block_table))
+    except AttributeError:
+        ok = False
+    if not ok:
+        _refuse(q, ("q", q, _BF16, 3), ("seq_lens", seq_lens, torch.int32, 1),
+                *_cache_specs(k, v, k_scales, v_scales, block_table))
     B, H, D = shape = q.shape
     n, rows, KVH, Dc = _cache_shape(k, v, k_scales, v_scales, B, block_table)
     _require(Dc == D, "q and the cache must have the same head size")
-    _require(seq_lens.shape[0] == B, "seq_lens must have B entries")
+    _require(seq_lens.shape == (B,), "seq_lens must have B entries")
     if out is None:
         out = torch.empty(shape, dtype=out_dtype, device=q.device)
     else:
-        _check_args(q, ("out", out, getattr(out, "dtype", None), 3))
+        _check_tensor("out", out, getattr(out, "dtype", None), 3)
         _require(out.shape == shape, "out must be [B, H, D]")
+        _same_device(q, out=out)
     ws, ws_bytes = None, 0
     if workspace is not None:
         _same_device(q, workspace=workspace)

@@ -23,8 +23,20 @@ struct PrepareQuantParams {
     QuantCache cache;
     int B, H;
     int n_rot;                    // rotated pairs
-    double freq[kPrepareMaxRot];  // theta^(-2i/D), i < n_rot
+    uint64_t turn[kPrepareMaxRot];   // turns per position of pair i, a 64-bit fraction
 };
+
+// (cos, sin) of pos turns of `turn`: the product wraps at whole turns, so the angle is
+// reduced exactly in integers.  turn is off by at most 2^-53 of itself (a double's step), the
+// angle by 2^18 * 2^-53 * 0.16 turns, 6e-12; its upper 32 bits as a signed fraction of a turn
+// by 2^-32 turns, 1.5e-9 rad.  (In fp64, at 2 operations a clock, the angles of the eight CTAs
+// of a sequence would cost more than its data.)
+__device__ __forceinline__ float2 turn_angle(int pos, uint64_t turn) {
+    const int32_t part = static_cast<int32_t>((static_cast<uint64_t>(pos) * turn) >> 32);
+    float sn, c;
+    sincosf(static_cast<float>(part) * 1.4629180792671596e-9f, &sn, &c);   // 2 pi / 2^32
+    return make_float2(c, sn);
+}
 
 template <int D>
 __global__ void __launch_bounds__(kPrepareThreads)
@@ -41,11 +53,29 @@ __global__ void __launch_bounds__(kPrepareThreads)
     const int b = blockIdx.x;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int vec = blockIdx.y * (kPrepareThreads / 32) + warp;   // q heads, k heads, v heads
-    const int pos = p.seq_lens[b] - 1;
-    if (pos < 0) return;   // no new token
+    const int L = p.seq_lens[b];
     const bool is_q = vec < p.H;
     const bool is_k = !is_q && vec < p.H + c.KVH;
     const int kvh = is_q ? 0 : (is_k ? vec - p.H : vec - p.H - c.KVH);
+    // the raw vector first: its load does not wait for the length, page and scale
+    float x[2][kPer];
+    if (vec < p.H + 2 * c.KVH) {
+        const __nv_bfloat16* src =
+            is_q ? p.q_raw + (static_cast<size_t>(b) * p.H + vec) * D
+                 : (is_k ? p.k_raw : p.v_raw) + (static_cast<size_t>(b) * c.KVH + kvh) * D;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < kPer; e += 4) {
+                const uint2 t = *reinterpret_cast<const uint2*>(src + h * kHalf + kPer * lane + e);
+                x[h][e] = __uint_as_float(t.x << 16);
+                x[h][e + 1] = __uint_as_float(t.x & 0xffff0000u);
+                x[h][e + 2] = __uint_as_float(t.y << 16);
+                x[h][e + 3] = __uint_as_float(t.y & 0xffff0000u);
+            }
+    }
+    const int pos = L - 1;
+    if (pos < 0) return;   // no new token
     size_t row = 0, scale_row = 0;
     const bool active =
         vec < p.H + 2 * c.KVH &&
@@ -55,28 +85,12 @@ __global__ void __launch_bounds__(kPrepareThreads)
     uint8_t* codes = nullptr;   // this head's first row of the block
     float* scale = nullptr;
     float old = 0.0f;
-
-    float x[2][kPer];
-    if (active) {
-        const __nv_bfloat16* src =
-            is_q ? p.q_raw + (static_cast<size_t>(b) * p.H + vec) * D
-                 : (is_k ? p.k_raw : p.v_raw) + (static_cast<size_t>(b) * c.KVH + kvh) * D;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int e = 0; e < kPer; e += 2) {
-                const __nv_bfloat162 t =
-                    *reinterpret_cast<const __nv_bfloat162*>(src + h * kHalf + kPer * lane + e);
-                x[h][e] = __low2float(t);
-                x[h][e + 1] = __high2float(t);
-            }
-        if (!is_q) {
-            codes = (is_k ? c.k : c.v) + (row * c.KVH + kvh) * D;
-            scale = (is_k ? c.k_scales : c.v_scales) + scale_row * c.KVH + kvh;
-            if (slot > 0) old = *scale;
-        }
+    if (active && !is_q) {
+        codes = (is_k ? c.k : c.v) + (row * c.KVH + kvh) * D;
+        scale = (is_k ? c.k_scales : c.v_scales) + scale_row * c.KVH + kvh;
+        if (slot > 0) old = *scale;
     }
-    if (tid < p.n_rot) cs[tid] = rope_angle(pos, p.freq[tid]);
+    if (tid < p.n_rot) cs[tid] = turn_angle(pos, p.turn[tid]);
     __syncthreads();
     if (!active) return;
 

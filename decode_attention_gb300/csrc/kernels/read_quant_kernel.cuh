@@ -2,8 +2,9 @@
 // positions s in [lo_b, min(L_b, out_rows)), in bf16 (exact: 4 significant bits, exponents
 // within range) or fp32.  Other rows of the output are left as they are.
 //
-// A CTA takes a quarter of a block of 16 positions of K or V (16 * KVH * D contiguous
-// codes); a thread loads all of its codes, 8 at a time, before it converts them.
+// A CTA takes one block of 16 positions of K or V (16 * KVH * D contiguous codes), or a
+// quarter of one when whole blocks would leave SMs idle (kParts); a thread keeps the loads of
+// 8 x 8 codes in flight.  Bound by the memory's read and write rate.
 #pragma once
 
 #include "quant_cache.cuh"
@@ -20,12 +21,12 @@ struct ReadQuantParams {
     int B, window, out_rows;
 };
 
-template <int KVH, int D, bool kF32>
+template <int KVH, int D, bool kF32, int kParts>
 __global__ void __launch_bounds__(kReadThreads)
     gqa_read_quant_kernel(const ReadQuantParams p) {
     constexpr int kRow = KVH * D;                                 // codes per position
-    constexpr int kParts = 4;                                     // items per block
     constexpr int kSteps = kQuantBlock * kRow / (8 * kReadThreads) / kParts;
+    constexpr int kBatch = kSteps < 8 ? kSteps : 8;               // loads in flight per thread
     __shared__ BlockIndex idx;
 
     ptx::grid_dependency_wait();
@@ -60,38 +61,41 @@ __global__ void __launch_bounds__(kReadThreads)
         const uint8_t* src = (is_v ? c.v : c.k) + row * kRow;
         const float* scale = (is_v ? c.v_scales : c.k_scales) + scale_row * KVH;
         const size_t out0 = (static_cast<size_t>(b) * p.out_rows + base) * kRow;
-        uint2 codes[kSteps];
+#pragma unroll 1
+        for (int s0 = 0; s0 < kSteps; s0 += kBatch) {
+            uint2 codes[kBatch];
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            const int at = at0 + s * kReadThreads * 8, pos = base + at / kRow;
-            codes[s] = make_uint2(0, 0);
-            if (pos >= lo && pos < hi) codes[s] = __ldcs(reinterpret_cast<const uint2*>(src + at));
-        }
+            for (int s = 0; s < kBatch; ++s) {
+                const int at = at0 + (s0 + s) * kReadThreads * 8, pos = base + at / kRow;
+                codes[s] = make_uint2(0, 0);
+                if (pos >= lo && pos < hi) codes[s] = __ldcs(reinterpret_cast<const uint2*>(src + at));
+            }
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            const int at = at0 + s * kReadThreads * 8, pos = base + at / kRow;
-            if (pos < lo || pos >= hi) continue;
-            const uint2 w = codes[s];
-            const float f = pow2f(scale_exponent(__ldg(scale + (at % kRow) / D)));
-            float2 v[4] = {ptx::e4m3x2_to_float2(static_cast<uint16_t>(w.x)),
-                           ptx::e4m3x2_to_float2(static_cast<uint16_t>(w.x >> 16)),
-                           ptx::e4m3x2_to_float2(static_cast<uint16_t>(w.y)),
-                           ptx::e4m3x2_to_float2(static_cast<uint16_t>(w.y >> 16))};
+            for (int s = 0; s < kBatch; ++s) {
+                const int at = at0 + (s0 + s) * kReadThreads * 8, pos = base + at / kRow;
+                if (pos < lo || pos >= hi) continue;
+                const uint2 w = codes[s];
+                const float f = pow2f(scale_exponent(__ldg(scale + (at % kRow) / D)));
+                float2 v[4] = {ptx::e4m3x2_to_float2(static_cast<uint16_t>(w.x)),
+                               ptx::e4m3x2_to_float2(static_cast<uint16_t>(w.x >> 16)),
+                               ptx::e4m3x2_to_float2(static_cast<uint16_t>(w.y)),
+                               ptx::e4m3x2_to_float2(static_cast<uint16_t>(w.y >> 16))};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = make_float2(v[i].x * f, v[i].y * f);
-            if (kF32) {
-                float4* o = reinterpret_cast<float4*>(static_cast<float*>(is_v ? p.v_out : p.k_out) + out0 + at);
-                __stcs(o, make_float4(v[0].x, v[0].y, v[1].x, v[1].y));
-                __stcs(o + 1, make_float4(v[2].x, v[2].y, v[3].x, v[3].y));
-            } else {
-                uint4 o;
-                uint32_t* ow = &o.x;
+                for (int i = 0; i < 4; ++i) v[i] = make_float2(v[i].x * f, v[i].y * f);
+                if (kF32) {
+                    float4* o = reinterpret_cast<float4*>(static_cast<float*>(is_v ? p.v_out : p.k_out) + out0 + at);
+                    __stcs(o, make_float4(v[0].x, v[0].y, v[1].x, v[1].y));
+                    __stcs(o + 1, make_float4(v[2].x, v[2].y, v[3].x, v[3].y));
+                } else {
+                    uint4 o;
+                    uint32_t* ow = &o.x;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const __nv_bfloat162 t = __floats2bfloat162_rn(v[i].x, v[i].y);
-                    ow[i] = *reinterpret_cast<const uint32_t*>(&t);
+                    for (int i = 0; i < 4; ++i) {
+                        const __nv_bfloat162 t = __floats2bfloat162_rn(v[i].x, v[i].y);
+                        ow[i] = *reinterpret_cast<const uint32_t*>(&t);
+                    }
+                    __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_v ? p.v_out : p.k_out) + out0 + at), o);
                 }
-                __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_v ? p.v_out : p.k_out) + out0 + at), o);
             }
         }
     }
