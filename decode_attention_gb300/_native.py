@@ -532,7 +532,7 @@ def _call_on(dev: int, stream, name: str, *args) -> None:
         handle = torch._C._cuda_getCurrentRawStream(dev)
     else:
         handle = stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:   # (CUDA is initialised: its tensors are here)
         st = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -761,12 +761,14 @@ def _decode_quant(q, k, v, k_scales, v_scales, block_table, seq_lens, window, ou
     if out is None:
         out = torch.empty(shape, dtype=out_dtype, device=q.device)
     else:
-        _check_tensor("out", out, getattr(out, "dtype", None), 3)
+        dtype = getattr(out, "dtype", None)
+        if not (_device_of(out) == dev and _all_on(dev, dtype, out)):
+            _refuse(q, ("out", out, dtype, 3))
         _require(out.shape == shape, "out must be [B, H, D]")
-        _same_device(q, out=out)
     ws, ws_bytes = None, 0
     if workspace is not None:
-        _same_device(q, workspace=workspace)
+        if workspace.get_device() != dev:
+            _same_device(q, workspace=workspace)
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     head = (q.data_ptr(), k.data_ptr(), v.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr())
     tail = (H, KVH, D, int(window), out.data_ptr(), _out_code(out), ws, ws_bytes)

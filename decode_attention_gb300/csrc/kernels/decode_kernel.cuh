@@ -419,15 +419,22 @@ __device__ __forceinline__ void store_out4(const DecodeParams& p, size_t idx, fl
 // One short pass per warp instead of one warp walking eight sequences per lane
 // keeps the plan's latency (and the code fetched cold on each SM) small.
 //
-// kAlign: ranges are widened to whole blocks of kAlign positions, which makes every piece
-// start and end on a block when `unit` is whole blocks too; the caller masks the
-// positions outside the attended range.  kExtra: see static_tiles.
+// Tune: kAlign widens the ranges to whole blocks of kAlign positions, which makes every
+// piece start and end on a block when `unit` is whole blocks too (the caller masks the
+// positions outside the attended range); kExtra: see static_tiles; kMinShare and
+// kChunksPerCta: the two constants above.
 // ---------------------------------------------------------------------------
 constexpr int kPlanWarps = kMaxBatch / 32;   // 8
 
-template <int kAlign = 1, int kExtra = 0>
+struct PlanTuning {
+    static constexpr int kAlign = 1, kExtra = 0;
+    static constexpr int kMinShare = kDynMinShare, kChunksPerCta = kDynChunksPerCta;
+};
+
+template <class Tune = PlanTuning>
 __device__ __forceinline__ void build_plan(PlanSmem& pl, const DecodeParams& p, int grid, int warp,
                                            int lane, int cta, int unit, uint32_t* xsum) {
+    constexpr int kAlign = Tune::kAlign, kExtra = Tune::kExtra;
     const int B = p.B, KVH = p.KVH;
     const int b = warp * 32 + lane;
     const bool plan_warp = warp < kPlanWarps;
@@ -476,15 +483,15 @@ __device__ __forceinline__ void build_plan(PlanSmem& pl, const DecodeParams& p, 
         const uint32_t N = tot * static_cast<uint32_t>(KVH);
         const uint32_t ugrid = static_cast<uint32_t>(grid);
         const uint32_t g = N < ugrid ? N : ugrid;
-        const uint32_t cdyn = static_cast<uint32_t>(kDynChunksPerCta) * ugrid;
+        const uint32_t cdyn = static_cast<uint32_t>(Tune::kChunksPerCta) * ugrid;
         const uint32_t cap = cdyn < static_cast<uint32_t>(p.max_dyn) ? cdyn : static_cast<uint32_t>(p.max_dyn);
         // the short chunks' slots are set aside first (at most half of them)
         const uint32_t tail_want = static_cast<uint32_t>(kDynTailPerCta) * ugrid;
         const uint32_t tail_cap = tail_want < cap / 2 ? tail_want : cap / 2;
         const uint32_t long_cap = cap - tail_cap;
-        // floor(N / g) >= kDynMinShare; none in the single-piece test mode
+        // floor(N / g) >= kMinShare; none in the single-piece test mode
         single = (p.test_flags & kTestSinglePiece) != 0;
-        const bool use_dyn = !single && g > 0 && N >= static_cast<uint32_t>(kDynMinShare) * g &&
+        const bool use_dyn = !single && g > 0 && N >= static_cast<uint32_t>(Tune::kMinShare) * g &&
                              long_cap > 0;
         int T = 0;
         if (use_dyn) {

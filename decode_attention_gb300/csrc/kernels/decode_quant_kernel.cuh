@@ -31,8 +31,10 @@
 // between the contractions, every warp repeats the softmax of all positions: 1370
 // instructions per warp and 128 positions at g = 2 against ~300 here.)
 //
-// Work split, timeouts and merging between CTAs are those of decode_kernel.cuh: a
-// persistent CTA per SM, a plan built from seq_lens on the device.  Pieces start and end on
+// Work split and timeouts are those of decode_kernel.cuh: a persistent CTA per SM, a plan
+// built from seq_lens on the device; split segments are merged by the combine kernel (merged
+// by the CTA of the last partial, as bf16 sliding calls are, every batch size was slower:
+// sliding windows of 1024, B = 1 11.7 us against 10.9, B = 64 96 against 87).  Pieces start and end on
 // blocks.  The consumer warps form groups of NC; each group is a unit of the plan with a
 // schedule of its own, so that one group computes while another merges its piece (g = 2:
 // two groups of 4).  At g = 8 the D x 8 accumulators of a block would take 128 registers and
@@ -56,21 +58,28 @@ struct DecodeQuantParams {
     int blocks;              // blocks per sequence (contiguous)
 };
 
-template <int kG, int kD, int kGroups, int kSplitD, int kRing, bool kMerge>
+// The plan's constants for this kernel, whose pieces cost 2-3 us of a group (q, merge,
+// barriers) while 8-bit rows stream twice as fast as bf16 ones: a piece counts as kExtra
+// blocks, and dynamic chunks are fewer and begin at four times the work.  Measured with 4
+// extra blocks, 256 positions and 8 chunks per CTA, and with these: decode_global_b8 37.3 and
+// 31.7 us, decode_sliding_b64_paged 89.4 and 84.6 us, decode_global_b64_paged 350 and 341 us.
+struct QuantPlanTuning {
+    static constexpr int kAlign = kQuantBlock, kExtra = 12;
+    static constexpr int kMinShare = 1024, kChunksPerCta = 4;
+};
+
+template <int kG, int kD, int kGroups, int kSplitD, int kRing>
 struct QuantPolicy {
     static constexpr int G = kG, D = kD, GROUPS = kGroups, RING = kRing;
     static constexpr int NC = 4;                         // blocks a group works on at a time
     static constexpr int SPLIT = kSplitD;                // warps per block, D / SPLIT dims each
     static constexpr int GW = NC * SPLIT;                // consumer warps per group
     static constexpr int SLOTS = NC * RING;              // of a group: one block of K and V each
-    static constexpr bool kMergeInKernel = kMerge;
     static constexpr int kConsumers = GROUPS * GW;
     static constexpr int kWarps = kConsumers + 2 * GROUPS;
     static constexpr int kThreads = (kWarps < kPlanWarps ? kPlanWarps : kWarps) * 32;
     static constexpr int kUnits = D / 16;                // 16-dim steps
     static constexpr int kOwnUnits = kUnits / SPLIT;     // those of one warp
-    // Cost of a piece (q, merge, barriers: 2-3 us of a group) in blocks, for the plan's balance
-    static constexpr int kExtra = 4;
     static constexpr bool kSplitCols = G == 2;           // hi and lo parts of P in one mma
     static constexpr int kMergeDims = 128 / SPLIT;       // dims of a warp merged per round
     static constexpr int kMergeStride = kMergeDims + 4;  // conflict-free float2 stores
@@ -108,7 +117,6 @@ struct alignas(1024) QuantSmem {
         };
         alignas(128) __nv_bfloat16 q[Pol::G][Pol::kQStride];
         float wm[Pol::NC][8], wl[Pol::NC][8];    // M and l per column of each warp (pair)
-        int merge_last;
     };
     uint8_t kv[Pol::GROUPS][Pol::SLOTS][2][kTileBytes];   // [slot][K, V][chunk][16 rows][128 B]
     Group group[Pol::GROUPS];
@@ -392,7 +400,7 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
     constexpr int SPLIT = Pol::SPLIT;
     constexpr int kLoads = NC / 2;             // rings a producer fills
     constexpr int kGroupThreads = Pol::GW * 32;   // consumers of a group
-    constexpr std::integral_constant<int, Pol::kExtra> kExtra{};
+    constexpr std::integral_constant<int, QuantPlanTuning::kExtra> kExtra{};
     constexpr uint32_t kTileBytes = QuantSmem<Pol>::kTileBytes;
     constexpr uint32_t kQBytes = G * D * 2;
     const DecodeParams& p = qp.d;
@@ -431,7 +439,7 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
     // (the plan's barriers make the lengths visible)
     for (int b = tid; b < B; b += blockDim.x)
         sm.len[b] = min(max(__ldg(p.seq_lens + b), 0), p.capacity);
-    build_plan<kQuantBlock, Pol::kExtra>(pl, p, units, warp, lane, cta, kQuantBlock,
+    build_plan<QuantPlanTuning>(pl, p, units, warp, lane, cta, kQuantBlock,
                             reinterpret_cast<uint32_t*>(&sm.kv[0][0][0][0]));
 
     // zeros for empty sequences and the segments' partial lists, as in decode_kernel.cuh
@@ -443,18 +451,16 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
             const size_t base = static_cast<size_t>(b) * H * D;
             for (int i = tid; i < H * D; i += nt) store_out(p, base + i, 0.0f);
         }
-        if (!Pol::kMergeInKernel) {
-            const int U = B * KVH;
-            const int u_end = (cta + 1) * U / static_cast<int>(gridDim.x);
-            for (int u = cta * U / static_cast<int>(gridDim.x) + tid; u < u_end; u += nt) {
-                const int b = u / KVH, kvh = u - b * KVH;
-                int4 e = make_int4(0, 0, 0, 0);
-                if (pl.n[b] != 0 && pl.g_eff > 0) {
-                    const SegmentParts sp(pl, b, kvh, p.dyn_slot_base, kExtra);
-                    e = make_int4(sp.first_s, sp.ns_parts, sp.dk0, sp.nd_parts);
-                }
-                p.ws_segs[u] = e;
+        const int U = B * KVH;
+        const int u_end = (cta + 1) * U / static_cast<int>(gridDim.x);
+        for (int u = cta * U / static_cast<int>(gridDim.x) + tid; u < u_end; u += nt) {
+            const int b = u / KVH, kvh = u - b * KVH;
+            int4 e = make_int4(0, 0, 0, 0);
+            if (pl.n[b] != 0 && pl.g_eff > 0) {
+                const SegmentParts sp(pl, b, kvh, p.dyn_slot_base, kExtra);
+                e = make_int4(sp.first_s, sp.ns_parts, sp.dk0, sp.nd_parts);
             }
+            p.ws_segs[u] = e;
         }
     }
     // this warp's group and its unit (a group without a unit has nothing to do)
@@ -493,7 +499,7 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
                 if (!ok) break;
                 int claimed = -1;
                 Piece w;
-                if (!next_piece<Pol::kExtra>(pl, p, unit, kQuantBlock, dynamic, x, stop, claimed, w)) {
+                if (!next_piece<QuantPlanTuning::kExtra>(pl, p, unit, kQuantBlock, dynamic, x, stop, claimed, w)) {
                     gr.piece.done = 1;
                     ptx::mbar_arrive(q_full);
                     break;
@@ -581,14 +587,6 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
                     wait_drain(ptx::smem_addr(&gr.full[(me + 2 * k) * RING + f % RING]), (f / RING) & 1u);
             if (me == 0 && n > 0) wait_drain(q_full, (n - 1u) & 1u);
         }
-        if (Pol::kMergeInKernel && me == 0 && dynamic) {
-            // no combine kernel follows: the last producer to finish claiming zeroes the claim
-            // counter for the next call
-            if (ptx::atom_add_acq_rel_gpu(p.ws_done, 1u) == static_cast<uint32_t>(pl.g_eff - 1)) {
-                atomicExch(p.ws_claim, 0u);
-                atomicExch(p.ws_done, 0u);
-            }
-        }
         return;
     }
 
@@ -601,31 +599,13 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
     const int own = gwarp % NC, half = gwarp / NC;   // ring, part of D
     const uint32_t q_frag = ptx::smem_addr(&gr.q_frag[0][0]);
     uint32_t taken = 0;   // blocks this warp has processed (its ring's fills, in order)
-    // In-kernel merge of a segment's partials: the group whose partial completes the count
-    // merges them.  The count's round trip is not waited for: its result is used one piece
-    // later.
-    bool counted = false, arrived = false;
-    int counted_b = 0, counted_kvh = 0;
-    auto merge_counted = [&]() {   // every thread of the group, after the barrier that follows the flag
-        if (!counted || !gr.merge_last) return;
-        const SegmentParts sp(pl, counted_b, counted_kvh, p.dyn_slot_base, kExtra);
-        const int u = counted_b * KVH + counted_kvh;
-#pragma unroll
-        for (int i = 0; i < G * D / 2; i += kGroupThreads)   // two outputs per thread and turn
-            merge_segment<G, D, G * D / 2>(p, sp, u, static_cast<size_t>(u) * G * D, i + gtid);
-        if (gtid == 0) p.ws_seg_count[u] = 0u;
-    };
     for (uint32_t n = 0;; ++n) {
         const bool there = __all_sync(0xffffffffu, wait_bounded(q_full, n & 1u, &sm.abort_flag, p.ws_flags));
         QuantPiece pc;
         pc.done = 1;
         if (there) pc = gr.piece;
         if (!pc.done) c.begin(&gr.q[0][0], gr.q_frag, gwarp, lane);
-        if (Pol::kMergeInKernel && pc.done && gtid == 0) gr.merge_last = arrived;
-        if (ptx::named_barrier_or(bar, kGroupThreads, pc.done != 0)) {
-            if constexpr (Pol::kMergeInKernel) merge_counted();
-            break;
-        }
+        if (ptx::named_barrier_or(bar, kGroupThreads, pc.done != 0)) break;
         if (gtid == 0) ptx::mbar_arrive(q_empty);   // every warp has read q and the piece
 
         bool gone = false;
@@ -684,27 +664,13 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
                 gr.wl[own][2 * lane + j] = ls;
             }
         }
-        if (Pol::kMergeInKernel && gtid == 0) gr.merge_last = arrived;
         if (ptx::named_barrier_or(bar, kGroupThreads, gone)) break;
         const size_t out_base = (static_cast<size_t>(pc.b) * H + pc.kvh * G) * D;
         c.merge(gr, p, out_base, pc.parts == 1 ? -1 : pc.slot, bar, own, half, lane);
-        if constexpr (Pol::kMergeInKernel) {
-            // count the partial (the merge's last barrier is behind its stores); whether it was
-            // the segment's last is looked at when the next piece ends
-            merge_counted();
-            counted = pc.parts > 1;
-            counted_b = pc.b;
-            counted_kvh = pc.kvh;
-            arrived = false;
-            if (counted && gtid == 0)
-                arrived = ptx::atom_add_acq_rel_gpu(p.ws_seg_count + pc.b * KVH + pc.kvh, 1u) + 1u ==
-                          static_cast<uint32_t>(pc.parts);
-        }
     }
 }
 
-using QuantSliding = QuantPolicy<2, 256, 2, 1, 3, false>;       // slidingDecodeGQA, many segments
-using QuantSlidingFew = QuantPolicy<2, 256, 2, 1, 3, true>;     // slidingDecodeGQA, few segments
-using QuantGlobal = QuantPolicy<8, 512, 1, 2, 3, false>;        // decodeGQA
+using QuantSliding = QuantPolicy<2, 256, 2, 1, 3>;   // slidingDecodeGQA
+using QuantGlobal = QuantPolicy<8, 512, 1, 2, 3>;    // decodeGQA
 
 }  // namespace gqa

@@ -52,19 +52,21 @@ cudaError_t launch(const LaunchArgs& a, const DecodeQuantParams& p) {
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.grid));
+    // (a workspace holds partials of at most kMaxCtas static units)
+    const int grid = a.grid < kMaxCtas / Pol::GROUPS ? a.grid : kMaxCtas / Pol::GROUPS;
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(Pol::kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = a.stream;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, gqa_decode_quant_kernel<Pol, kPaged>, tm_k, tm_v, p);
-    if (e != cudaSuccess || Pol::kMergeInKernel) return e;
+    if (e != cudaSuccess) return e;
 
     const int segments = a.p.B * a.p.KVH;
     constexpr int kChunksPerSeg = (Pol::G * Pol::D / 4 + kCombineThreads - 1) / kCombineThreads;
     const int items = segments * kChunksPerSeg;
-    const int most = kCombineBlocksPerSm * a.grid;
+    const int most = kCombineBlocksPerSm * grid;
     cudaLaunchConfig_t ccfg = cfg;
     ccfg.gridDim = dim3(static_cast<unsigned>(items < most ? items : most));
     ccfg.blockDim = dim3(kCombineThreads);
@@ -80,11 +82,8 @@ cudaError_t launch_quant(const LaunchArgs& a, bool sliding, bool paged) {
     p.k_scales = a.k_scales;
     p.v_scales = a.v_scales;
     p.blocks = static_cast<int>((a.rows + kQuantBlock - 1) / kQuantBlock);
-    if (sliding) {
-        if (a.p.B * a.p.KVH <= a.grid)
-            return paged ? launch<QuantSlidingFew, true>(a, p) : launch<QuantSlidingFew, false>(a, p);
+    if (sliding)
         return paged ? launch<QuantSliding, true>(a, p) : launch<QuantSliding, false>(a, p);
-    }
     return paged ? launch<QuantGlobal, true>(a, p) : launch<QuantGlobal, false>(a, p);
 }
 
