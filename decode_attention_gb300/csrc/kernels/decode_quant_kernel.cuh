@@ -25,25 +25,29 @@
 // An mma truncates its sum, so long chains of them drift: a block's products start from
 // zero and are added to the accumulators by ordinary additions.
 //
-// A warp works on whole blocks by itself: its own M, l and D x 8 accumulators, no exchange
-// with the other warps until the piece ends, when the 8 states are merged through shared
-// memory.  (With the 8 warps sharing each tile, one part of the dims each and a score tile
-// between the contractions, every warp repeats the softmax of all positions: 1370
-// instructions per warp and 128 positions at g = 2 against ~300 here.)
-//
 // Work split and timeouts are those of decode_kernel.cuh: a persistent CTA per SM, a plan
-// built from seq_lens on the device; split segments are merged by the combine kernel (merged
-// by the CTA of the last partial, as bf16 sliding calls are, every batch size was slower:
-// sliding windows of 1024, B = 1 11.7 us against 10.9, B = 64 96 against 87).  Pieces start and end on
-// blocks.  The consumer warps form groups of NC; each group is a unit of the plan with a
-// schedule of its own, so that one group computes while another merges its piece (g = 2:
-// two groups of 4).  At g = 8 the D x 8 accumulators of a block would take 128 registers and
-// leave one warp per scheduler; there two warps share a block, half of D each, and add their
-// halves of the scores (one group of 4 pairs).  A group has two
-// producer threads: the first walks its schedule and publishes pieces, both stream K and V
-// with TMA, one slot per block.  Block i of a piece goes to warp i % NC of the group, into
-// that warp's own ring of slots.  (A ring shared by the warps would let a warp wait on a slot's
-// barrier two fills ahead of its last completion, which a parity cannot tell apart.)
+// built from seq_lens on the device; split segments are merged by the combine kernel.  Pieces
+// start and end on blocks.  A CTA holds several units of the plan, each with a schedule of
+// its own, so that one computes while another begins or ends a piece.  In a unit, NC warps (at
+// g = 8, where the accumulators would take 128 registers and leave one warp per scheduler, NC
+// pairs, half of D each, which add their halves of the scores) work on a block each: block i of
+// a piece goes to warp i % NC, into that warp's own ring of slots, and the warp keeps M, l and
+// the D x 8 accumulators until the piece ends, when the NC states are merged through shared
+// memory.  (A ring shared by the warps would let a warp wait on a slot's barrier two fills
+// ahead of its last completion, which a parity cannot tell apart.)  Producer threads walk the
+// schedules and issue the TMA copies, one slot per block.
+//
+// NC = 4 or 2 (kernels_quant.cu has the rule): larger units leave fewer partials to merge and
+// read longer runs (decode_global_b16_long 905 us against 934, one sliding window of 1024
+// 11.0 against 14.5), smaller ones overlap more ends of pieces, which cost 2-3 us each (B = 128
+// of at most 16, 64 and 256 positions, g = 2: 29.9, 34.7, 45.5 against 20.5, 24.4, 40.6 us; g =
+// 8: 26.2, 28.7, 36.5 against 18.8, 22.4, 35.0).
+//
+// Measured on the way (decode_sliding_b64_paged / decode_global_b64_paged, now 85 / 342 us):
+// the 8 warps sharing each tile, with a score tile between the contractions, 171 / 386 us
+// (every warp repeats the softmax of all positions); blocks dealt to the warps in turn and one
+// producer thread, 153 / 447 us (its ~700 cycles per 16 KB are the time HBM takes for them);
+// units of one warp or pair, 92 / 353 us.
 #pragma once
 
 #include "decode_kernel.cuh"
@@ -58,68 +62,59 @@ struct DecodeQuantParams {
     int blocks;              // blocks per sequence (contiguous)
 };
 
-// The plan's constants for this kernel, whose pieces cost 2-3 us of a group (q, merge,
-// barriers) while 8-bit rows stream twice as fast as bf16 ones: a piece counts as kExtra
-// blocks, and dynamic chunks are fewer and begin at four times the work.  Measured with 4
-// extra blocks, 256 positions and 8 chunks per CTA, and with these: decode_global_b8 37.3 and
-// 31.7 us, decode_sliding_b64_paged 89.4 and 84.6 us, decode_global_b64_paged 350 and 341 us.
+// The plan's constants for this kernel: a piece costs about kExtra blocks, and dynamic
+// chunks begin at more work than for bf16 rows, which stream half as fast.
 struct QuantPlanTuning {
     static constexpr int kAlign = kQuantBlock, kExtra = 12;
     static constexpr int kMinShare = 1024, kChunksPerCta = 4;
 };
 
-template <int kG, int kD, int kGroups, int kSplitD, int kRing>
+template <int kG, int kD, int kGroups, int kBlocksAtOnce, int kSplitD, int kRing>
 struct QuantPolicy {
-    static constexpr int G = kG, D = kD, GROUPS = kGroups, RING = kRing;
-    static constexpr int NC = 4;                         // blocks a group works on at a time
+    static constexpr int G = kG, D = kD;
+    static constexpr int GROUPS = kGroups;               // units of the plan per CTA
+    static constexpr int NC = kBlocksAtOnce;             // blocks a unit works on at a time
     static constexpr int SPLIT = kSplitD;                // warps per block, D / SPLIT dims each
-    static constexpr int GW = NC * SPLIT;                // consumer warps per group
-    static constexpr int SLOTS = NC * RING;              // of a group: one block of K and V each
+    static constexpr int RING = kRing;                   // slots per block in work: one block of K and V each
+    static constexpr int GW = NC * SPLIT;                // consumer warps per unit
     static constexpr int kConsumers = GROUPS * GW;
-    static constexpr int kWarps = kConsumers + 2 * GROUPS;
-    static constexpr int kThreads = (kWarps < kPlanWarps ? kPlanWarps : kWarps) * 32;
-    static constexpr int kUnits = D / 16;                // 16-dim steps
-    static constexpr int kOwnUnits = kUnits / SPLIT;     // those of one warp
+    static constexpr int kFeeds = NC / 2;                // producers per unit, two rings each
+    static constexpr int kWarps = kConsumers + kFeeds * GROUPS;
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kOwnUnits = D / 16 / SPLIT;     // 16-dim steps of one warp
     static constexpr bool kSplitCols = G == 2;           // hi and lo parts of P in one mma
     static constexpr int kMergeDims = 128 / SPLIT;       // dims of a warp merged per round
     static constexpr int kMergeStride = kMergeDims + 4;  // conflict-free float2 stores
     static constexpr int kMergeCols = kSplitCols ? 2 * G : G;
-    static constexpr int kQStride = D + 16;              // padded row of q: conflict-free 8-byte loads
-    static_assert((G == 2 || G == 8) && kOwnUnits % 4 == 0 && (D / SPLIT) % kMergeDims == 0, "shape");
-    static_assert(SPLIT == 1 || SPLIT == 2, "a block is one warp's or two's");
+    static_assert((G == 2 || G == 8) && (SPLIT == 1 || SPLIT == 2) && (NC == 2 || NC == 4), "shape");
+    static_assert(kOwnUnits % 8 == 0 && (D / SPLIT) % kMergeDims == 0, "shape");
+    static_assert(kThreads >= kPlanWarps * 32, "the plan takes eight warps");
 };
 
-// One piece of work, published with its q.
+// One piece of work.
 struct QuantPiece {
     int b, kvh;
     int p0, p1;     // positions, whole blocks
     int lo, hi;     // attended positions of the sequence
-    int slot;       // workspace slot of the partial
-    int parts;      // partials of the segment (1: the piece is the whole segment)
+    int slot;       // workspace slot of the partial; -1: the piece is the whole segment
     int done;       // no more pieces
 };
 
 template <class Pol>
 struct alignas(1024) QuantSmem {
     static constexpr int kTileBytes = kQuantBlock * Pol::D;
-    struct Group {
-        alignas(8) uint64_t full[Pol::SLOTS];
-        alignas(8) uint64_t empty[Pol::SLOTS];
-        alignas(8) uint64_t q_full, q_empty;
-        float scales[Pol::SLOTS][2];
-        int bad[Pol::SLOTS];                     // the block's page id is out of range
+    struct Unit {
+        alignas(8) uint64_t full[Pol::NC * Pol::RING];
+        alignas(8) uint64_t empty[Pol::NC * Pol::RING];
+        alignas(8) uint64_t piece_full, piece_empty;
+        float scales[Pol::NC * Pol::RING][2];
+        int bad[Pol::NC * Pol::RING];            // the block's page id is out of range
         QuantPiece piece;
-        // a piece's q fragments are last read before its merge, whose last barrier precedes the
-        // next piece's
-        union alignas(16) {
-            uint2 q_frag[Pol::kUnits][32];                      // B fragments of q (column g = head g % G)
-            float wacc[Pol::SPLIT][Pol::NC][Pol::kMergeCols][Pol::kMergeStride];   // dims being merged
-        };
-        alignas(128) __nv_bfloat16 q[Pol::G][Pol::kQStride];
         float wm[Pol::NC][8], wl[Pol::NC][8];    // M and l per column of each warp (pair)
+        alignas(16) float wacc[Pol::SPLIT][Pol::NC][Pol::kMergeCols][Pol::kMergeStride];   // dims being merged
     };
-    uint8_t kv[Pol::GROUPS][Pol::SLOTS][2][kTileBytes];   // [slot][K, V][chunk][16 rows][128 B]
-    Group group[Pol::GROUPS];
+    uint8_t kv[Pol::GROUPS][Pol::NC * Pol::RING][2][kTileBytes];   // [slot][K, V][chunk][16 rows][128 B]
+    Unit unit[Pol::GROUPS];
     alignas(8) uint64_t stall_bar;               // kTestStall: a barrier nothing completes
     PlanSmem plan;
     int len[kMaxBatch];                          // clamped lengths
@@ -128,11 +123,12 @@ struct alignas(1024) QuantSmem {
 
 template <class Pol>
 struct QuantConsumer {
-    static constexpr int G = Pol::G, D = Pol::D, kUnits = Pol::kUnits, kOwnUnits = Pol::kOwnUnits;
+    static constexpr int G = Pol::G, D = Pol::D, kOwnUnits = Pol::kOwnUnits;
     static constexpr float kTop = 15.0f;    // largest exponent of a weight (f16 ends at 2^16)
     static constexpr float kRoom = 3.0f;    // binades left above the maximum when M is set
 
-    float q_factor[2];           // undo q's scaling for columns 2t and 2t + 1, times log2(e)
+    uint2 qb[kOwnUnits];         // B fragments of q (column g = head g % G) for this warp's dims
+    float q_undo[2];             // undo their scaling for columns 2t and 2t + 1
     float acc[kOwnUnits][4];     // rows: dims 2g (0, 1) and 2g + 1 (2, 3); columns 2t, 2t + 1
     float m[2];                  // M of columns 2t, 2t + 1
     float l[2];                  // this lane's share of their normalisers
@@ -142,17 +138,15 @@ struct QuantConsumer {
         return block + (unit >> 3) * 2048 + r * 128 + (((unit & 7) ^ (r & 7)) << 4);
     }
 
-    // q_heads: [G][kQStride] bf16 in shared memory.  Each warp makes its share of the fragments (a
-    // barrier follows).
-    __device__ __forceinline__ void begin(const __nv_bfloat16* q_heads, uint2 (*frag)[32], int warp,
-                                          int lane) {
+    // q_heads: [G][D] bf16 in global memory; `half`: which part of D is this warp's.
+    __device__ __forceinline__ void begin(const __nv_bfloat16* q_heads, int half, int lane) {
         const int g = lane >> 2, t = lane & 3;
-        const __nv_bfloat16* row = q_heads + (g % G) * Pol::kQStride + 4 * t;
+        const __nv_bfloat16* row = q_heads + (g % G) * D + half * (kOwnUnits * 16) + 4 * t;
         uint32_t top = 0;   // largest |q|: the bits of |bf16| order like the values
-#pragma unroll 8
-        for (int u = 0; u < kUnits; ++u) {
-            const uint2 w = *reinterpret_cast<const uint2*>(row + u * 16);
-            top = __vmaxu2(top, __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu));
+#pragma unroll
+        for (int u = 0; u < kOwnUnits; ++u) {
+            qb[u] = __ldg(reinterpret_cast<const uint2*>(row + u * 16));
+            top = __vmaxu2(top, __vmaxu2(qb[u].x & 0x7fff7fffu, qb[u].y & 0x7fff7fffu));
         }
         top = max(top & 0xffffu, top >> 16);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -160,15 +154,12 @@ struct QuantConsumer {
         const int e = max(static_cast<int>(top >> 7) - 127, -100);   // |q| < 2^(e + 1)
         const float f = pow2f(14 - e);
 #pragma unroll
-        for (int i = 0; i < kUnits / Pol::GW; ++i) {
-            const int u = warp * (kUnits / Pol::GW) + i;
-            const uint2 w = *reinterpret_cast<const uint2*>(row + u * 16);
-            frag[u][lane] = make_uint2(ptx::f16x2_pack(bf16lo(w.x) * f, bf16hi(w.x) * f),
-                                       ptx::f16x2_pack(bf16lo(w.y) * f, bf16hi(w.y) * f));
-        }
-        const float undo = pow2f(e - 14) * kLog2e;
-        q_factor[0] = __shfl_sync(0xffffffffu, undo, 8 * t);
-        q_factor[1] = __shfl_sync(0xffffffffu, undo, 8 * t + 4);
+        for (int u = 0; u < kOwnUnits; ++u)
+            qb[u] = make_uint2(ptx::f16x2_pack(bf16lo(qb[u].x) * f, bf16hi(qb[u].x) * f),
+                               ptx::f16x2_pack(bf16lo(qb[u].y) * f, bf16hi(qb[u].y) * f));
+        const float undo = pow2f(e - 14);
+        q_undo[0] = __shfl_sync(0xffffffffu, undo, 8 * t);
+        q_undo[1] = __shfl_sync(0xffffffffu, undo, 8 * t + 4);
 #pragma unroll
         for (int i = 0; i < kOwnUnits; ++i)
 #pragma unroll
@@ -177,37 +168,35 @@ struct QuantConsumer {
         l[0] = l[1] = 0.0f;
     }
 
-    // This warp's share (`half` of D) of a block's scores, c[i]: rows g (0, 1) and g + 8 (2, 3),
-    // columns 2t, 2t + 1.
-    __device__ __forceinline__ void scores(uint32_t k_blk, uint32_t q_frag, int half, float (&z)[4],
-                                           int lane) {
+    // This warp's share of a block's products <q, code>: rows g (0, 1) and g + 8 (2, 3), columns
+    // 2t, 2t + 1.
+    __device__ __forceinline__ void scores(uint32_t k_blk, int half, float (&z)[4], int lane) {
         const int mat = lane >> 3, r = (mat & 1) * 8 + (lane & 7);
         float c[4][4];   // four independent chains
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) c[i][j] = 0.0f;
-        // (unit_addr's chunks: kOwnUnits is a multiple of 8 units or the whole of D)
+        // (8 units fill one of unit_addr's chunks)
         const uint32_t k_half = k_blk + half * (kOwnUnits / 8) * 2048;
-        const uint32_t q_half = q_frag + half * kOwnUnits * 256;
 #pragma unroll
         for (int u = 0; u < kOwnUnits; u += 2) {
             uint32_t a[4];   // rows g, g + 8 of unit u, then of unit u + 1
             ptx::ldmatrix_x4(unit_addr(k_half, r, u + (mat >> 1)), a[0], a[1], a[2], a[3]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const uint2 q = ptx::lds64(q_half + (u + i) * 256 + lane * 8);
                 uint32_t a0, a1, a2, a3;
                 ptx::e4m3x4_to_f16x2(a[2 * i], a0, a2);
                 ptx::e4m3x4_to_f16x2(a[2 * i + 1], a1, a3);
-                ptx::mma_f16_16816(c[(u + i) & 3], a0, a1, a2, a3, q.x, q.y);
+                ptx::mma_f16_16816(c[(u + i) & 3], a0, a1, a2, a3, qb[u + i].x, qb[u + i].y);
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) z[i] = (c[0][i] + c[1][i]) + (c[2][i] + c[3][i]);
+        for (int i = 0; i < 4; ++i)
+            z[i] = ((c[0][i] + c[1][i]) + (c[2][i] + c[3][i])) * q_undo[i & 1];
     }
 
-    // The rest of a block, from its scores z: weights, M, l, and P.V for this warp's dims.  whole:
+    // The rest of a block, from its products z: weights, M, l, and P.V for this warp's dims.  whole:
     // every row is attended; else rows [first, last) are, and none of them on a bad page.
     template <bool whole>
     __device__ __forceinline__ void weigh(const float (&z)[4], uint32_t v_blk, float k_scale,
@@ -216,9 +205,8 @@ struct QuantConsumer {
         const int g = lane >> 2, t = lane & 3;
         const int mat = lane >> 3, r = (mat & 1) * 8 + (lane & 7);
         // log2 of the weights: y = log2(e) score + ev - M, rows g (0, 1) and g + 8 (2, 3)
-        const float fk = pow2f(scale_exponent(k_scale));
+        const float f = pow2f(scale_exponent(k_scale)) * kLog2e;
         const int ev = scale_exponent(v_scale);
-        const float f[2] = {fk * q_factor[0], fk * q_factor[1]};
         // (rows outside the range: 2^-inf)
         const float evf = static_cast<float>(ev);
         bool row_ok[2] = {true, true};
@@ -227,7 +215,7 @@ struct QuantConsumer {
             row_ok[1] = g + 8 >= first && g + 8 < last;
         }
         auto level = [&](int i, float shift) {
-            const float v = fmaf(z[i], f[i & 1], !whole && bad ? __uint_as_float(0x7fc00000u) : shift);
+            const float v = fmaf(z[i], f, !whole && bad ? __uint_as_float(0x7fc00000u) : shift);
             return row_ok[i >> 1] ? v : -INFINITY;
         };
         float y[4];
@@ -314,7 +302,7 @@ struct QuantConsumer {
     // the partial (acc, m, l) at workspace slot `slot`.  The M are whole numbers, so the
     // factors 2^(M_w - M) are exact.  Called by all consumer warps, after a barrier that
     // follows the stores of wm and wl.
-    __device__ __forceinline__ void merge(typename QuantSmem<Pol>::Group& sm, const DecodeParams& p,
+    __device__ __forceinline__ void merge(typename QuantSmem<Pol>::Unit& sm, const DecodeParams& p,
                                           size_t out_base, int slot, int bar, int own, int half,
                                           int lane) {
         const int g = lane >> 2, t = lane & 3, tid = own * 32 + lane;
@@ -395,14 +383,10 @@ template <class Pol, bool kPaged>
 __global__ void __launch_bounds__(Pol::kThreads, 1)
     gqa_decode_quant_kernel(const __grid_constant__ CUtensorMap tm_k,
                             const __grid_constant__ CUtensorMap tm_v, const DecodeQuantParams qp) {
-    constexpr int G = Pol::G, D = Pol::D, SLOTS = Pol::SLOTS, NC = Pol::NC, RING = Pol::RING;
-    constexpr int GROUPS = Pol::GROUPS;
-    constexpr int SPLIT = Pol::SPLIT;
-    constexpr int kLoads = NC / 2;             // rings a producer fills
-    constexpr int kGroupThreads = Pol::GW * 32;   // consumers of a group
+    constexpr int G = Pol::G, D = Pol::D, RING = Pol::RING, GROUPS = Pol::GROUPS, SPLIT = Pol::SPLIT;
+    constexpr int NC = Pol::NC;
     constexpr std::integral_constant<int, QuantPlanTuning::kExtra> kExtra{};
     constexpr uint32_t kTileBytes = QuantSmem<Pol>::kTileBytes;
-    constexpr uint32_t kQBytes = G * D * 2;
     const DecodeParams& p = qp.d;
 
     extern __shared__ uint8_t smem_raw[];
@@ -412,22 +396,22 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
     const int tid = threadIdx.x;
     const int warp = tid >> 5, lane = tid & 31;
     const int B = p.B, KVH = p.KVH, H = p.H;
-    const int cta = blockIdx.x;
-    const int units = static_cast<int>(gridDim.x) * GROUPS;   // units of the plan
+    const int cta = blockIdx.x, ctas = static_cast<int>(gridDim.x);
     PlanSmem& pl = sm.plan;
 
-    if (tid == 0) {
-        for (int g = 0; g < GROUPS; ++g) {
-            for (int s = 0; s < SLOTS; ++s) {
-                ptx::mbar_init(ptx::smem_addr(&sm.group[g].full[s]), 2);   // the tiles' bytes, the scales
-                ptx::mbar_init(ptx::smem_addr(&sm.group[g].empty[s]), SPLIT);
-            }
-            ptx::mbar_init(ptx::smem_addr(&sm.group[g].q_full), 1);
-            ptx::mbar_init(ptx::smem_addr(&sm.group[g].q_empty), 2);   // consumers, second producer
+    if (tid < GROUPS) {
+        typename QuantSmem<Pol>::Unit& un = sm.unit[tid];
+        for (int s = 0; s < NC * RING; ++s) {
+            ptx::mbar_init(ptx::smem_addr(&un.full[s]), 2);   // the tiles' bytes, the scales
+            ptx::mbar_init(ptx::smem_addr(&un.empty[s]), SPLIT);
         }
-        ptx::mbar_init(ptx::smem_addr(&sm.stall_bar), 1);
+        ptx::mbar_init(ptx::smem_addr(&un.piece_full), 1);
+        ptx::mbar_init(ptx::smem_addr(&un.piece_empty), Pol::GW + Pol::kFeeds - 1);   // who reads it
+        if (tid == 0) {
+            ptx::mbar_init(ptx::smem_addr(&sm.stall_bar), 1);
+            sm.abort_flag = 0;
+        }
         ptx::fence_mbar_init();
-        sm.abort_flag = 0;
     }
     if (warp == Pol::kConsumers && lane == 0) {
         ptx::prefetch_tensormap(&tm_k);
@@ -439,21 +423,22 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
     // (the plan's barriers make the lengths visible)
     for (int b = tid; b < B; b += blockDim.x)
         sm.len[b] = min(max(__ldg(p.seq_lens + b), 0), p.capacity);
-    build_plan<QuantPlanTuning>(pl, p, units, warp, lane, cta, kQuantBlock,
-                            reinterpret_cast<uint32_t*>(&sm.kv[0][0][0][0]));
+    build_plan<QuantPlanTuning>(pl, p, ctas * GROUPS, warp, lane, cta, kQuantBlock,
+                                reinterpret_cast<uint32_t*>(&sm.kv[0][0][0][0]));
 
-    // zeros for empty sequences and the segments' partial lists, as in decode_kernel.cuh
-    const bool has_work = cta * GROUPS < pl.g_eff;
+    // zeros for empty sequences and the segments' partial lists, as in decode_kernel.cuh.  (Unit
+    // cta + ctas * i is this CTA's i-th: few units still spread over all CTAs.)
+    const bool has_work = cta < pl.g_eff;
     if (!has_work || warp < Pol::kConsumers) {
         const int nt = has_work ? Pol::kConsumers * 32 : static_cast<int>(blockDim.x);
-        for (int b = cta; b < B; b += gridDim.x) {
+        for (int b = cta; b < B; b += ctas) {
             if (pl.n[b] != 0) continue;
             const size_t base = static_cast<size_t>(b) * H * D;
             for (int i = tid; i < H * D; i += nt) store_out(p, base + i, 0.0f);
         }
         const int U = B * KVH;
-        const int u_end = (cta + 1) * U / static_cast<int>(gridDim.x);
-        for (int u = cta * U / static_cast<int>(gridDim.x) + tid; u < u_end; u += nt) {
+        const int u_end = (cta + 1) * U / ctas;
+        for (int u = cta * U / ctas + tid; u < u_end; u += nt) {
             const int b = u / KVH, kvh = u - b * KVH;
             int4 e = make_int4(0, 0, 0, 0);
             if (pl.n[b] != 0 && pl.g_eff > 0) {
@@ -463,214 +448,208 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
             p.ws_segs[u] = e;
         }
     }
-    // this warp's group and its unit (a group without a unit has nothing to do)
-    const int group = warp < Pol::kConsumers ? warp / Pol::GW : (warp - Pol::kConsumers) / 2;
-    if (warp >= Pol::kWarps) return;
-    const int unit = cta * GROUPS + group;
-    if (unit >= pl.g_eff) return;
+    if (!has_work) return;
 
-    typename QuantSmem<Pol>::Group& gr = sm.group[group];
+    // this warp's unit (a group without a unit has nothing to do)
+    const int group = warp < Pol::kConsumers ? warp / Pol::GW : (warp - Pol::kConsumers) / Pol::kFeeds;
+    const int unit = cta + ctas * group;
+    if (unit >= pl.g_eff) return;
+    typename QuantSmem<Pol>::Unit& un = sm.unit[group];
     const uint32_t kv_base = ptx::smem_addr(&sm.kv[group][0][0][0]);
-    const uint32_t q_full = ptx::smem_addr(&gr.q_full), q_empty = ptx::smem_addr(&gr.q_empty);
+    const uint32_t piece_full = ptx::smem_addr(&un.piece_full), piece_empty = ptx::smem_addr(&un.piece_empty);
 
     if (warp >= Pol::kConsumers) {
-        // ================= producers: two threads per group =================
-        // The first walks the schedule and publishes each piece with its q; both fill the
-        // slots of every second warp.  (One thread spends ~700 cycles on 16 KB -- its TMA
-        // instructions, the scales, its barriers -- which is the time HBM takes to deliver
-        // them.)
+        // ======== producers: a thread per two rings of the unit ========
+        // The unit's first walks the schedule and publishes each piece; each fills the slots of
+        // its rings.  (One thread spends ~700 cycles on 16 KB -- its TMA instructions,
+        // the scales, its barriers -- which is the time HBM takes to deliver them.)
         if (lane != 0) return;
-        const int me = (warp - Pol::kConsumers) & 1;
+        constexpr int kFeeds = Pol::kFeeds, kLoads = 2;   // rings of a producer
+        const int me = (warp - Pol::kConsumers) % kFeeds;
         const uint64_t policy = ptx::policy_evict_first();
         const bool dynamic = pl.n_dyn > 0;
         long long x = static_unit_begin(pl, unit);
         const long long stop = static_unit_begin(pl, unit + 1);
-        uint32_t filled[kLoads];   // blocks sent to warps me, me + 2, ...
+        uint32_t filled[kLoads];   // blocks sent to rings me, me + kFeeds
 #pragma unroll
         for (int k = 0; k < kLoads; ++k) filled[k] = 0;
-        uint32_t n = 0;            // pieces published
         bool ok = true;
-        while (true) {
-            QuantPiece pc;
+        for (uint32_t n = 0; ok; ++n) {
+            int b, kvh, blk0, blk1;
             if (me == 0) {
-                // the description and q are free once the consumers began the piece before and
-                // the other producer has read it
-                ok = wait_bounded(q_empty, (n & 1u) ^ 1u, &sm.abort_flag, p.ws_flags);
+                // the description is free once the others have read the one before
+                ok = wait_bounded(piece_empty, (n & 1u) ^ 1u, &sm.abort_flag, p.ws_flags);
                 if (!ok) break;
                 int claimed = -1;
                 Piece w;
                 if (!next_piece<QuantPlanTuning::kExtra>(pl, p, unit, kQuantBlock, dynamic, x, stop, claimed, w)) {
-                    gr.piece.done = 1;
-                    ptx::mbar_arrive(q_full);
+                    un.piece.done = 1;
+                    ptx::mbar_arrive(piece_full);
                     break;
                 }
                 const int L = sm.len[w.b];
-                pc.b = w.b;
-                pc.kvh = w.kvh;
-                pc.p0 = w.p0;
-                pc.p1 = w.p1;
-                pc.lo = p.window > 0 && L > p.window ? L - p.window : 0;
-                pc.hi = L;
-                pc.slot = w.slot;
-                pc.parts = SegmentParts(pl, w.b, w.kvh, p.dyn_slot_base, kExtra).count();
-                pc.done = 0;
-                gr.piece = pc;
-                ptx::mbar_arrive_expect_tx(q_full, kQBytes);
-#pragma unroll
-                for (int h = 0; h < G; ++h)
-                    ptx::bulk_copy_g2s(ptx::smem_addr(&gr.q[h][0]),
-                                       p.q + (static_cast<size_t>(pc.b) * H + pc.kvh * G + h) * D,
-                                       D * 2, q_full);
+                un.piece.b = b = w.b;
+                un.piece.kvh = kvh = w.kvh;
+                un.piece.p0 = w.p0;
+                un.piece.p1 = w.p1;
+                un.piece.lo = p.window > 0 && L > p.window ? L - p.window : 0;
+                un.piece.hi = L;
+                un.piece.slot =
+                    SegmentParts(pl, w.b, w.kvh, p.dyn_slot_base, kExtra).count() == 1 ? -1 : w.slot;
+                un.piece.done = 0;
+                blk0 = w.p0 / kQuantBlock;
+                blk1 = w.p1 / kQuantBlock;
+                ptx::mbar_arrive(piece_full);
             } else {
-                ok = wait_bounded(q_full, n & 1u, &sm.abort_flag, p.ws_flags);
-                if (!ok) break;
-                pc = gr.piece;
-                if (pc.done) break;
-                ptx::mbar_arrive(q_empty);
+                ok = wait_bounded(piece_full, n & 1u, &sm.abort_flag, p.ws_flags);
+                if (!ok || un.piece.done) break;
+                b = un.piece.b;
+                kvh = un.piece.kvh;
+                blk0 = un.piece.p0 / kQuantBlock;
+                blk1 = un.piece.p1 / kQuantBlock;
+                ptx::mbar_arrive(piece_empty);
             }
-            ++n;
             const int32_t* bt_row =
-                kPaged ? p.block_table + static_cast<size_t>(pc.b) * p.max_pages : nullptr;
-            const int blk1 = pc.p1 / kQuantBlock;
-            const int chunk0 = pc.kvh * (D / 128);
+                kPaged ? p.block_table + static_cast<size_t>(b) * p.max_pages : nullptr;
+            const int chunk0 = kvh * (D / 128);
             int page[kLoads];   // page ids of the next round, loaded one round ahead
             if (kPaged) {
 #pragma unroll
                 for (int k = 0; k < kLoads; ++k) {
-                    const int blk = pc.p0 / kQuantBlock + me + 2 * k;
+                    const int blk = blk0 + me + kFeeds * k;
                     page[k] = blk < blk1 ? __ldg(bt_row + blk) : 0;
                 }
             }
-            for (int round = pc.p0 / kQuantBlock; ok && round < blk1; round += NC) {
+            for (int round = blk0; ok && round < blk1; round += NC) {
 #pragma unroll
                 for (int k = 0; k < kLoads; ++k) {
-                    const int w = me + 2 * k, blk = round + w;
+                    const int ring = me + kFeeds * k, blk = round + ring;
                     if (blk >= blk1) break;
-                    const int s = w * RING + static_cast<int>(filled[k] % RING);
-                    const uint32_t ph = (filled[k] / RING) & 1u;
-                    ok = wait_bounded(ptx::smem_addr(&gr.empty[s]), ph ^ 1u, &sm.abort_flag, p.ws_flags);
+                    const int s = ring * RING + static_cast<int>(filled[k] % RING);
+                    ok = wait_bounded(ptx::smem_addr(&un.empty[s]), ((filled[k] / RING) & 1u) ^ 1u,
+                                      &sm.abort_flag, p.ws_flags);
                     if (!ok) break;
-                    int outer = pc.b;
+                    int outer = b;
                     if (kPaged) {
                         const bool bad = page[k] < 0 || page[k] >= p.num_pages;
                         outer = bad ? 0 : page[k];   // (loaded, and masked by the consumer)
-                        gr.bad[s] = bad;
+                        un.bad[s] = bad;
                         if (bad) atomicOr(p.ws_flags, kFlagBadPage);
                         if (blk + NC < blk1) page[k] = __ldg(bt_row + blk + NC);
                     }
-                    const uint32_t full_bar = ptx::smem_addr(&gr.full[s]);
+                    const uint32_t full_bar = ptx::smem_addr(&un.full[s]);
                     ptx::mbar_arrive_expect_tx(full_bar, 2 * kTileBytes);
                     const uint32_t k_dst = kv_base + s * 2 * kTileBytes;
                     const int row = kPaged ? 0 : blk * kQuantBlock;
                     ptx::tma_load_4d(k_dst, &tm_k, full_bar, 0, row, chunk0, outer, policy);
                     ptx::tma_load_4d(k_dst + kTileBytes, &tm_v, full_bar, 0, row, chunk0, outer, policy);
                     const size_t at = (kPaged ? static_cast<size_t>(outer)
-                                              : static_cast<size_t>(pc.b) * qp.blocks + blk) * KVH + pc.kvh;
-                    const uint32_t sc_dst = ptx::smem_addr(&gr.scales[s][0]);
+                                              : static_cast<size_t>(b) * qp.blocks + blk) * KVH + kvh;
+                    const uint32_t sc_dst = ptx::smem_addr(&un.scales[s][0]);
                     ptx::cp_async4(sc_dst, qp.k_scales + at);
                     ptx::cp_async4(sc_dst + 4, qp.v_scales + at);
                     ptx::cp_async_mbar_arrive(full_bar);
                     ++filled[k];
-                    if ((p.test_flags & kTestStall) && me == 0 && k == 0 && filled[0] == 1)
+                    if ((p.test_flags & kTestStall) && group == 0 && me == 0 && k == 0 && filled[0] == 1)
                         ok = wait_bounded(ptx::smem_addr(&sm.stall_bar), 0u, &sm.abort_flag,
                                           p.ws_flags, kTestStallNs);
                     if (!ok) break;
                 }
             }
-            if (!ok) break;
         }
         if (!ok) {
             // let every copy already issued land before the CTA exits
 #pragma unroll
             for (int k = 0; k < kLoads; ++k)
                 for (uint32_t f = filled[k] > RING ? filled[k] - RING : 0u; f < filled[k]; ++f)
-                    wait_drain(ptx::smem_addr(&gr.full[(me + 2 * k) * RING + f % RING]), (f / RING) & 1u);
-            if (me == 0 && n > 0) wait_drain(q_full, (n - 1u) & 1u);
+                    wait_drain(ptx::smem_addr(&un.full[(me + kFeeds * k) * RING + f % RING]), (f / RING) & 1u);
         }
         return;
     }
 
     // ===================== consumers =====================
-    // Every warp of a group passes the same barriers for every piece, whatever its waits
-    // return; a warp whose wait gave up (or which saw the end) makes all of them leave at the
-    // next one.
+    // Every warp of a unit passes the same barriers for every piece, whatever its waits return:
+    // one that gave up (or saw the end) makes all of them leave at the piece's last barrier.
+    const int gwarp = warp - group * Pol::GW, own = gwarp / SPLIT, half = gwarp % SPLIT;
+    const int bar = 1 + group, pair_bar = 1 + GROUPS + group * NC + own;
     QuantConsumer<Pol> c;
-    const int gwarp = warp - group * Pol::GW, gtid = gwarp * 32 + lane, bar = 1 + group;
-    const int own = gwarp % NC, half = gwarp / NC;   // ring, part of D
-    const uint32_t q_frag = ptx::smem_addr(&gr.q_frag[0][0]);
     uint32_t taken = 0;   // blocks this warp has processed (its ring's fills, in order)
     for (uint32_t n = 0;; ++n) {
-        const bool there = __all_sync(0xffffffffu, wait_bounded(q_full, n & 1u, &sm.abort_flag, p.ws_flags));
-        QuantPiece pc;
+        const bool there = __all_sync(0xffffffffu, wait_bounded(piece_full, n & 1u, &sm.abort_flag, p.ws_flags));
+        QuantPiece pc{};
         pc.done = 1;
-        if (there) pc = gr.piece;
-        if (!pc.done) c.begin(&gr.q[0][0], gr.q_frag, gwarp, lane);
-        if (ptx::named_barrier_or(bar, kGroupThreads, pc.done != 0)) break;
-        if (gtid == 0) ptx::mbar_arrive(q_empty);   // every warp has read q and the piece
-
-        bool gone = false;
-        // (counted from the piece's first block: which warp takes a block, and so the order of
-        // the sums, does not depend on the pieces before)
-        for (int pos = pc.p0 + own * kQuantBlock; pos < pc.p1; pos += NC * kQuantBlock) {
-            const int s = own * RING + static_cast<int>(taken % RING);
-            const uint32_t ph = (taken / RING) & 1u;
-            gone = !__all_sync(0xffffffffu, wait_bounded(ptx::smem_addr(&gr.full[s]), ph, &sm.abort_flag, p.ws_flags));
-            const uint32_t k_tile = kv_base + s * 2 * kTileBytes;
-            float z[4];
-            if (SPLIT == 1) {
-                if (gone) break;
-                c.scores(k_tile, q_frag, 0, z, lane);
-            } else {
-                // the halves of the scores cross over through this warp's part of the K tile,
-                // which it has read
-                const uint32_t mine = k_tile + half * (kTileBytes / SPLIT) + lane * 16;
-                const uint32_t other = k_tile + (1 - half) * (kTileBytes / SPLIT) + lane * 16;
-                if (!gone) {
-                    c.scores(k_tile, q_frag, half, z, lane);
-                    __syncwarp();
-                    ptx::sts128(mine, __float_as_uint(z[0]), __float_as_uint(z[1]),
-                                __float_as_uint(z[2]), __float_as_uint(z[3]));
-                }
-                gone = ptx::named_barrier_or(1 + Pol::GROUPS + group * NC + own, 2 * 32, gone);
-                if (gone) break;
-                const uint4 o = ptx::lds128(other);
-                z[0] += __uint_as_float(o.x);
-                z[1] += __uint_as_float(o.y);
-                z[2] += __uint_as_float(o.z);
-                z[3] += __uint_as_float(o.w);
-            }
-            const float ks = gr.scales[s][0], vs = gr.scales[s][1];
-            const bool bad = kPaged && gr.bad[s] != 0;
-            const int first = pc.lo - pos, last = pc.hi - pos;
-            if (first <= 0 && last >= kQuantBlock && !bad)
-                c.template weigh<true>(z, k_tile + kTileBytes, ks, vs, 0, kQuantBlock, false, half, lane);
-            else
-                c.template weigh<false>(z, k_tile + kTileBytes, ks, vs, first, last, bad, half, lane);
-            if (SPLIT > 1) ptx::fence_proxy_async_smem();   // the scores, before the next copy
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&gr.empty[s]));
-            ++taken;
-        }
-
-        // normalisers of this warp's columns
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            float ls = c.l[j];
-            ls += __shfl_xor_sync(0xffffffffu, ls, 4);
-            ls += __shfl_xor_sync(0xffffffffu, ls, 8);
-            ls += __shfl_xor_sync(0xffffffffu, ls, 16);
-            if (half == 0 && lane < 4) {   // (the halves hold the same)
-                gr.wm[own][2 * lane + j] = c.m[j];
-                gr.wl[own][2 * lane + j] = ls;
-            }
-        }
-        if (ptx::named_barrier_or(bar, kGroupThreads, gone)) break;
+        if (there) pc = un.piece;
+        bool gone = pc.done != 0;
+        if (SPLIT > 1) gone = ptx::named_barrier_or(pair_bar, 2 * 32, gone);
+        __syncwarp();
         const size_t out_base = (static_cast<size_t>(pc.b) * H + pc.kvh * G) * D;
-        c.merge(gr, p, out_base, pc.parts == 1 ? -1 : pc.slot, bar, own, half, lane);
+        if (!gone) {
+            if (lane == 0) ptx::mbar_arrive(piece_empty);   // every lane has read it
+            c.begin(p.q + out_base, half, lane);
+            // (block i of a piece is warp i % NC's, whatever came before: the order of the sums
+            // does not depend on the schedule)
+            for (int pos = pc.p0 + own * kQuantBlock; pos < pc.p1; pos += NC * kQuantBlock) {
+                const int s = own * RING + static_cast<int>(taken % RING);
+                gone = !__all_sync(0xffffffffu, wait_bounded(ptx::smem_addr(&un.full[s]), (taken / RING) & 1u,
+                                                             &sm.abort_flag, p.ws_flags));
+                const uint32_t k_tile = kv_base + s * 2 * kTileBytes;
+                float z[4];
+                if (SPLIT == 1) {
+                    if (gone) break;
+                    c.scores(k_tile, 0, z, lane);
+                } else {
+                    // the halves of the scores cross over through this warp's part of the K
+                    // tile, which it has read
+                    const uint32_t mine = k_tile + half * (kTileBytes / SPLIT) + lane * 16;
+                    const uint32_t other = k_tile + (1 - half) * (kTileBytes / SPLIT) + lane * 16;
+                    if (!gone) {
+                        c.scores(k_tile, half, z, lane);
+                        __syncwarp();
+                        ptx::sts128(mine, __float_as_uint(z[0]), __float_as_uint(z[1]),
+                                    __float_as_uint(z[2]), __float_as_uint(z[3]));
+                    }
+                    gone = ptx::named_barrier_or(pair_bar, 2 * 32, gone);
+                    if (gone) break;
+                    const uint4 o = ptx::lds128(other);
+                    z[0] += __uint_as_float(o.x);
+                    z[1] += __uint_as_float(o.y);
+                    z[2] += __uint_as_float(o.z);
+                    z[3] += __uint_as_float(o.w);
+                }
+                const float ks = un.scales[s][0], vs = un.scales[s][1];
+                const bool bad = kPaged && un.bad[s] != 0;
+                const int first = pc.lo - pos, last = pc.hi - pos;
+                if (first <= 0 && last >= kQuantBlock && !bad)
+                    c.template weigh<true>(z, k_tile + kTileBytes, ks, vs, 0, kQuantBlock, false, half, lane);
+                else
+                    c.template weigh<false>(z, k_tile + kTileBytes, ks, vs, first, last, bad, half, lane);
+                if (SPLIT > 1) ptx::fence_proxy_async_smem();   // the scores, before the next copy
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&un.empty[s]));
+                ++taken;
+            }
+            // normalisers of this warp's columns (the halves of D hold the same)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float ls = c.l[j];
+                ls += __shfl_xor_sync(0xffffffffu, ls, 4);
+                ls += __shfl_xor_sync(0xffffffffu, ls, 8);
+                ls += __shfl_xor_sync(0xffffffffu, ls, 16);
+                if (half == 0 && lane < 4) {
+                    un.wm[own][2 * lane + j] = c.m[j];
+                    un.wl[own][2 * lane + j] = ls;
+                }
+            }
+        }
+        if (ptx::named_barrier_or(bar, Pol::GW * 32, gone)) break;
+        c.merge(un, p, out_base, pc.slot, bar, own, half, lane);
     }
 }
 
-using QuantSliding = QuantPolicy<2, 256, 2, 1, 3>;   // slidingDecodeGQA
-using QuantGlobal = QuantPolicy<8, 512, 1, 2, 3>;    // decodeGQA
+// slidingDecodeGQA and decodeGQA, for few and for many segments
+using QuantSliding = QuantPolicy<2, 256, 2, 4, 1, 3>;
+using QuantSlidingMany = QuantPolicy<2, 256, 4, 2, 1, 3>;
+using QuantGlobal = QuantPolicy<8, 512, 1, 4, 2, 3>;
+using QuantGlobalMany = QuantPolicy<8, 512, 2, 2, 2, 3>;
 
 }  // namespace gqa

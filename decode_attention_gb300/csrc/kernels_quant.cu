@@ -27,7 +27,7 @@ bool encode_codes_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_
 }
 
 template <class Pol, bool kPaged>
-cudaError_t launch(const LaunchArgs& a, const DecodeQuantParams& p) {
+cudaError_t launch(const LaunchArgs& a, const DecodeQuantParams& params) {
     constexpr size_t kSmem = sizeof(QuantSmem<Pol>) + 1024;   // + alignment slack
     static_assert(kSmem <= 227 * 1024, "shared memory");
     constexpr int kMaxDevices = 64;
@@ -52,8 +52,15 @@ cudaError_t launch(const LaunchArgs& a, const DecodeQuantParams& p) {
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    // (a workspace holds partials of at most kMaxCtas static units)
-    const int grid = a.grid < kMaxCtas / Pol::GROUPS ? a.grid : kMaxCtas / Pol::GROUPS;
+    // The workspace's kMaxCtas + B KVH + kMaxDynUnits partial slots: this kernel's units take
+    // the first `units` + B KVH, its dynamic chunks the rest (at least a quarter of theirs).
+    constexpr int kMostUnits = kMaxCtas + kMaxDynUnits * 3 / 4;
+    const int grid = a.grid < kMostUnits / Pol::GROUPS ? a.grid : kMostUnits / Pol::GROUPS;
+    const int units = grid * Pol::GROUPS;
+    DecodeQuantParams p = params;
+    p.d.dyn_slot_base = units + a.p.B * a.p.KVH;
+    p.d.max_dyn = kMaxCtas + kMaxDynUnits - units < kMaxDynUnits ? kMaxCtas + kMaxDynUnits - units
+                                                                 : kMaxDynUnits;
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(Pol::kThreads);
     cfg.dynamicSmemBytes = kSmem;
@@ -71,7 +78,7 @@ cudaError_t launch(const LaunchArgs& a, const DecodeQuantParams& p) {
     ccfg.gridDim = dim3(static_cast<unsigned>(items < most ? items : most));
     ccfg.blockDim = dim3(kCombineThreads);
     ccfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&ccfg, gqa_combine_kernel<Pol::G, Pol::D>, a.p, segments);
+    return cudaLaunchKernelEx(&ccfg, gqa_combine_kernel<Pol::G, Pol::D>, p.d, segments);
 }
 
 }  // namespace
@@ -82,8 +89,16 @@ cudaError_t launch_quant(const LaunchArgs& a, bool sliding, bool paged) {
     p.k_scales = a.k_scales;
     p.v_scales = a.v_scales;
     p.blocks = static_cast<int>((a.rows + kQuantBlock - 1) / kQuantBlock);
-    if (sliding)
-        return paged ? launch<QuantSliding, true>(a, p) : launch<QuantSliding, false>(a, p);
+    // Many segments: each CTA meets several pieces, whatever the lengths (which the host does
+    // not know), and smaller units overlap more of their ends.  With two or more segments per
+    // CTA the small units were faster at up to 1024 positions (by 1 .. 40%, the shorter the
+    // more) and 2.5% slower at 4096; with fewer they were slower by up to 30%.
+    const bool many = a.p.B * a.p.KVH >= 2 * a.grid;
+    if (sliding && many)
+        return paged ? launch<QuantSlidingMany, true>(a, p) : launch<QuantSlidingMany, false>(a, p);
+    if (sliding) return paged ? launch<QuantSliding, true>(a, p) : launch<QuantSliding, false>(a, p);
+    if (many)
+        return paged ? launch<QuantGlobalMany, true>(a, p) : launch<QuantGlobalMany, false>(a, p);
     return paged ? launch<QuantGlobal, true>(a, p) : launch<QuantGlobal, false>(a, p);
 }
 

@@ -30,6 +30,18 @@ def mode(flags):
         gqa.gqa_set_test_mode(prev)
 
 
+# batches below and above the number of segments at which the decode call changes its units
+FEW, MANY = "few", "many"
+
+
+def batch(layer, count, lens):
+    """`lens`, padded with short lengths to at least 2 * 152 segments for MANY."""
+    if count == FEW:
+        return lens
+    B = 24 if layer == "sliding" else 80
+    return lens + [(37 * i) % 150 for i in range(B - len(lens))]
+
+
 def new_workspace(geo, B, S):
     return gqa.new_workspace(B, S, geo["H"], geo["KVH"], geo["D"], 0)
 
@@ -40,7 +52,8 @@ def test_cold_repeated_calls(layer, paged):
     """Calls after a write larger than L2, over a batch of very uneven lengths (many pieces per
     CTA, dynamic chunks, merges): all equal bit for bit, the first checked."""
     geo = GEO[layer]
-    lens = [3, 2914, 130, 17, 1371, 40, 9000, 1, 640, 77, 16, 500] + [33 + 7 * i for i in range(40)]
+    lens = [3, 2914, 130, 17, 1371, 40, 9000, 1, 640, 77, 16, 500]
+    lens += [33 + 7 * i for i in range(40 if layer == "sliding" else 10)]
     cache = filled(geo, len(lens), max(lens), paged, seed=101)
     q = queries(geo, len(lens), 102)
     flush = torch.zeros(256 << 20, dtype=torch.uint8, device="cuda")
@@ -57,12 +70,13 @@ def test_cold_repeated_calls(layer, paged):
 
 @pytest.mark.parametrize("layer", ["sliding", "global"])
 @pytest.mark.parametrize("paged", [False, True])
-def test_one_piece_per_segment_agrees(layer, paged):
+@pytest.mark.parametrize("count", [FEW, MANY])
+def test_one_piece_per_segment_agrees(layer, paged, count):
     """GQA_TEST_SINGLE_PIECE: one unit computes every segment whole.  Both sides carry weights to
     at least 2^-16 and fp32 sums in another order: each lies within attend_tolerance of the
     reference, which check_decode holds both to."""
     geo = GEO[layer]
-    lens = [1500, 33, 700, 0, 16]
+    lens = batch(layer, count, [1500, 33, 700, 0, 16])
     cache = filled(geo, len(lens), 1500, paged, seed=103)
     q = queries(geo, len(lens), 104)
     ws = new_workspace(geo, len(lens), 1504)
@@ -85,14 +99,15 @@ def test_one_piece_per_segment_agrees(layer, paged):
 
 @pytest.mark.parametrize("layer", ["sliding", "global"])
 @pytest.mark.parametrize("paged", [False, True])
-def test_stalled_call_takes_the_timeout_exit(layer, paged):
+@pytest.mark.parametrize("count", [FEW, MANY])
+def test_stalled_call_takes_the_timeout_exit(layer, paged, count):
     """GQA_TEST_STALL: a producer waits 1 ms on a barrier that nothing completes.  The call
     ends, the status says so, and the workspace serves the next call."""
     geo = GEO[layer]
-    lens = [1, 700, 3000, 5000]
-    cache = filled(geo, len(lens), 5000, paged, seed=105)
+    lens = batch(layer, count, [1, 700, 2100, 3000])
+    cache = filled(geo, len(lens), 3000, paged, seed=105)
     q = queries(geo, len(lens), 106)
-    ws = new_workspace(geo, len(lens), 5008)
+    ws = new_workspace(geo, len(lens), 3008)
     torch.cuda.synchronize()
     t0 = time.perf_counter()
     with mode(gqa.GQA_TEST_STALL):
@@ -192,6 +207,20 @@ def test_streams_given_by_argument(layer):
                     c.ref[t][b][h].append(x[off[b]:off[b + 1], h], 0)
         check_decode(c, q, lens, 0, out)
         assert gqa.gqa_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("layer", ["sliding", "global"])
+def test_many_segments_repeated(layer):
+    """A batch of many segments, some of them long: equal calls, all sequences checked."""
+    geo = GEO[layer]
+    B = 40 if layer == "sliding" else 90
+    lens = [(61 * i) % 700 for i in range(B - 2)] + [3300, 5000]
+    cache = filled(geo, B, 5000, True, seed=115)
+    q = queries(geo, B, 116)
+    outs = [run_decode(cache, q, lens, 0, out_dtype=torch.float32) for _ in range(6)]
+    torch.cuda.synchronize()
+    check_decode(cache, q, lens, 0, outs[0])
+    assert all(torch.equal(o, outs[0]) for o in outs[1:])
 
 
 def test_one_tensor_as_keys_and_values():
