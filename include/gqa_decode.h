@@ -385,7 +385,8 @@ gqa_status_t gqa_decode_mq_paged(const void *q, const void *k_pages, const void 
  *   seq_lens       int32 [B] (device): lengths AFTER the append; with n_b new tokens
  *                  they go to the positions [L_b - n_b, L_b)
  * A block whose first position is among the new ones gets the scale of its new rows.  A
- * block that holds earlier rows keeps the larger of its scale and that of the new rows;
+ * block that holds earlier rows (all of them written before, by these calls) keeps the
+ * larger of its scale and that of the new rows;
  * when the scale grows, the earlier rows are coded again (exact, but for values that
  * become subnormal codes).  Rows from L_b on are left as they were.  Sequences without
  * new tokens are skipped, and so is a sequence whose offsets lie outside [0, N] or
