@@ -631,3 +631,64 @@ def test_matches_the_bf16_core_on_exact_values():
         b = gqa.gqa_decode(q, k, v, i32(lens), geo["window"], out_dtype=torch.float32)
         check_decode(cache, q, lens, geo["window"], a)
         assert float((a - b).abs().max()) <= 1e-3 * float(v.abs().max())
+
+
+# ---------------------------------------------------------------------------- refusals
+
+def test_binding_refusals_and_empty_batches():
+    """Wrong types, layouts, shapes and devices raise before anything is enqueued; an empty batch
+    or append is a no-op."""
+    geo = GEO["sliding"]
+    c, p = Cache(geo, 2, 40, False), Cache(geo, 2, 40, True)
+    gen = torch.Generator(device="cuda").manual_seed(95)
+    x, q, lens, off = rows(gen, (8, 16, 256)), queries(geo, 2, 96), i32([4, 4]), i32([0, 4, 8])
+    k, v, ks, vs = c.args
+    wide = torch.zeros(2, 40, 16, 512, device="cuda").to(E4M3)[..., ::2]
+    bad_caches = [(k.view(torch.uint8), v, ks, vs), (k, v[:1].clone(), ks, vs), (k, v, ks[:, :2].clone(), vs),
+                  (k, v, ks.double(), vs), (k, v, ks, vs.cpu()), (wide, wide, ks, vs), (k, v, ks[0], vs[0]),
+                  (None, v, ks, vs), (k, v, ks, None)]
+    raw = producer_inputs(geo, 2, 97)
+    head = (raw["q_raw"], raw["k_raw"], raw["v_raw"], raw["w_q"], raw["w_k"])
+    q_out = torch.empty_like(q)
+    for bad in bad_caches:
+        with pytest.raises(ValueError):
+            gqa.gqa_decode_quant(q, *bad, lens, 0)
+        with pytest.raises(ValueError):
+            gqa.gqa_append_quant(x, x, off, lens, *bad)
+        with pytest.raises(ValueError):
+            gqa.gqa_read_quant(*bad, lens, 0)
+        with pytest.raises(ValueError):
+            gqa.gqa_prepare_decode_quant(*head, lens, q_out, *bad)
+    with pytest.raises(ValueError):
+        gqa.gqa_decode_quant(q.float(), *c.args, lens, 0)
+    with pytest.raises(ValueError):
+        gqa.gqa_decode_quant(q, *c.args, lens.long(), 0)
+    with pytest.raises(ValueError):
+        gqa.gqa_decode_quant(q, *c.args, i32([4]), 0)
+    with pytest.raises(ValueError):
+        gqa.gqa_decode_quant(q, *c.args, lens, 0, out=torch.empty(2, 32, 512, device="cuda"))
+    with pytest.raises(TypeError):
+        gqa.gqa_decode_quant(q, *c.args, lens, 0, out=torch.empty(2, 32, 256, device="cuda").half())
+    with pytest.raises(ValueError):
+        gqa.gqa_append_quant(x, x[:4].clone(), off, lens, *c.args)
+    with pytest.raises(ValueError):
+        gqa.gqa_append_quant(x, x, i32([0, 8]), lens, *c.args)
+    with pytest.raises(ValueError):
+        gqa.gqa_append_quant(x[:, ::2], x[:, ::2], off, lens, *c.args)
+    with pytest.raises(ValueError):
+        gqa.gqa_read_quant(*c.args, lens, 0, k_out=torch.empty(2, 40, 16, 256, device="cuda"))
+    with pytest.raises(ValueError):
+        gqa.gqa_prepare_decode_quant(head[0], head[1], None, *head[3:], lens, q_out, *c.args)
+    with pytest.raises(ValueError):
+        gqa.gqa_decode_quant_paged(q, *p.args, None, lens, 0)
+    with pytest.raises(ValueError):
+        gqa.gqa_decode_quant_paged(q, *p.args, p.table[:1].clone(), lens, 0)
+    with pytest.raises(gqa.GQAError):
+        gqa.gqa_decode_quant(q, *c.args, lens, -1)
+    gqa.gqa_append_quant(x[:0], x[:0], i32([0, 0, 0]), lens, *c.args)      # no tokens
+    e = [t[:0] for t in c.args]
+    assert gqa.gqa_decode_quant(q[:0], *e, lens[:0], 0).shape == (0, 32, 256)
+    gqa.gqa_append_quant(x, x, off[:1], lens[:0], *e)
+    torch.cuda.synchronize()
+    c.check()                                                             # nothing was written
+    p.check()
