@@ -129,6 +129,9 @@ struct QuantConsumer {
     static constexpr int G = Pol::G, D = Pol::D, kOwnUnits = Pol::kOwnUnits;
     static constexpr float kTop = 15.0f;    // largest exponent of a weight (f16 ends at 2^16)
     static constexpr float kRoom = 3.0f;    // binades left above the maximum when M is set
+    // Weights of codes below 2^-126 are flushed.  l is at least 2^(11 - 64), so at value scales
+    // from 2^kLowExp up the flushed shares are below 2^-41 of it; below, they are taken apart.
+    static constexpr int kLowExp = -32;
 
     uint2 qb[kOwnUnits];         // B fragments of q (column g = head g % G) for this warp's dims
     float q_undo[2];             // undo their scaling for columns 2t and 2t + 1
@@ -236,8 +239,11 @@ struct QuantConsumer {
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
                 const float mn = fmaxf(m[j], ceilf(top) - (kTop - kRoom));
-                const float alpha = mn == m[j] ? 1.0f : ptx::ex2(m[j] - mn);
-                l[j] *= alpha;
+                // (in two steps for l, which may be near 2^100 when the values so far were tiny)
+                const float dm = mn == m[j] ? 0.0f : fmaxf(m[j] - mn, -252.0f);
+                const float a1 = ptx::ex2(floorf(0.5f * dm)), a2 = ptx::ex2(dm - floorf(0.5f * dm));
+                const float alpha = a1 * a2;
+                l[j] = l[j] * a1 * a2;
 #pragma unroll
                 for (int i = 0; i < kOwnUnits; ++i) {
                     acc[i][j] *= alpha;
@@ -253,8 +259,13 @@ struct QuantConsumer {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const float p0 = ptx::ex2(y[2 * i]), p1 = ptx::ex2(y[2 * i + 1]);
-            l[0] = fmaf(p0, unscale, l[0]);
-            l[1] = fmaf(p1, unscale, l[1]);
+            if (ev >= kLowExp) {
+                l[0] = fmaf(p0, unscale, l[0]);
+                l[1] = fmaf(p1, unscale, l[1]);
+            } else {
+                l[0] += ptx::ex2(y[2 * i] - evf);
+                l[1] += ptx::ex2(y[2 * i + 1] - evf);
+            }
             hi[i] = ptx::f16x2_pack(p0, p1);
             const float2 h = ptx::f16x2_unpack(hi[i]);
             lo[i] = ptx::f16x2_pack(p0 - h.x, p1 - h.y);
@@ -301,10 +312,31 @@ struct QuantConsumer {
         }
     }
 
+    // The end of this warp's share of a piece: M and l of its columns to wm and wl (the halves
+    // of D hold the same).  From here on l is in [1, 2) and M has its exponent: between equal
+    // shares of the softmax the M of the weights of codes differ by up to 128, and a merge
+    // would flush one of them.  l[j] becomes the factor by which the accumulators lag behind M.
+    __device__ __forceinline__ void finish(typename QuantSmem<Pol>::Unit& sm, int own, int half,
+                                           int lane) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            float ls = l[j];
+            ls += __shfl_xor_sync(0xffffffffu, ls, 4);
+            ls += __shfl_xor_sync(0xffffffffu, ls, 8);
+            ls += __shfl_xor_sync(0xffffffffu, ls, 16);
+            const int e = ls > 0.0f && ls < INFINITY ? (__float_as_int(ls) >> 23) - 127 : 0;
+            l[j] = pow2f(-e);
+            m[j] += static_cast<float>(e);
+            if (half == 0 && lane < 4) {
+                sm.wm[own][2 * lane + j] = m[j];
+                sm.wl[own][2 * lane + j] = ls * l[j];
+            }
+        }
+    }
+
     // Merge of the warps' states: the output (slot < 0; the piece is the whole segment) or
     // the partial (acc, m, l) at workspace slot `slot`.  The M are whole numbers, so the
-    // factors 2^(M_w - M) are exact.  Called by all consumer warps, after a barrier that
-    // follows the stores of wm and wl.
+    // factors 2^(M_w - M) are exact.  Called by all consumer warps, after finish() and a barrier.
     __device__ __forceinline__ void merge(typename QuantSmem<Pol>::Unit& sm, const DecodeParams& p,
                                           size_t out_base, int slot, int bar, int own, int half,
                                           int lane) {
@@ -320,7 +352,7 @@ struct QuantConsumer {
 #pragma unroll
             for (int w = 0; w < Pol::NC; ++w) top = fmaxf(top, sm.wm[w][2 * t + j]);
             // (a warp without a finite score weighs 0; its NaN stay)
-            const float f = m[j] == -INFINITY ? 0.0f : ptx::ex2(m[j] - top);
+            const float f = m[j] == -INFINITY ? 0.0f : ptx::ex2(m[j] - top) * l[j];
 #pragma unroll
             for (int i = 0; i < kOwnUnits; ++i) {
                 acc[i][j] *= f;
@@ -470,6 +502,7 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
         constexpr int kFeeds = Pol::kFeeds, kLoads = 2;   // rings of a producer
         const int me = (warp - Pol::kConsumers) % kFeeds;
         const uint64_t policy = ptx::policy_evict_first();
+        ptx::fence_proxy_async_smem();   // the plan used the slots
         const bool dynamic = pl.n_dyn > 0;
         long long x = static_unit_begin(pl, unit);
         const long long stop = static_unit_begin(pl, unit + 1);
@@ -629,18 +662,7 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
                 if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&un.empty[s]));
                 ++taken;
             }
-            // normalisers of this warp's columns (the halves of D hold the same)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                float ls = c.l[j];
-                ls += __shfl_xor_sync(0xffffffffu, ls, 4);
-                ls += __shfl_xor_sync(0xffffffffu, ls, 8);
-                ls += __shfl_xor_sync(0xffffffffu, ls, 16);
-                if (half == 0 && lane < 4) {
-                    un.wm[own][2 * lane + j] = c.m[j];
-                    un.wl[own][2 * lane + j] = ls;
-                }
-            }
+            c.finish(un, own, half, lane);
         }
         if (ptx::named_barrier_or(bar, Pol::GW * 32, gone)) break;
         c.merge(un, p, out_base, pc.slot, bar, own, half, lane);

@@ -456,10 +456,12 @@ gqa_status_t gqa_prepare_decode_quant_paged(const void *q_raw, const void *k_raw
 /*
  * gqa_decode and gqa_decode_paged over the 8-bit cache: the same attention core on the
  * values scale * code.  Scores, softmax and sums are held in fp32, and the weights are
- * applied to at least 16 significant bits, so the result differs from the core's on
- * those values by fp32 rounding.  Everything else -- q, window, out, workspace (the same
- * size), status bits, errors -- is as for gqa_decode and gqa_decode_paged; null or
- * misaligned scales return GQA_ERR_INVALID_ARGUMENT.
+ * applied to at least 16 significant bits.  The error is that of an fp32 evaluation
+ * relative to the largest value attended in a head, whatever the scales; a channel whose
+ * values are all below 2^-20 of that one (of other blocks) has fewer bits of its own.
+ * Everything else -- q, window, out, workspace (the same size), status bits, errors -- is
+ * as for gqa_decode and gqa_decode_paged; null or misaligned scales return
+ * GQA_ERR_INVALID_ARGUMENT.
  */
 gqa_status_t gqa_decode_quant(const void *q, const void *k, const void *v, const float *k_scales,
                               const float *v_scales, const int32_t *seq_lens, int B, int S, int H,

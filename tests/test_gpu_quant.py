@@ -452,6 +452,36 @@ def test_decode_scales_far_apart(layer, spread):
 
 
 @pytest.mark.parametrize("layer", ["sliding", "global"])
+@pytest.mark.parametrize("lens", [[700], [5000, 1200, 17]])
+def test_decode_scales_at_both_ends(layer, lens):
+    """One block of values near 2^68 among blocks of zeros (whose scale is 2^-64): the zeros'
+    weights vanish beside 2^128, their share of the normaliser (1% to 13%) does not."""
+    geo, KVH, D = GEO[layer], GEO[layer]["KVH"], GEO[layer]["D"]
+    cache = Cache(geo, len(lens), max(lens), False)
+    for t in range(2):
+        cache.codes[t].zero_()
+        cache.scales[t].fill_(2.0 ** -64)
+    q = torch.zeros((len(lens), geo["H"], D), dtype=torch.bfloat16, device="cuda")
+    q[..., 3] = 10.5                                        # scores 10.5 at one position, else 0
+    for b, L in enumerate(lens):
+        at = (L - 1) // 2
+        cache.codes[0].view(torch.uint8)[b, at, :, 3] = 0x38     # 1.0
+        cache.codes[1].view(torch.uint8)[b, at, :, ::2] = 0x7e   # 448
+        cache.scales[0][b, at // 16] = 1.0
+        cache.scales[1][b, at // 16] = 2.0 ** 60
+        for h in range(KVH):
+            for t in range(2):
+                r = cache.ref[t][b][h]
+                r.v[:] = 0.0
+                r.e[:] = -64
+                r.e[at // 16] = 60 if t else 0
+            cache.ref[0][b][h].v[at, 3] = 1.0
+            cache.ref[1][b][h].v[at, ::2] = 448.0
+    out = run_decode(cache, q, lens, 0, out_dtype=torch.float32)
+    check_decode(cache, q, lens, 0, out)
+
+
+@pytest.mark.parametrize("layer", ["sliding", "global"])
 def test_decode_queries_of_any_size(layer):
     """Heads of zeros, tiny, large and mixed-magnitude queries; scores that are all far below
     zero."""
