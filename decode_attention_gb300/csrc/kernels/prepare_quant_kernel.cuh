@@ -1,14 +1,20 @@
 // The decode-step producer (prepare_kernel.cuh: norms, rotary positions) writing the new
 // token of each sequence into the 8-bit cache (quant_cache.cuh).
 //
-// The same grid: a warp per head vector.  A k or v warp codes its row from the fp32
-// result (one rounding); at the first position of a block the scale starts anew, later
-// in the block it never shrinks, and when it grows the warp re-codes the block's earlier
-// rows of its head.
+// The same grid: a warp per head vector.  A k or v warp codes its row; at the first position
+// of a block the scale starts anew, later in the block it never shrinks, and when it grows
+// the warp re-codes the block's earlier rows of its head.
+//
+// An fp32 error of 2^-22 moves a value over a border between two codes once in some 10^5
+// values, a whole step each time.  Norm, weight and rotation of k and v are therefore taken to
+// some 2^-30 (twofold.cuh): codes and scales are those of the formulas but for one value in
+// 10^7.  In a graph that costs 2.9 us in place of 2.6 for one sequence and 9.8 in place of 7.7
+// for 256; a loop of calls is bound by the host either way (11 and 12.4 us).
 #pragma once
 
 #include "prepare_kernel.cuh"
 #include "quant_cache.cuh"
+#include "twofold.cuh"
 
 namespace gqa {
 
@@ -26,16 +32,54 @@ struct PrepareQuantParams {
     uint64_t turn[kPrepareMaxRot];   // turns per position of pair i, a 64-bit fraction
 };
 
-// (cos, sin) of pos turns of `turn`: the product wraps at whole turns, so the angle is
-// reduced exactly in integers.  turn is off by at most 2^-53 of itself (a double's step), the
-// angle by 2^18 * 2^-53 * 0.16 turns, 6e-12; its upper 32 bits as a signed fraction of a turn
-// by 2^-32 turns, 1.5e-9 rad.  (In fp64, at 2 operations a clock, the angles of the eight CTAs
-// of a sequence would cost more than its data.)
-__device__ __forceinline__ float2 turn_angle(int pos, uint64_t turn) {
-    const int32_t part = static_cast<int32_t>((static_cast<uint64_t>(pos) * turn) >> 32);
-    float sn, c;
-    sincosf(static_cast<float>(part) * 1.4629180792671596e-9f, &sn, &c);   // 2 pi / 2^32
-    return make_float2(c, sn);
+// The angle of position pos is pos turns of `turn`: the product wraps at whole turns, so it is
+// reduced exactly in integers.  turn is off by at most 2^-52 of itself (a double's steps), a
+// position below 2^18 by 2^-36 turns.  (In fp64, at 2 operations a clock, the angles of the eight
+// CTAs of a sequence would cost more than its data.)
+
+// One k or v head vector over a warp, as head_norm_rope: x becomes floats that round to a code
+// as the values do.
+template <int D>
+__device__ __forceinline__ void head_norm_rope_to_odd(float (&x)[2][D / 64], const __nv_bfloat16* w,
+                                                      const float2* cs, const float2* cs_l, int n_rot,
+                                                      int lane) {
+    constexpr int kHalf = D / 2;
+    constexpr int kPer = kHalf / 32;
+    float ss = 0.0f, ss_l = 0.0f;   // (the square of a bf16 value is exact)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            const Twofold t = exact_sum(ss, __fmul_rn(x[h][e], x[h][e]));
+            ss = t.h;
+            ss_l += t.l;
+        }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        const Twofold t = exact_sum(ss, __shfl_xor_sync(0xffffffffu, ss, off));
+        ss = t.h;
+        ss_l = __fadd_rn(ss_l, __shfl_xor_sync(0xffffffffu, ss_l, off)) + t.l;
+    }
+    if (!(ss < INFINITY)) ss_l = 0.0f;   // NaN, or beyond fp32
+    constexpr float kInvD = 1.0f / static_cast<float>(D);
+    const Twofold inv = reciprocal_sqrt(add(Twofold{ss * kInvD, ss_l * kInvD}, twofold(1e-6)));
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+        const int i = kPer * lane + e;
+        Twofold a = mul(inv, x[0][e]), b = mul(inv, x[1][e]);
+        if (w) {
+            a = mul(a, __bfloat162float(w[i]));
+            b = mul(b, __bfloat162float(w[kHalf + i]));
+            if (i < n_rot) {
+                const Twofold c{cs[i].x, cs_l[i].x}, s{cs[i].y, cs_l[i].y};
+                const Twofold a0 = a;
+                a = add(mul(a, c), neg(mul(b, s)));
+                b = add(mul(b, c), mul(a0, s));
+            }
+        }
+        x[0][e] = to_odd(a);
+        x[1][e] = to_odd(b);
+    }
 }
 
 template <int D>
@@ -44,7 +88,7 @@ __global__ void __launch_bounds__(kPrepareThreads)
     constexpr int kHalf = D / 2;
     constexpr int kPer = kHalf / 32;   // elements per lane in each half: 4 or 8
     constexpr int kWords = kPer / 4;   // code words per lane in each half
-    __shared__ float2 cs[kPrepareMaxRot];
+    __shared__ float2 cs[kPrepareMaxRot], cs_l[kPrepareMaxRot];   // (cos, sin): both floats of each
 
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
@@ -90,12 +134,17 @@ __global__ void __launch_bounds__(kPrepareThreads)
         scale = (is_k ? c.k_scales : c.v_scales) + scale_row * c.KVH + kvh;
         if (slot > 0) old = *scale;
     }
-    if (tid < p.n_rot) cs[tid] = turn_angle(pos, p.turn[tid]);
+    if (tid < p.n_rot && blockIdx.y * (kPrepareThreads / 32) < p.H + c.KVH) {   // (v is not rotated)
+        Twofold co, si;
+        cos_sin_of_turn(static_cast<uint64_t>(pos) * p.turn[tid], &co, &si);
+        cs[tid] = make_float2(co.h, si.h);
+        cs_l[tid] = make_float2(co.l, si.l);
+    }
     __syncthreads();
     if (!active) return;
 
-    head_norm_rope<D>(x, is_q ? p.w_q : (is_k ? p.w_k : nullptr), cs, p.n_rot, lane);
     if (is_q) {
+        head_norm_rope<D>(x, p.w_q, cs, p.n_rot, lane);
         __nv_bfloat16* dst = p.q_out + (static_cast<size_t>(b) * p.H + vec) * D;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -106,6 +155,7 @@ __global__ void __launch_bounds__(kPrepareThreads)
         return;
     }
 
+    head_norm_rope_to_odd<D>(x, is_k ? p.w_k : nullptr, cs, cs_l, p.n_rot, lane);
     float amax = 0.0f;   // largest finite magnitude
 #pragma unroll
     for (int h = 0; h < 2; ++h)

@@ -347,6 +347,35 @@ def test_producer(layer, paged):
         check_producer(layer, cache, raw, check_lens, q_out)
 
 
+@pytest.mark.parametrize("layer", ["sliding", "global"])
+def test_producer_codes_of_many_tokens(layer):
+    """First tokens of blocks: codes and scales are those of the 64-bit values, except where one
+    lies within 2^-28 (of its row's largest) of a border between two codes.  The producer's sine
+    and cosine are good to 2^-30, which a rotation counts at most sqrt(2) times, 1 / rms and
+    the products to 2^-40, and the angles and the 64-bit reference's own to 2^-38 at 2000."""
+    geo, B, S = GEO[layer], 256, 2000
+    lens = [1 + 16 * int(x) for x in np.random.default_rng(33).integers(0, S // 16, B)]
+    cache = [torch.zeros((B, S, geo["KVH"], geo["D"]), dtype=torch.uint8, device="cuda").view(E4M3)
+             for _ in "kv"]
+    scales = [torch.zeros((B, S // 16, geo["KVH"]), device="cuda") for _ in "kv"]
+    raw = producer_inputs(geo, B, 34)
+    q_out = torch.empty((B, 32, geo["D"]), dtype=torch.bfloat16, device="cuda")
+    gqa.gqa_prepare_decode_quant(raw["q_raw"], raw["k_raw"], raw["v_raw"], raw["w_q"], raw["w_k"],
+                                 i32(lens), q_out, *cache, *scales)
+    at = torch.tensor(lens, device="cuda") - 1
+    every = torch.arange(B, device="cuda")
+    for t, x in enumerate(producer_exact(layer, raw, lens)[1:]):
+        got = ref.VALUES[cache[t].view(torch.uint8)[every, at].cpu().numpy()]
+        s = scales[t][every, at // 16].double().cpu().numpy()
+        amax = np.abs(x).max(-1)
+        low, high = ([[ref.exponent(a * f) for a in row] for row in amax] for f in (1 - 2.0 ** -28, 1 + 2.0 ** -28))
+        assert np.all((s == np.exp2(np.array(low, float))) | (s == np.exp2(np.array(high, float))))
+        scaled, room = x / s[..., None], (amax / s)[..., None] * 2.0 ** -28
+        below, above = ref.e4m3(scaled - room), ref.e4m3(scaled + room)
+        assert np.mean(below != above) < 1e-5
+        assert np.all((got == below) | (got == above))
+
+
 # ---------------------------------------------------------------------------- decode
 
 def expected(cache, q, lens, window, b, h, G):
