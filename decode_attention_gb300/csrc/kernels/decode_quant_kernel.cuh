@@ -39,11 +39,11 @@
 //
 // NC = 4 or 2 (kernels_quant.cu has the rule): larger units leave fewer partials to merge and
 // read longer runs (decode_global_b16_long 905 us against 934, one sliding window of 1024
-// 11.0 against 14.5), smaller ones overlap more ends of pieces, which cost 2-3 us each (B = 128
+// 11.2 against 14.5), smaller ones overlap more ends of pieces, which cost 2-3 us each (B = 128
 // of at most 16, 64 and 256 positions, g = 2: 29.9, 34.7, 45.5 against 20.5, 24.4, 40.6 us; g =
 // 8: 26.2, 28.7, 36.5 against 18.8, 22.4, 35.0).
 //
-// Measured on the way (decode_sliding_b64_paged / decode_global_b64_paged, now 85 / 342 us):
+// Measured on the way (decode_sliding_b64_paged / decode_global_b64_paged, now 86 / 343 us):
 // the 8 warps sharing each tile, with a score tile between the contractions, 171 / 386 us
 // (every warp repeats the softmax of all positions); blocks dealt to the warps in turn and one
 // producer thread, 153 / 447 us (its ~700 cycles per 16 KB are the time HBM takes for them);
