@@ -202,9 +202,22 @@ struct QuantConsumer {
             z[i] = ((c[0][i] + c[1][i]) + (c[2][i] + c[3][i])) * q_undo[i & 1];
     }
 
-    // The rest of a block, from its products z: weights, M, l, and P.V for this warp's dims.  whole:
-    // every row is attended; else rows [first, last) are, and none of them on a bad page.
-    template <bool whole>
+    // Zeroes this warp's dims of the V rows outside [first, last): they hold anything, and 0 * NaN
+    // is NaN.  (As masks on every unit in weigh() it cost 1% of decode_global_b64_paged; a masked
+    // and a whole form of weigh() took 0.2 us more everywhere, by the size of their code.)
+    __device__ static __forceinline__ void clear_rows(uint32_t v_blk, int first, int last, int half, int lane) {
+        const uint32_t v_half = v_blk + half * (kOwnUnits / 8) * 2048;
+        const int r = lane & 15;
+        if (r < first || r >= last) {
+#pragma unroll
+            for (int i = 0; i < kOwnUnits; i += 2)
+                ptx::sts128(unit_addr(v_half, r, i + (lane >> 4)), 0u, 0u, 0u, 0u);
+        }
+        __syncwarp();
+    }
+
+    // The rest of a block, from its products z: weights, M, l, and P.V for this warp's dims.  Rows
+    // [first, last) are attended; bad: their page does not exist, and their weights are NaN.
     __device__ __forceinline__ void weigh(const float (&z)[4], uint32_t v_blk, float k_scale,
                                           float v_scale, int first, int last, bool bad, int half,
                                           int lane) {
@@ -214,14 +227,10 @@ struct QuantConsumer {
         const float f = pow2f(scale_exponent(k_scale)) * kLog2e;
         const int ev = scale_exponent(v_scale);
         // (rows outside the range: 2^-inf)
-        const float evf = static_cast<float>(ev);
-        bool row_ok[2] = {true, true};
-        if (!whole) {
-            row_ok[0] = g >= first && g < last;
-            row_ok[1] = g + 8 >= first && g + 8 < last;
-        }
+        const float evf = bad ? __uint_as_float(0x7fc00000u) : static_cast<float>(ev);
+        const bool row_ok[2] = {g >= first && g < last, g + 8 >= first && g + 8 < last};
         auto level = [&](int i, float shift) {
-            const float v = fmaf(z[i], f, !whole && bad ? __uint_as_float(0x7fc00000u) : shift);
+            const float v = fmaf(z[i], f, shift);
             return row_ok[i >> 1] ? v : -INFINITY;
         };
         float y[4];
@@ -276,17 +285,6 @@ struct QuantConsumer {
                 lo[i] = ptx::movmatrix_trans(lo[i]);
             }
         }
-        // rows outside the range hold anything: their codes are zeroed (0 * NaN)
-        uint32_t mask[2] = {0xffffffffu, 0xffffffffu};
-        if (!whole) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int pos = 8 * i + 2 * t;
-                mask[i] = ((pos >= first && pos < last) ? 0x0000ffffu : 0u) |
-                          ((pos + 1 >= first && pos + 1 < last) ? 0xffff0000u : 0u);
-                if (bad) mask[i] = 0u;
-            }
-        }
         const uint32_t v_half = v_blk + half * (kOwnUnits / 8) * 2048;
 #pragma unroll
         for (int u = 0; u < kOwnUnits; u += 2) {
@@ -295,10 +293,8 @@ struct QuantConsumer {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 uint32_t a0, a1, a2, a3;
-                const uint32_t w0 = whole ? w[2 * i] : w[2 * i] & mask[0];
-                const uint32_t w1 = whole ? w[2 * i + 1] : w[2 * i + 1] & mask[1];
-                ptx::e4m3x4_to_f16x2(__byte_perm(w0, 0u, 0x3120), a0, a1);
-                ptx::e4m3x4_to_f16x2(__byte_perm(w1, 0u, 0x3120), a2, a3);
+                ptx::e4m3x4_to_f16x2(__byte_perm(w[2 * i], 0u, 0x3120), a0, a1);
+                ptx::e4m3x4_to_f16x2(__byte_perm(w[2 * i + 1], 0u, 0x3120), a2, a3);
                 float d[4];
                 if (Pol::kSplitCols) {
                     ptx::mma_f16_16816_zero(d, a0, a1, a2, a3, hi[0], hi[1]);
@@ -653,11 +649,11 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
                 const float ks = un.scales[s][0], vs = un.scales[s][1];
                 const bool bad = kPaged && un.bad[s] != 0;
                 const int first = pc.lo - pos, last = pc.hi - pos;
-                if (first <= 0 && last >= kQuantBlock && !bad)
-                    c.template weigh<true>(z, k_tile + kTileBytes, ks, vs, 0, kQuantBlock, false, half, lane);
-                else
-                    c.template weigh<false>(z, k_tile + kTileBytes, ks, vs, first, last, bad, half, lane);
-                if (SPLIT > 1) ptx::fence_proxy_async_smem();   // the scores, before the next copy
+                const bool part = first > 0 || last < kQuantBlock || bad;
+                if (part) c.clear_rows(k_tile + kTileBytes, first, bad ? 0 : last, half, lane);
+                c.weigh(z, k_tile + kTileBytes, ks, vs, first, last, bad, half, lane);
+                // (the scores and cleared rows, before the next copy)
+                if (SPLIT > 1 || part) ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&un.empty[s]));
                 ++taken;
