@@ -355,7 +355,7 @@ struct QuantConsumer {
                 acc[i][j + 2] *= f;
             }
         }
-        float top[G / kHeadStep], ls[G / kHeadStep];   // of this thread's heads
+        float top[G / kHeadStep], ls[G / kHeadStep], inv[G / kHeadStep];   // of this thread's heads
 #pragma unroll
         for (int k = 0; k < G / kHeadStep; ++k) {
             const int h = k * kHeadStep + tid / (W / 2);
@@ -368,7 +368,14 @@ struct QuantConsumer {
                 const float mw = sm.wm[w][h];
                 ls[k] += (mw == -INFINITY ? 0.0f : ptx::ex2(mw - top[k])) * sm.wl[w][h];
             }
+            inv[k] = slot < 0 ? 1.0f / ls[k] : 1.0f;
+            if (slot >= 0 && half == 0 && tid % (W / 2) == 0)
+                *reinterpret_cast<float2*>(p.ws_ml + (static_cast<size_t>(slot) * G + h) * 2) =
+                    make_float2(top[k], ls[k]);
         }
+        const bool floats = slot >= 0 || p.out_f32;
+        float* to = slot < 0 ? static_cast<float*>(p.out) + out_base
+                             : p.ws_acc + static_cast<size_t>(slot) * G * D;
 #pragma unroll
         for (int r = 0; r < D / Pol::SPLIT / W; ++r) {
             if (2 * t < Pol::kMergeCols) {   // (at kSplitCols t = 1 holds the lo parts' products)
@@ -393,19 +400,14 @@ struct QuantConsumer {
                         s.y += x.y;
                     }
                 const size_t at = static_cast<size_t>(h) * D + half * (D / Pol::SPLIT) + r * W + d;
-                if (slot < 0) {
-                    const float inv = 1.0f / ls[k];
-                    store_out2(p, out_base + at, s.x * inv, s.y * inv);
-                } else {
-                    *reinterpret_cast<float2*>(p.ws_acc + static_cast<size_t>(slot) * G * D + at) = s;
-                    if (half == 0 && r == 0 && d == 0) {
-                        float* ml = p.ws_ml + (static_cast<size_t>(slot) * G + h) * 2;
-                        ml[0] = top[k];
-                        ml[1] = ls[k];
-                    }
-                }
+                if (floats)
+                    *reinterpret_cast<float2*>(to + at) = make_float2(s.x * inv[k], s.y * inv[k]);
+                else
+                    *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + out_base + at) =
+                        __floats2bfloat162_rn(s.x * inv[k], s.y * inv[k]);
             }
-            ptx::named_barrier_sync(bar, Pol::GW * 32);   // wacc is filled again
+            // (wacc is filled again: in the next round, or after the barrier that ends the next piece)
+            if (r + 1 < D / Pol::SPLIT / W) ptx::named_barrier_sync(bar, Pol::GW * 32);
         }
     }
 };
