@@ -37,11 +37,11 @@
 // ahead of its last completion, which a parity cannot tell apart.)  Producer threads walk the
 // schedules and issue the TMA copies, one slot per block.
 //
-// NC = 4 or 2 (kernels_quant.cu has the rule): larger units leave fewer partials to merge and
-// read longer runs (decode_global_b16_long 905 us against 934, one sliding window of 1024
-// 11.2 against 14.5), smaller ones overlap more ends of pieces, which cost 2-3 us each (B = 128
-// of at most 16, 64 and 256 positions, g = 2: 29.9, 34.7, 45.5 against 20.5, 24.4, 40.6 us; g =
-// 8: 26.2, 28.7, 36.5 against 18.8, 22.4, 35.0).
+// NC = 4 or 2 (kernels_quant.cu has the rule and what both measure): larger units leave fewer
+// partials to merge and read longer runs, smaller ones overlap more ends of pieces, which
+// cost 2-3 us each.  A piece of one block takes a warp 3.2 us: 0.7 for q, 1.3 for the block, 1.0
+// for the merge.  Much of that is fetching instructions (each warp is somewhere else in some 20 KB
+// of code), so code that is kept short, with one form for all cases, is faster here.
 //
 // Measured on the way (decode_sliding_b64_paged / decode_global_b64_paged, now 86 / 343 us):
 // the 8 warps sharing each tile, with a score tile between the contractions, 171 / 386 us

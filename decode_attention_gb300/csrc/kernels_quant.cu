@@ -90,10 +90,13 @@ cudaError_t launch_quant(const LaunchArgs& a, bool sliding, bool paged) {
     p.v_scales = a.v_scales;
     p.blocks = static_cast<int>((a.rows + kQuantBlock - 1) / kQuantBlock);
     // Many segments: each CTA meets several pieces, whatever the lengths (which the host does
-    // not know), and smaller units overlap more of their ends.  With two or more segments per
-    // CTA the small units were faster at up to 1024 positions (by 1 .. 40%, the shorter the
-    // more) and 2.5% slower at 4096; with fewer they were slower by up to 30%.
-    const bool many = a.p.B * a.p.KVH >= 2 * a.grid;
+    // not know), and smaller units overlap more of their ends.  In a graph, large / small units:
+    // g = 8 and one segment per CTA (B = 40) at most 16, 256, 1024, 4096 positions 13.7 / 10.4,
+    // 18.8 / 18.6, 28.5 / 28.5, 73.3 / 71.6 us; two (B = 72) 15.1 / 11.7, 25.2 / 23.0, 47.3 / 43.0,
+    // 116.2 / 116.0; with fewer than one, up to 37% slower.  g = 2 and one (B = 10) 8.3 / 8.0,
+    // 11.4 / 11.3, 16.5 / 16.7, 20.6 / 20.8; two (B = 20) 10.9 / 8.3, 14.0 / 13.9, 23.3 / 23.7,
+    // 33.5 / 33.4.
+    const bool many = a.p.B * a.p.KVH >= (sliding ? 2 : 1) * a.grid;
     if (sliding && many)
         return paged ? launch<QuantSlidingMany, true>(a, p) : launch<QuantSlidingMany, false>(a, p);
     if (sliding) return paged ? launch<QuantSliding, true>(a, p) : launch<QuantSliding, false>(a, p);
