@@ -103,6 +103,50 @@ struct QuantPiece {
     int done;       // no more pieces
 };
 
+// The static pieces of one unit of the plan in order, as next_piece gives them: a search and
+// a division for the first (on every call's way to its first copy), steps from there.
+struct StaticWalk {
+    static constexpr int kExtra = QuantPlanTuning::kExtra;
+    uint32_t x, stop;   // the unit's tiles
+    int b, kvh, k;      // the segment that holds tile x, and x's place in it
+
+    __device__ __forceinline__ static int tiles(const PlanSmem& pl, int b) {
+        return kExtra + pl.sn[b] / kQuantBlock;   // (sn is whole blocks)
+    }
+    __device__ __forceinline__ StaticWalk(const PlanSmem& pl, int B, uint32_t first, uint32_t end)
+        : x(first), stop(end), b(0), kvh(0), k(0) {
+        if (x >= stop) return;
+        b = upper_seq(pl.spref, B, x);
+        const uint32_t st = static_cast<uint32_t>(tiles(pl, b)), rel = x - pl.spref[b];
+        kvh = static_cast<int>(rel / st);
+        k = static_cast<int>(rel - static_cast<uint32_t>(kvh) * st);
+    }
+    __device__ __forceinline__ bool next(const PlanSmem& pl, int KVH, int unit, Piece& w) {
+        while (x < stop) {
+            const int st = tiles(pl, b), k0 = k;
+            const int take = min(static_cast<int>(min(stop - x, 0x7fffffffu)), st - k0);
+            w.b = b;
+            w.kvh = kvh;
+            w.p0 = pl.lo[b] + max(k0 - kExtra, 0) * kQuantBlock;
+            w.p1 = pl.lo[b] + (k0 + take - kExtra) * kQuantBlock;
+            w.slot = unit + b * KVH + kvh;
+            x += static_cast<uint32_t>(take);
+            k += take;
+            if (k == st) {
+                k = 0;
+                if (++kvh == KVH) {
+                    kvh = 0;
+                    if (x < stop)
+                        do ++b;
+                        while (pl.sn[b] == 0);   // (ends: tile x is in a later sequence)
+                }
+            }
+            if (k0 + take > kExtra) return true;   // else only tiles without positions
+        }
+        return false;
+    }
+};
+
 template <class Pol>
 struct alignas(1024) QuantSmem {
     static constexpr int kTileBytes = kQuantBlock * Pol::D;
@@ -496,14 +540,14 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
         // The unit's first walks the schedule and publishes each piece; each fills the slots of
         // its rings.  (One thread spends ~700 cycles on 16 KB -- its TMA instructions,
         // the scales, its barriers -- which is the time HBM takes to deliver them.)
+        const uint32_t edge = static_cast<uint32_t>(static_unit_begin(pl, unit + (lane & 1)));
+        StaticWalk walk(pl, B, __shfl_sync(0xffffffffu, edge, 0), __shfl_sync(0xffffffffu, edge, 1));
         if (lane != 0) return;
         constexpr int kFeeds = Pol::kFeeds, kLoads = 2;   // rings of a producer
         const int me = (warp - Pol::kConsumers) % kFeeds;
         const uint64_t policy = ptx::policy_evict_first();
         ptx::fence_proxy_async_smem();   // the plan used the slots
         const bool dynamic = pl.n_dyn > 0;
-        long long x = static_unit_begin(pl, unit);
-        const long long stop = static_unit_begin(pl, unit + 1);
         uint32_t filled[kLoads];   // blocks sent to rings me, me + kFeeds
 #pragma unroll
         for (int k = 0; k < kLoads; ++k) filled[k] = 0;
@@ -514,12 +558,18 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
                 // the description is free once the others have read the one before
                 ok = wait_bounded(piece_empty, (n & 1u) ^ 1u, &sm.abort_flag, p.ws_flags);
                 if (!ok) break;
-                int claimed = -1;
                 Piece w;
-                if (!next_piece<QuantPlanTuning::kExtra>(pl, p, unit, kQuantBlock, dynamic, x, stop, claimed, w)) {
-                    un.piece.done = 1;
-                    ptx::mbar_arrive(piece_full);
-                    break;
+                bool whole = false;   // the piece is its segment
+                if (walk.next(pl, KVH, unit, w)) {
+                    whole = w.p1 - w.p0 == pl.n[w.b];
+                } else {
+                    int claimed = -1;
+                    long long none = 0;
+                    if (!next_piece<QuantPlanTuning::kExtra>(pl, p, unit, kQuantBlock, dynamic, none, 0, claimed, w)) {
+                        un.piece.done = 1;
+                        ptx::mbar_arrive(piece_full);
+                        break;
+                    }
                 }
                 const int L = sm.len[w.b];
                 un.piece.b = b = w.b;
@@ -528,8 +578,7 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
                 un.piece.p1 = w.p1;
                 un.piece.lo = p.window > 0 && L > p.window ? L - p.window : 0;
                 un.piece.hi = L;
-                un.piece.slot =
-                    SegmentParts(pl, w.b, w.kvh, p.dyn_slot_base, kExtra).count() == 1 ? -1 : w.slot;
+                un.piece.slot = whole ? -1 : w.slot;
                 un.piece.done = 0;
                 blk0 = w.p0 / kQuantBlock;
                 blk1 = w.p1 / kQuantBlock;
