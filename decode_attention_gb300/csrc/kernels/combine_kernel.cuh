@@ -31,7 +31,10 @@ constexpr int kCombineBatch = 16;       // pieces whose loads are in flight toge
 // left sliding T = 8 with ~13 items per block, ~15 us)
 constexpr int kCombineBlocksPerSm = 16;
 
-template <int G, int D>
+// kByMaximum: a batch's maximum first, then its weights side by side, in place of a chain of
+// running maxima (the 8-bit cache's kernel, whose m are whole numbers: 16 pieces in
+// a third of the instructions).
+template <int G, int D, bool kByMaximum = false>
 __global__ void __launch_bounds__(kCombineThreads)
     gqa_combine_kernel(const DecodeParams p, int num_segments) {
     const int T = p.T > 1 ? p.T : 1;
@@ -83,19 +86,38 @@ __global__ void __launch_bounds__(kCombineThreads)
                         aj[q] = __ldg(reinterpret_cast<const float4*>(p.ws_acc + sl * R * D) + f4);
                     }
                 }
+                if constexpr (kByMaximum) {
+                    float Mn = M;
 #pragma unroll
-                for (int q = 0; q < kCombineBatch; ++q) {
-                    if (j0 + q >= nparts) break;
-                    const float Mn = fmaxf(M, mj[q]);
-                    // 0 on the first piece (M = -inf); a piece that saw no key weighs 0
-                    const float sc = M == -INFINITY ? 0.0f : exp2f(M - Mn);
-                    const float w = mj[q] == -INFINITY ? 0.0f : exp2f(mj[q] - Mn);
-                    den = den * sc + w * lj[q];
-                    num.x = num.x * sc + w * aj[q].x;
-                    num.y = num.y * sc + w * aj[q].y;
-                    num.z = num.z * sc + w * aj[q].z;
-                    num.w = num.w * sc + w * aj[q].w;
+                    for (int q = 0; q < kCombineBatch; ++q) Mn = fmaxf(Mn, mj[q]);
+                    const float sc = M == -INFINITY ? 0.0f : ptx::ex2(M - Mn);
+                    den *= sc;
+                    num = make_float4(num.x * sc, num.y * sc, num.z * sc, num.w * sc);
+#pragma unroll
+                    for (int q = 0; q < kCombineBatch; ++q) {   // (past nparts: 0 times 0)
+                        const float w = mj[q] == -INFINITY ? 0.0f : ptx::ex2(mj[q] - Mn);
+                        den = fmaf(w, lj[q], den);
+                        num.x = fmaf(w, aj[q].x, num.x);
+                        num.y = fmaf(w, aj[q].y, num.y);
+                        num.z = fmaf(w, aj[q].z, num.z);
+                        num.w = fmaf(w, aj[q].w, num.w);
+                    }
                     M = Mn;
+                } else {
+#pragma unroll
+                    for (int q = 0; q < kCombineBatch; ++q) {
+                        if (j0 + q >= nparts) break;
+                        const float Mn = fmaxf(M, mj[q]);
+                        // 0 on the first piece (M = -inf); a piece that saw no key weighs 0
+                        const float sc = M == -INFINITY ? 0.0f : exp2f(M - Mn);
+                        const float w = mj[q] == -INFINITY ? 0.0f : exp2f(mj[q] - Mn);
+                        den = den * sc + w * lj[q];
+                        num.x = num.x * sc + w * aj[q].x;
+                        num.y = num.y * sc + w * aj[q].y;
+                        num.z = num.z * sc + w * aj[q].z;
+                        num.w = num.w * sc + w * aj[q].w;
+                        M = Mn;
+                    }
                 }
             }
             // no key in any piece: the empty sum (a NaN normaliser from a bad page stays NaN)

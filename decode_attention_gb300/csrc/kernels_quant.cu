@@ -78,7 +78,7 @@ cudaError_t launch(const LaunchArgs& a, const DecodeQuantParams& params) {
     ccfg.gridDim = dim3(static_cast<unsigned>(items < most ? items : most));
     ccfg.blockDim = dim3(kCombineThreads);
     ccfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&ccfg, gqa_combine_kernel<Pol::G, Pol::D>, p.d, segments);
+    return cudaLaunchKernelEx(&ccfg, gqa_combine_kernel<Pol::G, Pol::D, true>, p.d, segments);
 }
 
 }  // namespace
