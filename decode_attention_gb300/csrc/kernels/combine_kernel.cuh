@@ -134,4 +134,96 @@ __global__ void __launch_bounds__(kCombineThreads)
     }
 }
 
+// The same for few segments of many pieces (kByMaximum's arithmetic, T = 1): a block takes
+// 128 outputs, and each of its warps the pieces w, w + 4, ..., so that 64 pieces take one round
+// trip of loads in place of four.
+template <int G, int D>
+__global__ void __launch_bounds__(kCombineThreads)
+    gqa_combine_wide_kernel(const DecodeParams p, int num_segments) {
+    constexpr int kWarps = kCombineThreads / 32;
+    constexpr int kChunks = G * D / 128;   // items per segment
+    __shared__ float part_m[kWarps], part_l[kWarps];
+    __shared__ float4 part[kWarps][32];
+
+    ptx::grid_dependency_wait();
+    ptx::allow_dependent_launch();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.ws_claim = 0u;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int item = blockIdx.x; item < num_segments * kChunks; item += gridDim.x) {
+        const int u = item / kChunks, f4 = (item - u * kChunks) * 32 + lane;
+        const int h = (f4 * 4) / D;
+        const int4 e = p.ws_segs[u];   // first_s, ns_parts, dk0, nd_parts
+        const int nparts = e.y + e.w;
+        if (nparts <= 1) continue;     // (the whole block alike)
+        float M = -INFINITY, den = 0.0f;
+        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j0 = warp; j0 < nparts; j0 += kWarps * kCombineBatch) {
+            float mj[kCombineBatch], lj[kCombineBatch];
+            float4 aj[kCombineBatch];
+            float Mn = M;
+#pragma unroll
+            for (int q = 0; q < kCombineBatch; ++q) {
+                const int j = j0 + q * kWarps;
+                mj[q] = -INFINITY;
+                lj[q] = 0.0f;
+                aj[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (j < nparts) {
+                    const size_t sl = j < e.y
+                                          ? static_cast<size_t>(e.x + j) + u
+                                          : static_cast<size_t>(p.dyn_slot_base) + e.z + (j - e.y);
+                    const float2 ml = __ldg(reinterpret_cast<const float2*>(p.ws_ml) + sl * G + h);
+                    mj[q] = ml.x;
+                    lj[q] = ml.y;
+                    aj[q] = __ldg(reinterpret_cast<const float4*>(p.ws_acc + sl * G * D) + f4);
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < kCombineBatch; ++q) Mn = fmaxf(Mn, mj[q]);
+            const float sc = M == -INFINITY ? 0.0f : ptx::ex2(M - Mn);
+            den *= sc;
+            num = make_float4(num.x * sc, num.y * sc, num.z * sc, num.w * sc);
+#pragma unroll
+            for (int q = 0; q < kCombineBatch; ++q) {
+                const float w = mj[q] == -INFINITY ? 0.0f : ptx::ex2(mj[q] - Mn);
+                den = fmaf(w, lj[q], den);
+                num.x = fmaf(w, aj[q].x, num.x);
+                num.y = fmaf(w, aj[q].y, num.y);
+                num.z = fmaf(w, aj[q].z, num.z);
+                num.w = fmaf(w, aj[q].w, num.w);
+            }
+            M = Mn;
+        }
+        // (128 divides D: the item's outputs are one head's, M and den the warp's)
+        static_assert(D % 128 == 0, "one head per item");
+        if (lane == 0) {
+            part_m[warp] = M;
+            part_l[warp] = den;
+        }
+        part[warp][lane] = num;
+        __syncthreads();
+        if (warp == 0) {
+            float top = part_m[0];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) top = fmaxf(top, part_m[w]);
+            den = 0.0f;
+            num = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = part_m[w] == -INFINITY ? 0.0f : ptx::ex2(part_m[w] - top);
+                const float4 a = part[w][lane];
+                den = fmaf(f, part_l[w], den);
+                num.x = fmaf(f, a.x, num.x);
+                num.y = fmaf(f, a.y, num.y);
+                num.z = fmaf(f, a.z, num.z);
+                num.w = fmaf(f, a.w, num.w);
+            }
+            const float inv = den == 0.0f ? 0.0f : 1.0f / den;
+            store_out4(p, static_cast<size_t>(u) * G * D + 4 * static_cast<size_t>(f4),
+                       make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv));
+        }
+        __syncthreads();   // part is filled again
+    }
+}
+
 }  // namespace gqa

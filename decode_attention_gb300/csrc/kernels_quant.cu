@@ -71,13 +71,20 @@ cudaError_t launch(const LaunchArgs& a, const DecodeQuantParams& params) {
     if (e != cudaSuccess) return e;
 
     const int segments = a.p.B * a.p.KVH;
-    constexpr int kChunksPerSeg = (Pol::G * Pol::D / 4 + kCombineThreads - 1) / kCombineThreads;
-    const int items = segments * kChunksPerSeg;
+    // Up to four of its small items per SM the wide form is faster (up to 1024 / 4096 positions,
+    // narrow and wide: g = 2, B = 1 9.5 / 9.5 and 8.5 / 8.5 us, B = 8 14.1 / 17.9 and 13.9 /
+    // 17.8; g = 8, B = 1 12.4 / 15.1 and 9.6 / 11.2, B = 4 11.7 / 17.1 and 10.6 / 15.0), beyond
+    // that its blocks cost more than they hide (B = 12, g = 2 23.2 and 23.8; B = 6, g = 8 19.4 and
+    // 19.8; B = 36 67 and 73).
+    const bool wide = segments * (Pol::G * Pol::D / 128) <= 4 * grid;
+    const int chunk = wide ? 128 : 4 * kCombineThreads;   // outputs per item
+    const int items = segments * ((Pol::G * Pol::D + chunk - 1) / chunk);
     const int most = kCombineBlocksPerSm * grid;
     cudaLaunchConfig_t ccfg = cfg;
     ccfg.gridDim = dim3(static_cast<unsigned>(items < most ? items : most));
     ccfg.blockDim = dim3(kCombineThreads);
     ccfg.dynamicSmemBytes = 0;
+    if (wide) return cudaLaunchKernelEx(&ccfg, gqa_combine_wide_kernel<Pol::G, Pol::D>, p.d, segments);
     return cudaLaunchKernelEx(&ccfg, gqa_combine_kernel<Pol::G, Pol::D, true>, p.d, segments);
 }
 

@@ -266,3 +266,22 @@ def test_positions_beyond_32_bit_offsets():
         assert np.max(np.abs(got - want)) <= tol
     assert torch.all(k.view(torch.uint8)[:B - 1] == 0)
     assert torch.all(k.view(torch.uint8)[B - 1, :S - n] == 0)
+
+
+@pytest.mark.parametrize("layer,count", [("sliding", 9), ("sliding", 10), ("global", 4), ("global", 5)])
+def test_partials_of_few_and_more_segments(layer, count):
+    """Batches on both sides of the step between the forms of the combine kernel, with pieces
+    in numbers from none (an empty sequence) to dozens."""
+    geo = GEO[layer]
+    lens = [6000 if layer == "global" else 2500, 0, 16, 1100, 333, 1, 1500, 1023, 97, 700][:count]
+    cache = filled(geo, count, max(lens), True, seed=121)
+    q = queries(geo, count, 122)
+    out = run_decode(cache, q, lens, 0, out_dtype=torch.float32)
+    check_decode(cache, q, lens, 0, out)
+    assert torch.all(out[1] == 0)
+    assert torch.equal(out, run_decode(cache, q, lens, 0, out_dtype=torch.float32))
+    bad = cache.table.clone()
+    bad[0, 60] = -1                                    # one piece of many is NaN
+    got = run_decode(cache, q, lens, 0, table=bad, out_dtype=torch.float32)
+    assert torch.all(torch.isnan(got[0])) and torch.equal(got[1:], out[1:])
+    assert gqa.gqa_device_status() == gqa.GQA_DEVICE_BAD_PAGE
