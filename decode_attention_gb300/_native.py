@@ -8,6 +8,7 @@ first call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -193,6 +194,13 @@ class _OnDevice:
 
 def _lib_on(device) -> _OnDevice:
     return _OnDevice(device)
+
+
+def _own_on(stream):
+    """Context in which a call on `stream` makes its tensors (None: the current stream).  The
+    caching allocator hands out memory in the order of the current stream, so a tensor made on
+    another one may still be in use there, and a fill enqueued there is not ordered with the call."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _same_device(ref: torch.Tensor, **tensors):
@@ -643,8 +651,9 @@ def _read_quant(k, v, k_scales, v_scales, block_table, seq_lens, window, k_out, 
     if k_out is None:
         if out_rows is None:
             out_rows = rows if block_table is None else block_table.shape[1] * rows
-        k_out = torch.zeros((B, out_rows, KVH, D), dtype=out_dtype, device=k.device)
-        v_out = torch.zeros_like(k_out)
+        with _own_on(stream):
+            k_out = torch.zeros((B, out_rows, KVH, D), dtype=out_dtype, device=k.device)
+            v_out = torch.zeros_like(k_out)
     dtype = getattr(k_out, "dtype", None)
     try:
         ok = _all_on(dev, dtype, k_out, v_out) and k_out.dim() == 4
@@ -672,7 +681,7 @@ def gqa_read_quant(k: torch.Tensor, v: torch.Tensor, k_scales: torch.Tensor,
     """Values of a contiguous 8-bit cache: returns (k_out, v_out) [B,rows,KVH,D] (bf16 or fp32)
     with row s = position s for the last `window` positions (0: all) of each sequence.  Other
     rows of given outputs are left as they are; new outputs (out_rows rows, default S) start
-    at zero."""
+    at zero and belong to the stream of the call, as an output that another call makes."""
     return _read_quant(k, v, k_scales, v_scales, None, seq_lens, window, k_out, v_out, out_rows,
                        out_dtype, stream)
 
@@ -759,7 +768,8 @@ def _decode_quant(q, k, v, k_scales, v_scales, block_table, seq_lens, window, ou
     _require(Dc == D, "q and the cache must have the same head size")
     _require(seq_lens.shape == (B,), "seq_lens must have B entries")
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=q.device)
+        with _own_on(stream):
+            out = torch.empty(shape, dtype=out_dtype, device=q.device)
     else:
         dtype = getattr(out, "dtype", None)
         if not (_device_of(out) == dev and _all_on(dev, dtype, out)):
