@@ -223,7 +223,8 @@ def new_workspace(B: int, max_seq: int, H: int, KVH: int, D: int, window: int,
     n = gqa_workspace_size(B, max_seq, H, KVH, D, window)
     if n == 0:
         raise GQAError("gqa_workspace_size", GQA_ERR_INVALID_ARGUMENT)
-    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    with _own_on(stream):
+        ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
     gqa_workspace_init(ws, stream)
     return ws
 
@@ -262,7 +263,8 @@ def gqa_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_lens: torc
     _require(tuple(k.shape) == (B, S, KVH, D) and v.shape == k.shape, "k/v shape mismatch")
     _require(seq_lens.shape[0] == B, "seq_lens must have B entries")
     if out is None:
-        out = torch.empty((B, H, D), dtype=out_dtype, device=q.device)
+        with _own_on(stream):
+            out = torch.empty((B, H, D), dtype=out_dtype, device=q.device)
     _check_tensor("out", out, out.dtype, 3)
     _require(tuple(out.shape) == (B, H, D), "out must be [B, H, D]")
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -289,7 +291,8 @@ def gqa_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
     _require(v_pages.shape == k_pages.shape and k_pages.shape[3] == D, "page pool shape mismatch")
     _require(block_table.shape[0] == B and seq_lens.shape[0] == B, "batch size mismatch")
     if out is None:
-        out = torch.empty((B, H, D), dtype=out_dtype, device=q.device)
+        with _own_on(stream):
+            out = torch.empty((B, H, D), dtype=out_dtype, device=q.device)
     _check_tensor("out", out, out.dtype, 3)
     _require(tuple(out.shape) == (B, H, D), "out must be [B, H, D]")
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -317,7 +320,8 @@ def gqa_decode_ring(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_lens:
     _require(tuple(k.shape) == (B, C, KVH, D) and v.shape == k.shape, "k/v shape mismatch")
     _require(seq_lens.shape[0] == B, "seq_lens must have B entries")
     if out is None:
-        out = torch.empty((B, H, D), dtype=out_dtype, device=q.device)
+        with _own_on(stream):
+            out = torch.empty((B, H, D), dtype=out_dtype, device=q.device)
     _check_tensor("out", out, out.dtype, 3)
     _require(tuple(out.shape) == (B, H, D), "out must be [B, H, D]")
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -343,7 +347,8 @@ def gqa_decode_keqv(q: torch.Tensor, v: torch.Tensor, w_k: torch.Tensor, seq_len
     _require(tuple(v.shape) == (B, S, KVH, D) and w_k.shape[0] == D, "v / w_k shape mismatch")
     _require(seq_lens.shape[0] == B, "seq_lens must have B entries")
     if out is None:
-        out = torch.empty((B, H, D), dtype=out_dtype, device=q.device)
+        with _own_on(stream):
+            out = torch.empty((B, H, D), dtype=out_dtype, device=q.device)
     _check_tensor("out", out, out.dtype, 3)
     _require(tuple(out.shape) == (B, H, D), "out must be [B, H, D]")
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -370,7 +375,8 @@ def gqa_decode_keqv_paged(q: torch.Tensor, v_pages: torch.Tensor, w_k: torch.Ten
     _require(v_pages.shape[3] == D and w_k.shape[0] == D, "page pool / w_k shape mismatch")
     _require(block_table.shape[0] == B and seq_lens.shape[0] == B, "batch size mismatch")
     if out is None:
-        out = torch.empty((B, H, D), dtype=out_dtype, device=q.device)
+        with _own_on(stream):
+            out = torch.empty((B, H, D), dtype=out_dtype, device=q.device)
     _check_tensor("out", out, out.dtype, 3)
     _require(tuple(out.shape) == (B, H, D), "out must be [B, H, D]")
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -392,10 +398,11 @@ def gqa_workspace_size_mq(B: int, T: int, H: int, KVH: int, D: int) -> int:
     return int(load_library().gqa_workspace_size_mq(B, T, H, KVH, D))
 
 
-def _mq_out(q, out, out_dtype):
+def _mq_out(q, out, out_dtype, stream):
     B, T, H, D = q.shape
     if out is None:
-        out = torch.empty((B, T, H, D), dtype=out_dtype, device=q.device)
+        with _own_on(stream):
+            out = torch.empty((B, T, H, D), dtype=out_dtype, device=q.device)
     _check_tensor("out", out, out.dtype, 4)
     _require(tuple(out.shape) == (B, T, H, D), "out must be [B, T, H, D]")
     return out
@@ -414,7 +421,7 @@ def gqa_decode_mq(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_lens: t
     _, S, KVH, _ = k.shape
     _require(tuple(k.shape) == (B, S, KVH, D) and v.shape == k.shape, "k/v shape mismatch")
     _require(seq_lens.shape[0] == B, "seq_lens must have B entries")
-    out = _mq_out(q, out, out_dtype)
+    out = _mq_out(q, out, out_dtype, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _same_device(q, k=k, v=v, seq_lens=seq_lens, out=out, workspace=workspace)
     st = _lib_on(q.device).gqa_decode_mq(
@@ -438,7 +445,7 @@ def gqa_decode_mq_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.T
     P, page_size, KVH, _ = k_pages.shape
     _require(v_pages.shape == k_pages.shape and k_pages.shape[3] == D, "page pool shape mismatch")
     _require(block_table.shape[0] == B and seq_lens.shape[0] == B, "batch size mismatch")
-    out = _mq_out(q, out, out_dtype)
+    out = _mq_out(q, out, out_dtype, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _same_device(q, k_pages=k_pages, v_pages=v_pages, block_table=block_table,
                  seq_lens=seq_lens, out=out, workspace=workspace)

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import decode_attention_gb300 as gqa
+from decode_attention_gb300 import inputs
 from tests.test_gpu_quant import GEO, filled, i32, queries, run_decode
 
 pytestmark = pytest.mark.gpu
@@ -60,3 +61,26 @@ def test_outputs_made_on_a_given_stream(paged):
         torch.cuda.synchronize()
         assert torch.equal(got, want)
         assert all(torch.equal(a, b) for a, b in zip(got_kv, want_kv))
+
+
+@pytest.mark.parametrize("layer", ["sliding", "global"])
+def test_bf16_outputs_made_on_a_given_stream(layer):
+    geo = GEO[layer]
+    H, KVH, D = geo["H"], geo["KVH"], geo["D"]
+    case = inputs.contiguous_case(2, 333, H, KVH, D, [40, 333], 203, device="cuda")
+    args = (case["q"], case["k"], case["v"], case["seq_lens"], geo["window"])
+    mq = (torch.stack([case["q"], case["q"]], 1).contiguous(), *args[1:])
+    want, want_mq = gqa.gqa_decode(*args), gqa.gqa_decode_mq(*mq)
+    stream, busy = torch.cuda.Stream(), Busy()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        busy.start()
+        busy.late_fill([want.shape], want.dtype)
+        busy.late_fill([want_mq.shape], want.dtype)
+        ws = gqa.new_workspace(2, 333, H, KVH, D, geo["window"], stream=stream)
+        got = gqa.gqa_decode(*args, workspace=ws, stream=stream)
+        got_mq = gqa.gqa_decode_mq(*mq, stream=stream)
+        stream.synchronize()
+        assert not busy.done.query(), "the current stream was to be busy throughout"
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(got_mq, want_mq)

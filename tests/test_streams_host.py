@@ -94,3 +94,40 @@ def test_outputs_of_the_8_bit_calls(made, call, paged):
     made.clear()
     call(paged)
     assert all(s is None for _, s in made), "the current stream when none is given"
+
+
+def bf16_call(name, **kw):
+    """One of the calls over a bf16 cache, at the smallest shapes it takes."""
+    KVH, D = (4, 512) if "keqv" in name else (16, 256)
+    q = tensor((2, 2, 32, D) if "mq" in name else (2, 32, D), BF16)
+    paged = name.endswith("paged")
+    cache = [tensor((5, 16, KVH, D) if paged else (2, 40, KVH, D), BF16) for _ in "kv"]
+    if "keqv" in name:
+        cache = [cache[0], tensor((D,), BF16)]
+    args = [q, *cache] + ([tensor((2, 3), I32)] if paged else []) + [tensor((2,), I32)]
+    return getattr(gqa, name)(*args, *([] if "keqv" in name else [8]), **kw)
+
+
+@pytest.mark.parametrize("name", ["gqa_decode", "gqa_decode_paged", "gqa_decode_ring", "gqa_decode_keqv",
+                                  "gqa_decode_keqv_paged", "gqa_decode_mq", "gqa_decode_mq_paged"])
+def test_outputs_of_the_bf16_calls(made, name):
+    stream = FakeStream()
+    bf16_call(name, stream=stream)
+    assert [s for _, s in made if s is not None] == [stream]
+    made.clear()
+    bf16_call(name)
+    assert all(s is None for _, s in made)
+
+
+def test_new_workspace(made):
+    """The workspace's zeros are written on the stream that it is made for."""
+    stream = FakeStream()
+    lib = type("Lib", (), {"gqa_workspace_init": lambda *args: gqa.GQA_OK})()
+    size = gqa.gqa_workspace_size(2, 40, 32, 16, 256, 0)
+    with pytest.MonkeyPatch.context() as patch:
+        patch.setattr(_native, "gqa_workspace_size", lambda *args: size)
+        patch.setattr(_native, "load_library", lambda: lib)
+        ws = gqa.new_workspace(2, 40, 32, 16, 256, 0, stream=stream)
+        assert made == [("empty", stream)] and ws.numel() == size
+        gqa.new_workspace(2, 40, 32, 16, 256, 0)
+    assert made[1:] == [("empty", None)]
