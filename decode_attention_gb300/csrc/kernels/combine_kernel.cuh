@@ -120,8 +120,9 @@ __global__ void __launch_bounds__(kCombineThreads)
                     }
                 }
             }
-            // no key in any piece: the empty sum (a NaN normaliser from a bad page stays NaN)
-            const float inv = den == 0.0f ? 0.0f : 1.0f / den;
+            // no key in any piece: the empty sum (a NaN normaliser from a bad page stays NaN).  (By
+            // maximum every piece has keys: no weight at all means scores of -inf, which is NaN.)
+            const float inv = !kByMaximum && den == 0.0f ? 0.0f : 1.0f / den;
             // row t * G + g of segment u = (b, kvh) is output row (b T + t) H + kvh G + g
             // of [B, T, H, D] (for T = 1: u G + g)
             const int KVH = p.KVH;
@@ -218,7 +219,7 @@ __global__ void __launch_bounds__(kCombineThreads)
                 num.z = fmaf(f, a.z, num.z);
                 num.w = fmaf(f, a.w, num.w);
             }
-            const float inv = den == 0.0f ? 0.0f : 1.0f / den;
+            const float inv = 1.0f / den;
             store_out4(p, static_cast<size_t>(u) * G * D + 4 * static_cast<size_t>(f4),
                        make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv));
         }

@@ -8,7 +8,10 @@
 // score, ev moves an exponent.  M is a whole number, at least the running maximum of x
 // less 15: differences of exponents are then exact, the accumulators are rescaled by
 // powers of two (and seldom), and the weights lie in (0, 2^15], where f16 hi + lo parts
-// hold them to 22 bits.
+// hold them to 22 bits.  M is held in two parts, the ceiling of the score that set it and the
+// ev beside it less 12, and x - M is formed part by part: from 2^24 on, where floats have a spacing
+// above 1, a sum of the two would lose ev and could pass 2^15.  The scores themselves are rounded
+// once, to fp32, and equal ones weigh the same whatever their blocks' scales.
 //
 // Both contractions run as warp-level f16 mma (m16n8k16, fp32 accumulate) with the cache
 // as the A operand, so that the g <= 8 query heads of a KV head fill the 8 columns of B
@@ -173,6 +176,7 @@ struct QuantConsumer {
     static constexpr int G = Pol::G, D = Pol::D, kOwnUnits = Pol::kOwnUnits;
     static constexpr float kTop = 15.0f;    // largest exponent of a weight (f16 ends at 2^16)
     static constexpr float kRoom = 3.0f;    // binades left above the maximum when M is set
+    static constexpr float kLowest = -3.402823466e38f;   // ms of no score yet (finite: less it is)
     // Weights of codes below 2^-126 are flushed.  l is at least 2^(11 - 64), so at value scales
     // from 2^kLowExp up the flushed shares are below 2^-41 of it; below, they are taken apart.
     static constexpr int kLowExp = -32;
@@ -180,7 +184,7 @@ struct QuantConsumer {
     uint2 qb[kOwnUnits];         // B fragments of q (column g = head g % G) for this warp's dims
     float q_undo[2];             // undo their scaling for columns 2t and 2t + 1
     float acc[kOwnUnits][4];     // rows: dims 2g (0, 1) and 2g + 1 (2, 3); columns 2t, 2t + 1
-    float m[2];                  // M of columns 2t, 2t + 1
+    float ms[2], me[2];          // M = ms + me of columns 2t, 2t + 1: of the scores, of the scales
     float l[2];                  // this lane's share of their normalisers
 
     // Byte address of 16-byte unit `unit` of row r of a block.
@@ -214,7 +218,8 @@ struct QuantConsumer {
         for (int i = 0; i < kOwnUnits; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-        m[0] = m[1] = -INFINITY;
+        ms[0] = ms[1] = kLowest;
+        me[0] = me[1] = 0.0f;
         l[0] = l[1] = 0.0f;
     }
 
@@ -267,33 +272,34 @@ struct QuantConsumer {
                                           int lane) {
         const int g = lane >> 2, t = lane & 3;
         const int mat = lane >> 3, r = (mat & 1) * 8 + (lane & 7);
-        // log2 of the weights: y = log2(e) score + ev - M, rows g (0, 1) and g + 8 (2, 3)
+        // log2(e) score, rows g (0, 1) and g + 8 (2, 3), rounded once and for all; rows outside the
+        // range weigh 2^-inf
         const float f = pow2f(scale_exponent(k_scale)) * kLog2e;
         const int ev = scale_exponent(v_scale);
-        // (rows outside the range: 2^-inf)
         const float evf = bad ? __uint_as_float(0x7fc00000u) : static_cast<float>(ev);
         const bool row_ok[2] = {g >= first && g < last, g + 8 >= first && g + 8 < last};
-        auto level = [&](int i, float shift) {
-            const float v = fmaf(z[i], f, shift);
-            return row_ok[i >> 1] ? v : -INFINITY;
-        };
-        float y[4];
+        float x[4], y[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            y[i] = level(i, evf - m[i & 1]);
+            x[i] = row_ok[i >> 1] ? __fmul_rn(z[i], f) : -INFINITY;
+            y[i] = (x[i] - ms[i & 1]) + (evf - me[i & 1]);
         }
-        // M moves only when a weight would pass 2^kTop (and on the first block, M = -inf)
+        // M moves only when a weight would pass 2^kTop (and on the first block)
         const float ym = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
         if (__any_sync(0xffffffffu, ym > kTop)) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                float top = fmaxf(level(j, evf), level(j + 2, evf));
+                float top = fmaxf(x[j], x[j + 2]);
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                const float mn = fmaxf(m[j], ceilf(top) - (kTop - kRoom));
+                top = ceilf(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)));
+                const float up = (top - ms[j]) + (evf - (kTop - kRoom) - me[j]);
+                if (up > 0.0f) {   // (never of a NaN)
+                    ms[j] = top;
+                    me[j] = evf - (kTop - kRoom);
+                }
                 // (in two steps for l, which may be near 2^100 when the values so far were tiny)
-                const float dm = mn == m[j] ? 0.0f : fmaxf(m[j] - mn, -252.0f);
+                const float dm = up > 0.0f ? fmaxf(-up, -252.0f) : 0.0f;
                 const float a1 = ptx::ex2(floorf(0.5f * dm)), a2 = ptx::ex2(dm - floorf(0.5f * dm));
                 const float alpha = a1 * a2;
                 l[j] = l[j] * a1 * a2;
@@ -302,9 +308,8 @@ struct QuantConsumer {
                     acc[i][j] *= alpha;
                     acc[i][j + 2] *= alpha;
                 }
-                m[j] = mn;
-                y[j] = level(j, evf - mn);
-                y[j + 2] = level(j + 2, evf - mn);
+                y[j] = (x[j] - ms[j]) + (evf - me[j]);
+                y[j + 2] = (x[j + 2] - ms[j]) + (evf - me[j]);
             }
         }
         uint32_t hi[2], lo[2];   // B fragments: column g, positions (2t, 2t + 1) of each half
@@ -356,6 +361,9 @@ struct QuantConsumer {
     // of D hold the same).  From here on l is in [1, 2) and M has its exponent: between equal
     // shares of the softmax the M of the weights of codes differ by up to 128, and a merge
     // would flush one of them.  l[j] becomes the factor by which the accumulators lag behind M.
+    // M is one float again.  Where that has a spacing above 1 (from 2^24 on) l keeps what M
+    // cannot hold, at most 2^19 either way: l 2^M lies within [2^-1, 2^18] times 2^x of the
+    // largest x, and that x is a float.  ms[j] becomes M.
     __device__ __forceinline__ void finish(typename QuantSmem<Pol>::Unit& sm, int own, int half,
                                            int lane) {
 #pragma unroll
@@ -365,10 +373,11 @@ struct QuantConsumer {
             ls += __shfl_xor_sync(0xffffffffu, ls, 8);
             ls += __shfl_xor_sync(0xffffffffu, ls, 16);
             const int e = ls > 0.0f && ls < INFINITY ? (__float_as_int(ls) >> 23) - 127 : 0;
-            l[j] = pow2f(-e);
-            m[j] += static_cast<float>(e);
+            const float m = ms[j] + (me[j] + static_cast<float>(e));
+            l[j] = pow2f(static_cast<int>(me[j] - (m - ms[j])));
+            ms[j] = m;
             if (half == 0 && lane < 4) {
-                sm.wm[own][2 * lane + j] = m[j];
+                sm.wm[own][2 * lane + j] = m;
                 sm.wl[own][2 * lane + j] = ls * l[j];
             }
         }
@@ -391,8 +400,8 @@ struct QuantConsumer {
             float top = -INFINITY;
 #pragma unroll
             for (int w = 0; w < Pol::NC; ++w) top = fmaxf(top, sm.wm[w][2 * t + j]);
-            // (a warp without a finite score weighs 0; its NaN stay)
-            const float f = m[j] == -INFINITY ? 0.0f : ptx::ex2(m[j] - top) * l[j];
+            // (a warp without a score weighs 0 beside one with; its NaN stay)
+            const float f = ptx::ex2(ms[j] - top) * l[j];
 #pragma unroll
             for (int i = 0; i < kOwnUnits; ++i) {
                 acc[i][j] *= f;
@@ -408,10 +417,7 @@ struct QuantConsumer {
 #pragma unroll
             for (int w = 0; w < Pol::NC; ++w) top[k] = fmaxf(top[k], sm.wm[w][h]);
 #pragma unroll
-            for (int w = 0; w < Pol::NC; ++w) {
-                const float mw = sm.wm[w][h];
-                ls[k] += (mw == -INFINITY ? 0.0f : ptx::ex2(mw - top[k])) * sm.wl[w][h];
-            }
+            for (int w = 0; w < Pol::NC; ++w) ls[k] += ptx::ex2(sm.wm[w][h] - top[k]) * sm.wl[w][h];
             inv[k] = slot < 0 ? 1.0f / ls[k] : 1.0f;
             if (slot >= 0 && half == 0 && tid % (W / 2) == 0)
                 *reinterpret_cast<float2*>(p.ws_ml + (static_cast<size_t>(slot) * G + h) * 2) =
