@@ -177,12 +177,16 @@ struct QuantConsumer {
     static constexpr float kTop = 15.0f;    // largest exponent of a weight (f16 ends at 2^16)
     static constexpr float kRoom = 3.0f;    // binades left above the maximum when M is set
     static constexpr float kLowest = -3.402823466e38f;   // ms of no score yet (finite: less it is)
+    // Scores wait for the keys' scale as 2^-kPark of themselves: a product <q, code> may be up to
+    // 2^147, and with a scale down to 2^-64 the score is a float all the same.  At the other end
+    // what is lost to fp32's smallest numbers is below 2^-60 of a unit after any key scale.
+    static constexpr int kPark = 24;
     // Weights of codes below 2^-126 are flushed.  l is at least 2^(11 - 64), so at value scales
     // from 2^kLowExp up the flushed shares are below 2^-41 of it; below, they are taken apart.
     static constexpr int kLowExp = -32;
 
     uint2 qb[kOwnUnits];         // B fragments of q (column g = head g % G) for this warp's dims
-    float q_undo[2];             // undo their scaling for columns 2t and 2t + 1
+    float q_undo[2];             // undo their scaling for columns 2t and 2t + 1, times 2^-kPark
     float acc[kOwnUnits][4];     // rows: dims 2g (0, 1) and 2g + 1 (2, 3); columns 2t, 2t + 1
     float ms[2], me[2];          // M = ms + me of columns 2t, 2t + 1: of the scores, of the scales
     float l[2];                  // this lane's share of their normalisers
@@ -205,13 +209,13 @@ struct QuantConsumer {
         top = max(top & 0xffffu, top >> 16);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = max(static_cast<int>(top >> 7) - 127, -100);   // |q| < 2^(e + 1)
+        const int e = max(static_cast<int>(top >> 7) - 127, -88);   // |q| < 2^(e + 1)
         const float f = pow2f(14 - e);
 #pragma unroll
         for (int u = 0; u < kOwnUnits; ++u)
             qb[u] = make_uint2(ptx::f16x2_pack(bf16lo(qb[u].x) * f, bf16hi(qb[u].x) * f),
                                ptx::f16x2_pack(bf16lo(qb[u].y) * f, bf16hi(qb[u].y) * f));
-        const float undo = pow2f(e - 14);
+        const float undo = pow2f(e - 14 - kPark);
         q_undo[0] = __shfl_sync(0xffffffffu, undo, 8 * t);
         q_undo[1] = __shfl_sync(0xffffffffu, undo, 8 * t + 4);
 #pragma unroll
@@ -223,8 +227,8 @@ struct QuantConsumer {
         l[0] = l[1] = 0.0f;
     }
 
-    // This warp's share of a block's products <q, code>: rows g (0, 1) and g + 8 (2, 3), columns
-    // 2t, 2t + 1.
+    // This warp's share of a block's products 2^-kPark <q, code>: rows g (0, 1) and g + 8 (2, 3),
+    // columns 2t, 2t + 1.
     __device__ __forceinline__ void scores(uint32_t k_blk, int half, float (&z)[4], int lane) {
         const int mat = lane >> 3, r = (mat & 1) * 8 + (lane & 7);
         float c[4][4];   // four independent chains
@@ -274,7 +278,7 @@ struct QuantConsumer {
         const int mat = lane >> 3, r = (mat & 1) * 8 + (lane & 7);
         // log2(e) score, rows g (0, 1) and g + 8 (2, 3), rounded once and for all; rows outside the
         // range weigh 2^-inf
-        const float f = pow2f(scale_exponent(k_scale)) * kLog2e;
+        const float f = pow2f(scale_exponent(k_scale) + kPark) * kLog2e;
         const int ev = scale_exponent(v_scale);
         const float evf = bad ? __uint_as_float(0x7fc00000u) : static_cast<float>(ev);
         const bool row_ok[2] = {g >= first && g < last, g + 8 >= first && g + 8 < last};

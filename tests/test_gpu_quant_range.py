@@ -129,3 +129,21 @@ def test_scores_beyond_fp32_units(layer, many, sign):
         out = run_decode(cache, q, lens, 0, out_dtype=torch.float32)
         assert int(torch.isfinite(out).logical_not().sum()) == 0, (score, exponent)
         check_winners(cache, out, won)
+
+
+@pytest.mark.parametrize("layer", ["sliding", "global"])
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_queries_and_key_scales_at_opposite_ends(layer, many, sign):
+    """The largest queries with the smallest key scales, and tiny queries with the largest: the
+    scores are finite fp32 numbers, whatever their factors' sizes."""
+    geo, lens = GEO[layer], batch(layer, many)
+    for i, (q7, exponent) in enumerate([(1.5 * 2.0 ** 127, -64), (2.0 ** 126, -63), (2.0 ** 115, -20),
+                                        (2.0 ** -62, 63), (2.0 ** -61, 62)]):
+        cache = RandomCache(geo, len(lens), max(lens), many, 321 + i, 12)
+        q = torch.zeros((len(lens), geo["H"], geo["D"]), dtype=torch.bfloat16, device="cuda")
+        q[..., CHANNEL] = sign * q7
+        won = one_channel_keys(cache, lens, sign * q7, exponent, 331 + i)
+        out = run_decode(cache, q, lens, 0, out_dtype=torch.float32)
+        assert int(torch.isfinite(out).logical_not().sum()) == 0, (q7, exponent)
+        check_winners(cache, out, won)
