@@ -16,8 +16,8 @@
 // Both contractions run as warp-level f16 mma (m16n8k16, fp32 accumulate) with the cache
 // as the A operand, so that the g <= 8 query heads of a KV head fill the 8 columns of B
 // and no row is idle.  e4m3 widens to f16 exactly, two codes per instruction.  q is scaled
-// by a power of two per head, which makes its bf16 values exact in f16 down to 2^-30 of
-// the largest.
+// by a power of two per head, which makes its bf16 values exact in f16 down to 2^-31 of
+// the largest (at g = 8 of the largest in each half of D).
 //   scores  S[pos, h] = K[pos, :] . q[h, :] for the 16 positions of a block; the k index
 //           pairs of an A fragment are the bytes (4t, 4t+1) and (4t+2, 4t+3) of a 16-byte
 //           unit, q's B fragment in the same order

@@ -459,6 +459,9 @@ gqa_status_t gqa_prepare_decode_quant_paged(const void *q_raw, const void *k_raw
  * applied to at least 16 significant bits.  The error is that of an fp32 evaluation
  * relative to the largest value attended in a head, whatever the scales; a channel whose
  * values are all below 2^-20 of that one (of other blocks) has fewer bits of its own.
+ * Elements of q down to 2^-31 of their head's largest count exactly; smaller ones are
+ * rounded to within 2^-39 of it (or 2^-127), which shows where the largest meet zeros in
+ * every key.
  * Everything else -- q, window, out, workspace (the same size), status bits, errors -- is
  * as for gqa_decode and gqa_decode_paged; null or misaligned scales return
  * GQA_ERR_INVALID_ARGUMENT.

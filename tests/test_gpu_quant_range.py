@@ -12,7 +12,7 @@ import pytest
 import torch
 
 from tests import quant_reference as ref
-from tests.test_gpu_quant import E4M3, GEO, run_decode
+from tests.test_gpu_quant import E4M3, GEO, filled, run_decode
 
 pytestmark = pytest.mark.gpu
 
@@ -147,3 +147,32 @@ def test_queries_and_key_scales_at_opposite_ends(layer, many, sign):
         out = run_decode(cache, q, lens, 0, out_dtype=torch.float32)
         assert int(torch.isfinite(out).logical_not().sum()) == 0, (q7, exponent)
         check_winners(cache, out, won)
+
+
+@pytest.mark.parametrize("layer", ["sliding", "global"])
+@pytest.mark.parametrize("small", [False, True])
+def test_query_elements_far_below_their_heads_largest(layer, small):
+    """The head's largest element meets zero codes, so that the others decide.  Down to 2^-31 of
+    it they count exactly: attend_tolerance.  Below, each is off by at most 2^-39 of the largest,
+    a score by that times the sum of |k|, a weight by twice as much."""
+    geo, lens = GEO[layer], [200, 1500]
+    cache = filled(geo, 2, 1500, False, seed=341, spread=1)
+    cache.codes[0].view(torch.uint8)[..., CHANNEL] = 0
+    g = torch.Generator(device="cuda").manual_seed(342)
+    q = torch.rand((2, geo["H"], geo["D"]), generator=g, device="cuda") * 0.25 + 0.125
+    q = torch.where(torch.rand(q.shape, generator=g, device="cuda") < 0.5, -q, q).bfloat16()
+    if small:
+        q = q * 2.0 ** -4
+    q[..., CHANNEL] = 2.0 ** 28
+    out = run_decode(cache, q, lens, 0, out_dtype=torch.float32).double().cpu().numpy()
+    G, qd = geo["H"] // geo["KVH"], q.double().cpu().numpy()
+    for b, L in enumerate(lens):
+        for h in range(cache.KVH):
+            cache.ref[0][b][h].v[:, CHANNEL] = 0.0
+            k, v = (cache.ref[t][b][h].stored(0, L) for t in range(2))
+            heads = qd[b, h * G:(h + 1) * G]
+            tol = ref.attend_tolerance(heads, k, v)
+            if small:
+                tol += 2 * 2.0 ** (28 - 39) * float(np.abs(k).sum(1).max() * np.abs(v).max())
+            worst = float(np.abs(out[b, h * G:(h + 1) * G] - ref.attend(heads, k, v)).max())
+            assert worst <= tol, (b, h)
