@@ -49,7 +49,8 @@ constexpr int kKeqvTcTilesPerCta = 64;
 // [acc_off, ...)      softmax partial acc:    slots x G x D floats
 // slots = kMaxCtas + B * KVH + kMaxDynUnits bounds the partials one call can
 // store: static unit j keeps its piece of segment u at slot j + u, dynamic
-// chunk k at slot kMaxCtas + B * KVH + k.
+// chunk k at slot kMaxCtas + B * KVH + k.  (The 8-bit cache's kernel has several units per
+// CTA: its dynamic chunks start at units + B * KVH, and as many fewer of them fit.)
 // The status word and the counters must be zero before a call; every completed
 // call leaves them so (gqa_device_status zeroes the whole header after a call
 // that raised a status bit, e.g. one that timed out half-way).

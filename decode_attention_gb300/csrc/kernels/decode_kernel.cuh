@@ -234,35 +234,10 @@ struct Piece {
     bool unit_end;
 };
 
-// The CTA's pieces in order: the pieces of consecutive segments in its static unit
-// [x, stop) (static tiles of `tile` positions), then dynamic chunks claimed through the
-// counter (a claim may already be in flight in `claimed`, -1 when not).  Fills `pc` and
-// returns true, or returns false when no piece is left.  One call site per producer
-// keeps the producer's code (and its instruction-cache footprint) small.
-template <int kExtra = 0>
-__device__ __forceinline__ bool next_piece(const PlanSmem& pl, const DecodeParams& p, int cta,
-                                           int tile, bool dynamic, long long& x, long long stop,
-                                           int& claimed, Piece& pc) {
-    const int B = p.B, KVH = p.KVH;
-    while (x < stop) {
-        const int b = upper_seq(pl.spref, B, x);
-        const int st = static_tiles<kExtra>(pl, b);
-        const long long rel = x - pl.spref[b];
-        const int kvh = static_cast<int>(div_floor(rel, st));
-        const int k0 = static_cast<int>(rel - static_cast<long long>(kvh) * st);
-        const int take = static_cast<int>(stop - x < st - k0 ? stop - x : st - k0);
-        x += take;
-        if (kExtra > 0 && k0 + take <= kExtra) continue;   // no positions among them
-        const int e = k0 + take == st ? pl.sn[b] : (k0 + take - kExtra) * tile;
-        pc.b = b;
-        pc.kvh = kvh;
-        pc.p0 = pl.lo[b] + (k0 > kExtra ? k0 - kExtra : 0) * tile;
-        pc.p1 = pl.lo[b] + e;
-        pc.slot = cta + b * KVH + kvh;
-        pc.unit_end = x >= stop;
-        return true;
-    }
-    if (!dynamic) return false;
+// The next dynamic chunk, claimed through the counter (a claim may already be in flight in
+// `claimed`, -1 when not).  Fills `pc` and returns true, or returns false when none is left.
+__device__ __forceinline__ bool claim_piece(const PlanSmem& pl, const DecodeParams& p, int& claimed,
+                                            Piece& pc) {
     if (claimed < 0) claimed = static_cast<int>(atomicAdd(p.ws_claim, 1u));
     const int k = claimed;
     claimed = -1;
@@ -272,7 +247,7 @@ __device__ __forceinline__ bool next_piece(const PlanSmem& pl, const DecodeParam
     const bool is_long = k < pl.n_dyn0;
     const int kk = is_long ? k : k - pl.n_dyn0;
     const uint16_t* pref = is_long ? pl.dpref : pl.dpref1;
-    const int b = upper_seq(pref, B, kk);
+    const int b = upper_seq(pref, p.B, kk);
     const int per = is_long ? pl.dn[b] : pl.dn1[b];
     const int rel = kk - pref[b];
     const int kvh = rel / per;
@@ -286,6 +261,33 @@ __device__ __forceinline__ bool next_piece(const PlanSmem& pl, const DecodeParam
     pc.slot = p.dyn_slot_base + pl.dpref[b] + pl.dpref1[b] + kvh * (pl.dn[b] + pl.dn1[b]) + local;
     pc.unit_end = true;
     return true;
+}
+
+// The CTA's pieces in order: the pieces of consecutive segments in its static unit
+// [x, stop) (static tiles of `tile` positions), then dynamic chunks (claim_piece).  Fills `pc`
+// and returns true, or returns false when no piece is left.  One call site per producer
+// keeps the producer's code (and its instruction-cache footprint) small.
+__device__ __forceinline__ bool next_piece(const PlanSmem& pl, const DecodeParams& p, int cta,
+                                           int tile, bool dynamic, long long& x, long long stop,
+                                           int& claimed, Piece& pc) {
+    if (x < stop) {
+        const int b = upper_seq(pl.spref, p.B, x);
+        const int st = static_tiles(pl, b);
+        const long long rel = x - pl.spref[b];
+        const int kvh = static_cast<int>(div_floor(rel, st));
+        const int k0 = static_cast<int>(rel - static_cast<long long>(kvh) * st);
+        const int take = static_cast<int>(stop - x < st - k0 ? stop - x : st - k0);
+        x += take;
+        const int e = k0 + take == st ? pl.sn[b] : (k0 + take) * tile;
+        pc.b = b;
+        pc.kvh = kvh;
+        pc.p0 = pl.lo[b] + k0 * tile;
+        pc.p1 = pl.lo[b] + e;
+        pc.slot = cta + b * p.KVH + kvh;
+        pc.unit_end = x >= stop;
+        return true;
+    }
+    return dynamic && claim_piece(pl, p, claimed, pc);
 }
 
 // What the producer publishes with every stage.

@@ -106,8 +106,9 @@ struct QuantPiece {
     int done;       // no more pieces
 };
 
-// The static pieces of one unit of the plan in order, as next_piece gives them: a search and
-// a division for the first (on every call's way to its first copy), steps from there.
+// The static pieces of one unit of the plan in order: a search and a division for the first (on
+// every call's way to its first copy), steps from there.  Each segment's tiles begin with kExtra
+// that hold no positions.
 struct StaticWalk {
     static constexpr int kExtra = QuantPlanTuning::kExtra;
     uint32_t x, stop;   // the unit's tiles
@@ -574,8 +575,7 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
                     whole = w.p1 - w.p0 == pl.n[w.b];
                 } else {
                     int claimed = -1;
-                    long long none = 0;
-                    if (!next_piece<QuantPlanTuning::kExtra>(pl, p, unit, kQuantBlock, dynamic, none, 0, claimed, w)) {
+                    if (!dynamic || !claim_piece(pl, p, claimed, w)) {
                         un.piece.done = 1;
                         ptx::mbar_arrive(piece_full);
                         break;
