@@ -31,9 +31,55 @@ constexpr int kCombineBatch = 16;       // pieces whose loads are in flight toge
 // left sliding T = 8 with ~13 items per block, ~15 us)
 constexpr int kCombineBlocksPerSm = 16;
 
-// kByMaximum: a batch's maximum first, then its weights side by side, in place of a chain of
-// running maxima (the 8-bit cache's kernel, whose m are whole numbers: 16 pieces in
-// a third of the instructions).
+// A batch of one segment's partials, as one thread sees them: pieces j0, j0 + kStep, ... below
+// nparts (past it: m = -inf and zeros).
+struct PartialBatch {
+    float m[kCombineBatch], l[kCombineBatch];
+    float4 a[kCombineBatch];
+
+    // e: the segment's partial list; R query rows of D; the outputs [4 f4, 4 f4 + 4) of row h.
+    template <int kStep>
+    __device__ __forceinline__ void load(const DecodeParams& p, const int4& e, int u, int R, int D,
+                                         int h, int f4, int j0, int nparts) {
+#pragma unroll
+        for (int q = 0; q < kCombineBatch; ++q) {
+            const int j = j0 + q * kStep;
+            m[q] = -INFINITY;
+            l[q] = 0.0f;
+            a[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (j < nparts) {
+                const size_t sl = j < e.y ? static_cast<size_t>(e.x + j) + u
+                                          : static_cast<size_t>(p.dyn_slot_base) + e.z + (j - e.y);
+                const float2 ml = __ldg(reinterpret_cast<const float2*>(p.ws_ml) + sl * R + h);
+                m[q] = ml.x;
+                l[q] = ml.y;
+                a[q] = __ldg(reinterpret_cast<const float4*>(p.ws_acc + sl * R * D) + f4);
+            }
+        }
+    }
+    // Adds the batch to (M, den, num): its maximum first, then the weights side by side.
+    __device__ __forceinline__ void add_by_maximum(float& M, float& den, float4& num) const {
+        float Mn = M;
+#pragma unroll
+        for (int q = 0; q < kCombineBatch; ++q) Mn = fmaxf(Mn, m[q]);
+        const float sc = M == -INFINITY ? 0.0f : ptx::ex2(M - Mn);
+        den *= sc;
+        num = make_float4(num.x * sc, num.y * sc, num.z * sc, num.w * sc);
+#pragma unroll
+        for (int q = 0; q < kCombineBatch; ++q) {   // (past nparts: 0 times 0)
+            const float w = m[q] == -INFINITY ? 0.0f : ptx::ex2(m[q] - Mn);
+            den = fmaf(w, l[q], den);
+            num.x = fmaf(w, a[q].x, num.x);
+            num.y = fmaf(w, a[q].y, num.y);
+            num.z = fmaf(w, a[q].z, num.z);
+            num.w = fmaf(w, a[q].w, num.w);
+        }
+        M = Mn;
+    }
+};
+
+// kByMaximum: add_by_maximum in place of a chain of running maxima (the 8-bit cache's kernel,
+// whose m are whole numbers: 16 pieces in a third of the instructions).
 template <int G, int D, bool kByMaximum = false>
 __global__ void __launch_bounds__(kCombineThreads)
     gqa_combine_kernel(const DecodeParams p, int num_segments) {
@@ -68,54 +114,23 @@ __global__ void __launch_bounds__(kCombineThreads)
             float M = -INFINITY, den = 0.0f;
             float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int j0 = 0; j0 < nparts; j0 += kCombineBatch) {
-                float mj[kCombineBatch], lj[kCombineBatch];
-                float4 aj[kCombineBatch];
-#pragma unroll
-                for (int q = 0; q < kCombineBatch; ++q) {
-                    const int j = j0 + q;
-                    mj[q] = -INFINITY;
-                    lj[q] = 0.0f;
-                    aj[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (j < nparts) {
-                        const size_t sl = j < e.y
-                                              ? static_cast<size_t>(e.x + j) + u
-                                              : static_cast<size_t>(p.dyn_slot_base) + e.z + (j - e.y);
-                        const float2 ml = __ldg(reinterpret_cast<const float2*>(p.ws_ml) + sl * R + h);
-                        mj[q] = ml.x;
-                        lj[q] = ml.y;
-                        aj[q] = __ldg(reinterpret_cast<const float4*>(p.ws_acc + sl * R * D) + f4);
-                    }
-                }
+                PartialBatch t;
+                t.load<1>(p, e, u, R, D, h, f4, j0, nparts);
                 if constexpr (kByMaximum) {
-                    float Mn = M;
-#pragma unroll
-                    for (int q = 0; q < kCombineBatch; ++q) Mn = fmaxf(Mn, mj[q]);
-                    const float sc = M == -INFINITY ? 0.0f : ptx::ex2(M - Mn);
-                    den *= sc;
-                    num = make_float4(num.x * sc, num.y * sc, num.z * sc, num.w * sc);
-#pragma unroll
-                    for (int q = 0; q < kCombineBatch; ++q) {   // (past nparts: 0 times 0)
-                        const float w = mj[q] == -INFINITY ? 0.0f : ptx::ex2(mj[q] - Mn);
-                        den = fmaf(w, lj[q], den);
-                        num.x = fmaf(w, aj[q].x, num.x);
-                        num.y = fmaf(w, aj[q].y, num.y);
-                        num.z = fmaf(w, aj[q].z, num.z);
-                        num.w = fmaf(w, aj[q].w, num.w);
-                    }
-                    M = Mn;
+                    t.add_by_maximum(M, den, num);
                 } else {
 #pragma unroll
                     for (int q = 0; q < kCombineBatch; ++q) {
                         if (j0 + q >= nparts) break;
-                        const float Mn = fmaxf(M, mj[q]);
+                        const float Mn = fmaxf(M, t.m[q]);
                         // 0 on the first piece (M = -inf); a piece that saw no key weighs 0
                         const float sc = M == -INFINITY ? 0.0f : exp2f(M - Mn);
-                        const float w = mj[q] == -INFINITY ? 0.0f : exp2f(mj[q] - Mn);
-                        den = den * sc + w * lj[q];
-                        num.x = num.x * sc + w * aj[q].x;
-                        num.y = num.y * sc + w * aj[q].y;
-                        num.z = num.z * sc + w * aj[q].z;
-                        num.w = num.w * sc + w * aj[q].w;
+                        const float w = t.m[q] == -INFINITY ? 0.0f : exp2f(t.m[q] - Mn);
+                        den = den * sc + w * t.l[q];
+                        num.x = num.x * sc + w * t.a[q].x;
+                        num.y = num.y * sc + w * t.a[q].y;
+                        num.z = num.z * sc + w * t.a[q].z;
+                        num.w = num.w * sc + w * t.a[q].w;
                         M = Mn;
                     }
                 }
@@ -160,40 +175,9 @@ __global__ void __launch_bounds__(kCombineThreads)
         float M = -INFINITY, den = 0.0f;
         float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int j0 = warp; j0 < nparts; j0 += kWarps * kCombineBatch) {
-            float mj[kCombineBatch], lj[kCombineBatch];
-            float4 aj[kCombineBatch];
-            float Mn = M;
-#pragma unroll
-            for (int q = 0; q < kCombineBatch; ++q) {
-                const int j = j0 + q * kWarps;
-                mj[q] = -INFINITY;
-                lj[q] = 0.0f;
-                aj[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (j < nparts) {
-                    const size_t sl = j < e.y
-                                          ? static_cast<size_t>(e.x + j) + u
-                                          : static_cast<size_t>(p.dyn_slot_base) + e.z + (j - e.y);
-                    const float2 ml = __ldg(reinterpret_cast<const float2*>(p.ws_ml) + sl * G + h);
-                    mj[q] = ml.x;
-                    lj[q] = ml.y;
-                    aj[q] = __ldg(reinterpret_cast<const float4*>(p.ws_acc + sl * G * D) + f4);
-                }
-            }
-#pragma unroll
-            for (int q = 0; q < kCombineBatch; ++q) Mn = fmaxf(Mn, mj[q]);
-            const float sc = M == -INFINITY ? 0.0f : ptx::ex2(M - Mn);
-            den *= sc;
-            num = make_float4(num.x * sc, num.y * sc, num.z * sc, num.w * sc);
-#pragma unroll
-            for (int q = 0; q < kCombineBatch; ++q) {
-                const float w = mj[q] == -INFINITY ? 0.0f : ptx::ex2(mj[q] - Mn);
-                den = fmaf(w, lj[q], den);
-                num.x = fmaf(w, aj[q].x, num.x);
-                num.y = fmaf(w, aj[q].y, num.y);
-                num.z = fmaf(w, aj[q].z, num.z);
-                num.w = fmaf(w, aj[q].w, num.w);
-            }
-            M = Mn;
+            PartialBatch t;
+            t.load<kWarps>(p, e, u, G, D, h, f4, j0, nparts);
+            t.add_by_maximum(M, den, num);
         }
         // (128 divides D: the item's outputs are one head's, M and den the warp's)
         static_assert(D % 128 == 0, "one head per item");
