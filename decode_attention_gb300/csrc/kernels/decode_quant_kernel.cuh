@@ -46,7 +46,7 @@
 // for the merge.  Much of that is fetching instructions (each warp is somewhere else in some 20 KB
 // of code), so code that is kept short, with one form for all cases, is faster here.
 //
-// Measured on the way (decode_sliding_b64_paged / decode_global_b64_paged, now 86 / 343 us):
+// Measured on the way (decode_sliding_b64_paged / decode_global_b64_paged, now 83-86 / 334-344 us):
 // the 8 warps sharing each tile, with a score tile between the contractions, 171 / 386 us
 // (every warp repeats the softmax of all positions); blocks dealt to the warps in turn and one
 // producer thread, 153 / 447 us (its ~700 cycles per 16 KB are the time HBM takes for them);

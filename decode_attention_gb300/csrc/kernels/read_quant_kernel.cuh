@@ -4,7 +4,9 @@
 //
 // A CTA takes one block of 16 positions of K or V (16 * KVH * D contiguous codes), or a
 // quarter of one when whole blocks would leave SMs idle (kParts); a thread keeps the loads of
-// 8 x 8 codes in flight.  Bound by the memory's read and write rate.
+// 8 x 8 codes in flight.  Bound by the memory's read and write rate: bf16 491 us for 3.18 GB
+// (read_global_b16_paged, the copy rate's 470), fp32 1095 us for 5.30 GB (782), two stores for
+// every load.
 #pragma once
 
 #include "quant_cache.cuh"

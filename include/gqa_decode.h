@@ -433,9 +433,10 @@ gqa_status_t gqa_read_quant_paged(const void *k_pages, const void *v_pages, cons
 
 /*
  * gqa_prepare_decode into the 8-bit cache: the same norms and rotary positions for one
- * new token per sequence, q_out in bf16, the token's key and value coded from the fp32
- * results into position L - 1 under the append's rules (v_raw is required: there is no
- * 8-bit form of the single K=V cache).  Sequences with L < 1 are skipped; a token past
+ * new token per sequence, q_out in bf16, the token's key and value coded into position
+ * L - 1 under the append's rules (v_raw is required: there is no 8-bit form of the single
+ * K=V cache).  Norm, weight and rotation of the key and the value are taken to some 2^-30,
+ * so their codes are those of the exact values but for about one in 10^7.  Sequences with L < 1 are skipped; a token past
  * the capacity or on a page id outside [0, P) is not written.  Errors as for
  * gqa_prepare_decode.
  */
