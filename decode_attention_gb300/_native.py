@@ -210,9 +210,21 @@ def _same_device(ref: torch.Tensor, **tensors):
             _require(t.device == ref.device, f"{name} must be on {ref.device} (q's device)")
 
 
+def _workspace_bytes(workspace) -> int:
+    """Bytes of a workspace from its first element on, never more than its memory holds (the
+    elements of an expanded tensor share theirs)."""
+    if workspace is None:
+        return 0
+    size = workspace.element_size()
+    n = workspace.numel() * size
+    if workspace.is_contiguous():
+        return n
+    return min(n, workspace.untyped_storage().nbytes() - workspace.storage_offset() * size)
+
+
 def gqa_workspace_init(workspace: torch.Tensor, stream=None) -> None:
     """Zero a caller-owned workspace before its first use."""
-    st = load_library().gqa_workspace_init(_ptr(workspace), workspace.numel() * workspace.element_size(),
+    st = load_library().gqa_workspace_init(_ptr(workspace), _workspace_bytes(workspace),
                                            _stream_handle(stream, workspace.device))
     _check("gqa_workspace_init", st)
 
@@ -267,7 +279,7 @@ def gqa_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_lens: torc
             out = torch.empty((B, H, D), dtype=out_dtype, device=q.device)
     _check_tensor("out", out, out.dtype, 3)
     _require(tuple(out.shape) == (B, H, D), "out must be [B, H, D]")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = _workspace_bytes(workspace)
     _same_device(q, k=k, v=v, seq_lens=seq_lens, out=out, workspace=workspace)
     st = _lib_on(q.device).gqa_decode(
         _ptr(q), _ptr(k), _ptr(v), _ptr(seq_lens), B, S, H, KVH, D, int(window), _ptr(out),
@@ -295,7 +307,7 @@ def gqa_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
             out = torch.empty((B, H, D), dtype=out_dtype, device=q.device)
     _check_tensor("out", out, out.dtype, 3)
     _require(tuple(out.shape) == (B, H, D), "out must be [B, H, D]")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = _workspace_bytes(workspace)
     _same_device(q, k_pages=k_pages, v_pages=v_pages, block_table=block_table,
                  seq_lens=seq_lens, out=out, workspace=workspace)
     st = _lib_on(q.device).gqa_decode_paged(
@@ -324,7 +336,7 @@ def gqa_decode_ring(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_lens:
             out = torch.empty((B, H, D), dtype=out_dtype, device=q.device)
     _check_tensor("out", out, out.dtype, 3)
     _require(tuple(out.shape) == (B, H, D), "out must be [B, H, D]")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = _workspace_bytes(workspace)
     _same_device(q, k=k, v=v, seq_lens=seq_lens, out=out, workspace=workspace)
     st = _lib_on(q.device).gqa_decode_ring(
         _ptr(q), _ptr(k), _ptr(v), _ptr(seq_lens), B, C, H, KVH, D, int(window), _ptr(out),
@@ -351,7 +363,7 @@ def gqa_decode_keqv(q: torch.Tensor, v: torch.Tensor, w_k: torch.Tensor, seq_len
             out = torch.empty((B, H, D), dtype=out_dtype, device=q.device)
     _check_tensor("out", out, out.dtype, 3)
     _require(tuple(out.shape) == (B, H, D), "out must be [B, H, D]")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = _workspace_bytes(workspace)
     _same_device(q, v=v, w_k=w_k, seq_lens=seq_lens, out=out, workspace=workspace)
     st = _lib_on(q.device).gqa_decode_keqv(
         _ptr(q), _ptr(v), _ptr(w_k), _ptr(seq_lens), B, S, H, KVH, D, _ptr(out), _out_code(out),
@@ -379,7 +391,7 @@ def gqa_decode_keqv_paged(q: torch.Tensor, v_pages: torch.Tensor, w_k: torch.Ten
             out = torch.empty((B, H, D), dtype=out_dtype, device=q.device)
     _check_tensor("out", out, out.dtype, 3)
     _require(tuple(out.shape) == (B, H, D), "out must be [B, H, D]")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = _workspace_bytes(workspace)
     _same_device(q, v_pages=v_pages, w_k=w_k, block_table=block_table, seq_lens=seq_lens,
                  out=out, workspace=workspace)
     st = _lib_on(q.device).gqa_decode_keqv_paged(
@@ -422,7 +434,7 @@ def gqa_decode_mq(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_lens: t
     _require(tuple(k.shape) == (B, S, KVH, D) and v.shape == k.shape, "k/v shape mismatch")
     _require(seq_lens.shape[0] == B, "seq_lens must have B entries")
     out = _mq_out(q, out, out_dtype, stream)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = _workspace_bytes(workspace)
     _same_device(q, k=k, v=v, seq_lens=seq_lens, out=out, workspace=workspace)
     st = _lib_on(q.device).gqa_decode_mq(
         _ptr(q), _ptr(k), _ptr(v), _ptr(seq_lens), B, T, S, H, KVH, D, int(window), _ptr(out),
@@ -446,7 +458,7 @@ def gqa_decode_mq_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.T
     _require(v_pages.shape == k_pages.shape and k_pages.shape[3] == D, "page pool shape mismatch")
     _require(block_table.shape[0] == B and seq_lens.shape[0] == B, "batch size mismatch")
     out = _mq_out(q, out, out_dtype, stream)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = _workspace_bytes(workspace)
     _same_device(q, k_pages=k_pages, v_pages=v_pages, block_table=block_table,
                  seq_lens=seq_lens, out=out, workspace=workspace)
     st = _lib_on(q.device).gqa_decode_mq_paged(
@@ -786,7 +798,7 @@ def _decode_quant(q, k, v, k_scales, v_scales, block_table, seq_lens, window, ou
     if workspace is not None:
         if workspace.get_device() != dev:
             _same_device(q, workspace=workspace)
-        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        ws, ws_bytes = workspace.data_ptr(), _workspace_bytes(workspace)
     head = (q.data_ptr(), k.data_ptr(), v.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr())
     tail = (H, KVH, D, int(window), out.data_ptr(), _out_code(out), ws, ws_bytes)
     if block_table is None:
