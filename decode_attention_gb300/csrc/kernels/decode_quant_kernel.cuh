@@ -177,7 +177,7 @@ struct QuantConsumer {
     static constexpr int G = Pol::G, D = Pol::D, kOwnUnits = Pol::kOwnUnits;
     static constexpr float kTop = 15.0f;    // largest exponent of a weight (f16 ends at 2^16)
     static constexpr float kRoom = 3.0f;    // binades left above the maximum when M is set
-    static constexpr float kLowest = -3.402823466e38f;   // ms of no score yet (finite: less it is)
+    static constexpr float kLowest = -3.402823466e38f;   // ms of no score yet (differences are numbers)
     // Scores wait for the keys' scale as 2^-kPark of themselves: a product <q, code> may be up to
     // 2^147, and with a scale down to 2^-64 the score is a float all the same.  At the other end
     // what is lost to fp32's smallest numbers is below 2^-60 of a unit after any key scale.
