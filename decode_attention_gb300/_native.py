@@ -39,6 +39,8 @@ GQA_TEST_STALL = 2
 
 PAGE_SIZE = 16
 GQA_MAX_SEQ = 262144   # longest cache (positions) a call accepts
+GQA_NIBBLE_PLANE = 256   # channels of a plane of the 4-bit cache
+GQA_NIBBLE_ROW = 272     # bytes of a plane's row
 
 EXPORTED_SYMBOLS = ("gqa_workspace_size", "gqa_workspace_init", "gqa_decode", "gqa_decode_paged",
                     "gqa_device_status", "gqa_decode_noalloc", "gqa_decode_ring",
@@ -49,6 +51,10 @@ EXPORTED_SYMBOLS = ("gqa_workspace_size", "gqa_workspace_init", "gqa_decode", "g
                     "gqa_read_quant_paged", "gqa_prepare_decode_quant",
                     "gqa_prepare_decode_quant_paged", "gqa_decode_quant",
                     "gqa_decode_quant_paged",
+                    "gqa_append_nibble", "gqa_append_nibble_paged", "gqa_read_nibble",
+                    "gqa_read_nibble_paged", "gqa_prepare_tokens", "gqa_prepare_tokens_paged",
+                    "gqa_prepare_tokens_nibble", "gqa_prepare_tokens_nibble_paged",
+                    "gqa_decode_nibble", "gqa_decode_nibble_paged",
                     "gqa_check_inputs_host", "gqa_noalloc_status", "gqa_decode_keqv_kernel",
                     "gqa_set_test_mode", "gqa_get_test_mode",
                     "gqa_status_string")
@@ -134,6 +140,31 @@ def load_library(build_if_needed: bool = True) -> ctypes.CDLL:
         lib.gqa_decode_quant_paged.argtypes = [vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, ci,
                                                ci, ci, vp, ci, vp, sz, vp]
         lib.gqa_decode_quant_paged.restype = ci
+        lib.gqa_append_nibble.argtypes = [vp, vp, vp, vp, ci, ci, ci, ci, ci, vp, vp]
+        lib.gqa_append_nibble.restype = ci
+        lib.gqa_append_nibble_paged.argtypes = [vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, ci, ci, vp, vp]
+        lib.gqa_append_nibble_paged.restype = ci
+        lib.gqa_read_nibble.argtypes = [vp, vp, ci, ci, ci, ci, ci, vp, vp, ci, ci, vp]
+        lib.gqa_read_nibble.restype = ci
+        lib.gqa_read_nibble_paged.argtypes = [vp, vp, vp, ci, ci, ci, ci, ci, ci, ci, vp, vp, ci, ci, vp]
+        lib.gqa_read_nibble_paged.restype = ci
+        lib.gqa_prepare_tokens.argtypes = [vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, vp, vp, vp,
+                                           ci, ci, vp]
+        lib.gqa_prepare_tokens.restype = ci
+        lib.gqa_prepare_tokens_paged.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci,
+                                                 ci, ci, ci, vp, vp, vp, vp]
+        lib.gqa_prepare_tokens_paged.restype = ci
+        lib.gqa_prepare_tokens_nibble.argtypes = [vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, vp,
+                                                  vp, ci, vp]
+        lib.gqa_prepare_tokens_nibble.restype = ci
+        lib.gqa_prepare_tokens_nibble_paged.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, ci, ci, ci,
+                                                        ci, ci, ci, ci, ci, vp, vp, vp]
+        lib.gqa_prepare_tokens_nibble_paged.restype = ci
+        lib.gqa_decode_nibble.argtypes = [vp, vp, vp, ci, ci, ci, ci, ci, ci, vp, ci, vp, sz, vp]
+        lib.gqa_decode_nibble.restype = ci
+        lib.gqa_decode_nibble_paged.argtypes = [vp, vp, vp, vp, ci, ci, ci, ci, ci, ci, ci, ci, vp,
+                                                ci, vp, sz, vp]
+        lib.gqa_decode_nibble_paged.restype = ci
         lib.gqa_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), vp]
         lib.gqa_device_status.restype = ci
         lib.gqa_check_inputs_host.argtypes = [vp, ci, ci, ci, vp, ci, ci, ctypes.POINTER(ci)]
@@ -828,6 +859,319 @@ def gqa_decode_quant_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torc
     _require(block_table is not None, "block_table is required")
     return _decode_quant(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, window,
                          out, out_dtype, workspace, stream)
+
+
+# ---- the 4-bit cache, and the producer for many tokens ----
+
+_U8 = torch.uint8
+_NIBBLE_GEOMETRY = {16: (16, 256), 8: (4, 512)}   # planes: (KVH, D)
+
+
+def _nibble_specs(kv, block_table):
+    if block_table is None:
+        return (("kv", kv, _U8, 4),)
+    return (("kv_pages", kv, _U8, 4), ("block_table", block_table, torch.int32, 2))
+
+
+def _nibble_on(dev: int, kv, block_table) -> bool:
+    """Device, dtype and number of dims of a 4-bit cache's tensors."""
+    return (_all_on(dev, _U8, kv) and kv.dim() == 4
+            and (block_table is None
+                 or (_all_on(dev, torch.int32, block_table) and block_table.dim() == 2)))
+
+
+def _nibble_shape(kv, B: int, block_table):
+    """(sequences or pages, rows, KVH, D) of a 4-bit cache that passed _nibble_on."""
+    n, planes, rows, size = kv.shape
+    if size != GQA_NIBBLE_ROW or planes not in _NIBBLE_GEOMETRY:
+        raise ValueError(f"a 4-bit cache is [.., planes, rows, {GQA_NIBBLE_ROW}] with "
+                         f"{sorted(_NIBBLE_GEOMETRY)} planes")
+    if block_table is None:
+        _require(n == B, "the cache must hold B sequences")
+    else:
+        _require(block_table.shape[0] == B, "block_table must have B rows")
+    return n, rows, *_NIBBLE_GEOMETRY[planes]
+
+
+def _append_nibble(k_new, v_new, token_offsets, block_table, seq_lens, kv, stream):
+    dev = _device_of(k_new)
+    try:
+        ok = (dev >= 0 and _all_on(dev, _BF16, k_new, v_new) and k_new.dim() == 3
+              and _all_on(dev, torch.int32, token_offsets, seq_lens) and seq_lens.dim() == 1
+              and _nibble_on(dev, kv, block_table))
+    except AttributeError:
+        ok = False
+    if not ok:
+        _refuse(k_new, ("k_new", k_new, _BF16, 3), ("v_new", v_new, _BF16, 3),
+                ("token_offsets", token_offsets, torch.int32, 1),
+                ("seq_lens", seq_lens, torch.int32, 1), *_nibble_specs(kv, block_table))
+    B = seq_lens.shape[0]
+    n, rows, KVH, D = _nibble_shape(kv, B, block_table)
+    _require(token_offsets.shape == (B + 1,), "token_offsets must have B + 1 entries")
+    shape = k_new.shape
+    N = shape[0]
+    _require(shape == (N, KVH, D) and v_new.shape == shape, "k_new / v_new must be [N, KVH, D]")
+    if block_table is None:
+        _call_on(dev, stream, "gqa_append_nibble", k_new.data_ptr(), v_new.data_ptr(),
+                 token_offsets.data_ptr(), seq_lens.data_ptr(), B, N, rows, KVH, D, kv.data_ptr())
+    else:
+        _call_on(dev, stream, "gqa_append_nibble_paged", k_new.data_ptr(), v_new.data_ptr(),
+                 token_offsets.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), B, N, n,
+                 block_table.shape[1], rows, KVH, D, kv.data_ptr())
+
+
+def gqa_append_nibble(k_new: torch.Tensor, v_new: torch.Tensor, token_offsets: torch.Tensor,
+                      seq_lens: torch.Tensor, kv: torch.Tensor, stream=None) -> None:
+    """Quantised append to a contiguous 4-bit cache: rows token_offsets[b] .. token_offsets[b+1]
+    of k_new, v_new [N,KVH,D] (bf16) go to the last positions before seq_lens[b] of kv
+    [B,KVH*D/256,S,272] (uint8)."""
+    _append_nibble(k_new, v_new, token_offsets, None, seq_lens, kv, stream)
+
+
+def gqa_append_nibble_paged(k_new: torch.Tensor, v_new: torch.Tensor, token_offsets: torch.Tensor,
+                            block_table: torch.Tensor, seq_lens: torch.Tensor,
+                            kv_pages: torch.Tensor, stream=None) -> None:
+    """gqa_append_nibble into a page pool [P,KVH*D/256,16,272]."""
+    _require(block_table is not None, "block_table is required")
+    _append_nibble(k_new, v_new, token_offsets, block_table, seq_lens, kv_pages, stream)
+
+
+def _read_nibble(kv, block_table, seq_lens, window, k_out, v_out, out_rows, out_dtype, stream):
+    dev = _device_of(kv)
+    try:
+        ok = (dev >= 0 and _all_on(dev, torch.int32, seq_lens) and seq_lens.dim() == 1
+              and _nibble_on(dev, kv, block_table))
+    except AttributeError:
+        ok = False
+    if not ok:
+        _refuse(kv, ("seq_lens", seq_lens, torch.int32, 1), *_nibble_specs(kv, block_table))
+    B = seq_lens.shape[0]
+    n, rows, KVH, D = _nibble_shape(kv, B, block_table)
+    _require((k_out is None) == (v_out is None), "give both k_out and v_out, or neither")
+    if k_out is None:
+        if out_rows is None:
+            out_rows = rows if block_table is None else block_table.shape[1] * rows
+        with _own_on(stream):
+            k_out = torch.zeros((B, out_rows, KVH, D), dtype=out_dtype, device=kv.device)
+            v_out = torch.zeros_like(k_out)
+    dtype = getattr(k_out, "dtype", None)
+    try:
+        ok = _all_on(dev, dtype, k_out, v_out) and k_out.dim() == 4
+    except AttributeError:
+        ok = False
+    if not ok:
+        _refuse(kv, ("k_out", k_out, dtype, 4), ("v_out", v_out, dtype, 4))
+    R = k_out.shape[1]
+    _require(k_out.shape == (B, R, KVH, D) and v_out.shape == k_out.shape,
+             "k_out / v_out must be [B, rows, KVH, D]")
+    tail = (int(window), k_out.data_ptr(), v_out.data_ptr(), R, _out_code(k_out))
+    if block_table is None:
+        _call_on(dev, stream, "gqa_read_nibble", kv.data_ptr(), seq_lens.data_ptr(), B, rows, KVH, D,
+                 *tail)
+    else:
+        _call_on(dev, stream, "gqa_read_nibble_paged", kv.data_ptr(), block_table.data_ptr(),
+                 seq_lens.data_ptr(), B, n, block_table.shape[1], rows, KVH, D, *tail)
+    return k_out, v_out
+
+
+def gqa_read_nibble(kv: torch.Tensor, seq_lens: torch.Tensor, window: int,
+                    k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None,
+                    out_rows: int | None = None, out_dtype=torch.bfloat16, stream=None):
+    """Values of a contiguous 4-bit cache [B,KVH*D/256,S,272]: returns (k_out, v_out)
+    [B,rows,KVH,D] (bf16 or fp32) with row s = position s for the last `window` positions (0: all)
+    of each sequence.  Other rows of given outputs are left as they are; new outputs (out_rows
+    rows, default S) start at zero and belong to the stream of the call."""
+    return _read_nibble(kv, None, seq_lens, window, k_out, v_out, out_rows, out_dtype, stream)
+
+
+def gqa_read_nibble_paged(kv_pages: torch.Tensor, block_table: torch.Tensor,
+                          seq_lens: torch.Tensor, window: int, k_out: torch.Tensor | None = None,
+                          v_out: torch.Tensor | None = None, out_rows: int | None = None,
+                          out_dtype=torch.bfloat16, stream=None):
+    """gqa_read_nibble from a page pool [P,KVH*D/256,16,272]."""
+    _require(block_table is not None, "block_table is required")
+    return _read_nibble(kv_pages, block_table, seq_lens, window, k_out, v_out, out_rows, out_dtype,
+                        stream)
+
+
+def _producer_inputs(q_raw, k_raw, v_raw, w_q, w_k, token_offsets, seq_lens, q_out):
+    """The producer's inputs and q_out as specs; v_raw may be None."""
+    return (("q_raw", q_raw, _BF16, 3), ("k_raw", k_raw, _BF16, 3),
+            *((("v_raw", v_raw, _BF16, 3),) if v_raw is not None else ()),
+            ("w_q", w_q, _BF16, 1), ("w_k", w_k, _BF16, 1),
+            ("token_offsets", token_offsets, torch.int32, 1),
+            ("seq_lens", seq_lens, torch.int32, 1), ("q_out", q_out, _BF16, 3))
+
+
+def _producer_on(dev: int, specs) -> bool:
+    return all(t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
+               for _, t, dtype, _ in specs)
+
+
+def _producer_shape(specs, KVH: int, D: int):
+    """(B, N, H) of the producer's inputs for a cache of KVH heads of D."""
+    t = {name: tuple(x.shape) for name, x, _, _ in specs}
+    _require(len(t["q_raw"]) == 3 and len(t["seq_lens"]) == 1, "tensor shapes do not fit together")
+    N, H, _ = t["q_raw"]
+    B, = t["seq_lens"]
+    _require(t["q_raw"] == (N, H, D) and t["q_out"] == (N, H, D), "q_raw and q_out must be [N, H, D]")
+    _require(t["k_raw"] == (N, KVH, D) and t.get("v_raw", t["k_raw"]) == (N, KVH, D),
+             "k_raw / v_raw must be [N, KVH, D]")
+    _require(t["w_q"] == (D,) and t["w_k"] == (D,), "w_q / w_k must be [D]")
+    _require(t["token_offsets"] == (B + 1,), "token_offsets must have B + 1 entries")
+    return B, N, H
+
+
+def _prepare_tokens_nibble(q_raw, k_raw, v_raw, w_q, w_k, token_offsets, block_table, seq_lens,
+                           q_out, kv, stream):
+    dev = _device_of(q_raw)
+    _require(v_raw is not None, "v_raw is required")
+    specs = _producer_inputs(q_raw, k_raw, v_raw, w_q, w_k, token_offsets, seq_lens, q_out)
+    try:
+        ok = dev >= 0 and _producer_on(dev, specs) and _nibble_on(dev, kv, block_table)
+    except AttributeError:
+        ok = False
+    if not ok:
+        _refuse(q_raw, *specs, *_nibble_specs(kv, block_table))
+    n, rows, KVH, D = _nibble_shape(kv, seq_lens.numel(), block_table)
+    B, N, H = _producer_shape(specs, KVH, D)
+    head = (q_raw.data_ptr(), k_raw.data_ptr(), v_raw.data_ptr(), w_q.data_ptr(), w_k.data_ptr(),
+            token_offsets.data_ptr())
+    if block_table is None:
+        _call_on(dev, stream, "gqa_prepare_tokens_nibble", *head, seq_lens.data_ptr(), B, N, H, KVH,
+                 D, q_out.data_ptr(), kv.data_ptr(), rows)
+    else:
+        _call_on(dev, stream, "gqa_prepare_tokens_nibble_paged", *head, block_table.data_ptr(),
+                 seq_lens.data_ptr(), B, N, n, block_table.shape[1], rows, H, KVH, D,
+                 q_out.data_ptr(), kv.data_ptr())
+
+
+def gqa_prepare_tokens_nibble(q_raw: torch.Tensor, k_raw: torch.Tensor, v_raw: torch.Tensor,
+                              w_q: torch.Tensor, w_k: torch.Tensor, token_offsets: torch.Tensor,
+                              seq_lens: torch.Tensor, q_out: torch.Tensor, kv: torch.Tensor,
+                              stream=None) -> None:
+    """gqa_prepare_tokens into a contiguous 4-bit cache kv [B,KVH*D/256,S,272] (uint8)."""
+    _prepare_tokens_nibble(q_raw, k_raw, v_raw, w_q, w_k, token_offsets, None, seq_lens, q_out, kv,
+                           stream)
+
+
+def gqa_prepare_tokens_nibble_paged(q_raw: torch.Tensor, k_raw: torch.Tensor, v_raw: torch.Tensor,
+                                    w_q: torch.Tensor, w_k: torch.Tensor,
+                                    token_offsets: torch.Tensor, block_table: torch.Tensor,
+                                    seq_lens: torch.Tensor, q_out: torch.Tensor,
+                                    kv_pages: torch.Tensor, stream=None) -> None:
+    """gqa_prepare_tokens_nibble into a page pool [P,KVH*D/256,16,272]."""
+    _require(block_table is not None, "block_table is required")
+    _prepare_tokens_nibble(q_raw, k_raw, v_raw, w_q, w_k, token_offsets, block_table, seq_lens, q_out,
+                           kv_pages, stream)
+
+
+def _prepare_tokens(q_raw, k_raw, v_raw, w_q, w_k, token_offsets, block_table, seq_lens, q_out, k, v,
+                    ring, stream):
+    dev = _device_of(q_raw)
+    specs = _producer_inputs(q_raw, k_raw, v_raw, w_q, w_k, token_offsets, seq_lens, q_out)
+    kind = "cache" if block_table is None else "pages"
+    caches = ((("k_" + kind, k, _BF16, 4),) if k is not None else ()) + (("v_" + kind, v, _BF16, 4),)
+    if block_table is not None:
+        caches += (("block_table", block_table, torch.int32, 2),)
+    try:
+        ok = dev >= 0 and _producer_on(dev, specs + caches) and v.dim() == 4
+    except AttributeError:
+        ok = False
+    if not ok:
+        _refuse(q_raw, *specs, *caches)
+    n, rows, KVH, D = shape = v.shape
+    _require(k is None or k.shape == shape, "k and v must have the same shape")
+    B, N, H = _producer_shape(specs, KVH, D)
+    k_ptr = None if k is None else k.data_ptr()
+    head = (q_raw.data_ptr(), k_raw.data_ptr(), None if v_raw is None else v_raw.data_ptr(),
+            w_q.data_ptr(), w_k.data_ptr(), token_offsets.data_ptr())
+    if block_table is None:
+        _require(n == B, "the cache must hold B sequences")
+        _call_on(dev, stream, "gqa_prepare_tokens", *head, seq_lens.data_ptr(), B, N, H, KVH, D,
+                 q_out.data_ptr(), k_ptr, v.data_ptr(), rows, 1 if ring else 0)
+    else:
+        _require(block_table.dim() == 2 and block_table.shape[0] == B, "block_table must have B rows")
+        _call_on(dev, stream, "gqa_prepare_tokens_paged", *head, block_table.data_ptr(),
+                 seq_lens.data_ptr(), B, N, n, block_table.shape[1], rows, H, KVH, D,
+                 q_out.data_ptr(), k_ptr, v.data_ptr())
+
+
+def gqa_prepare_tokens(q_raw: torch.Tensor, k_raw: torch.Tensor, v_raw, w_q: torch.Tensor,
+                       w_k: torch.Tensor, token_offsets: torch.Tensor, seq_lens: torch.Tensor,
+                       q_out: torch.Tensor, k_cache, v_cache: torch.Tensor, ring: bool = False,
+                       stream=None) -> None:
+    """gqa_prepare_decode for any number of new tokens per sequence: tokens token_offsets[b] ..
+    token_offsets[b+1] of q_raw [N,H,D], k_raw, v_raw [N,KVH,D] stand at the last positions before
+    seq_lens[b]; q_out [N,H,D] is packed alike, keys and values go to a contiguous cache
+    [B,rows,KVH,D] (a ring of the last `rows` positions when ring).  v_raw None: values = keys."""
+    _prepare_tokens(q_raw, k_raw, v_raw, w_q, w_k, token_offsets, None, seq_lens, q_out, k_cache,
+                    v_cache, ring, stream)
+
+
+def gqa_prepare_tokens_paged(q_raw: torch.Tensor, k_raw: torch.Tensor, v_raw, w_q: torch.Tensor,
+                             w_k: torch.Tensor, token_offsets: torch.Tensor,
+                             block_table: torch.Tensor, seq_lens: torch.Tensor,
+                             q_out: torch.Tensor, k_pages, v_pages: torch.Tensor,
+                             stream=None) -> None:
+    """gqa_prepare_tokens into page pools [P,16,KVH,D] through a block table."""
+    _require(block_table is not None, "block_table is required")
+    _prepare_tokens(q_raw, k_raw, v_raw, w_q, w_k, token_offsets, block_table, seq_lens, q_out,
+                    k_pages, v_pages, False, stream)
+
+
+def _decode_nibble(q, kv, block_table, seq_lens, window, out, out_dtype, workspace, stream):
+    dev = _device_of(q)
+    try:
+        ok = (dev >= 0 and _all_on(dev, _BF16, q) and q.dim() == 3
+              and _all_on(dev, torch.int32, seq_lens) and _nibble_on(dev, kv, block_table))
+    except AttributeError:
+        ok = False
+    if not ok:
+        _refuse(q, ("q", q, _BF16, 3), ("seq_lens", seq_lens, torch.int32, 1),
+                *_nibble_specs(kv, block_table))
+    B, H, D = shape = q.shape
+    n, rows, KVH, Dc = _nibble_shape(kv, B, block_table)
+    _require(Dc == D, "q and the cache must have the same head size")
+    _require(seq_lens.shape == (B,), "seq_lens must have B entries")
+    if out is None:
+        with _own_on(stream):
+            out = torch.empty(shape, dtype=out_dtype, device=q.device)
+    else:
+        dtype = getattr(out, "dtype", None)
+        if not (_device_of(out) == dev and _all_on(dev, dtype, out)):
+            _refuse(q, ("out", out, dtype, 3))
+        _require(out.shape == shape, "out must be [B, H, D]")
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        if workspace.get_device() != dev:
+            _same_device(q, workspace=workspace)
+        ws, ws_bytes = workspace.data_ptr(), _workspace_bytes(workspace)
+    tail = (H, KVH, D, int(window), out.data_ptr(), _out_code(out), ws, ws_bytes)
+    if block_table is None:
+        _call_on(dev, stream, "gqa_decode_nibble", q.data_ptr(), kv.data_ptr(), seq_lens.data_ptr(), B,
+                 rows, *tail)
+    else:
+        _call_on(dev, stream, "gqa_decode_nibble_paged", q.data_ptr(), kv.data_ptr(),
+                 block_table.data_ptr(), seq_lens.data_ptr(), B, n, block_table.shape[1], rows, *tail)
+    return out
+
+
+def gqa_decode_nibble(q: torch.Tensor, kv: torch.Tensor, seq_lens: torch.Tensor, window: int,
+                      out: torch.Tensor | None = None, out_dtype=torch.bfloat16,
+                      workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """gqa_decode over a contiguous 4-bit cache: q [B,H,D] (bf16), kv [B,KVH*D/256,S,272] (uint8),
+    seq_lens int32 [B]."""
+    return _decode_nibble(q, kv, None, seq_lens, window, out, out_dtype, workspace, stream)
+
+
+def gqa_decode_nibble_paged(q: torch.Tensor, kv_pages: torch.Tensor, block_table: torch.Tensor,
+                            seq_lens: torch.Tensor, window: int, out: torch.Tensor | None = None,
+                            out_dtype=torch.bfloat16, workspace: torch.Tensor | None = None,
+                            stream=None) -> torch.Tensor:
+    """gqa_decode_nibble over a page pool [P,KVH*D/256,16,272]."""
+    _require(block_table is not None, "block_table is required")
+    return _decode_nibble(q, kv_pages, block_table, seq_lens, window, out, out_dtype, workspace, stream)
 
 
 def gqa_decode_noalloc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_lens: torch.Tensor,

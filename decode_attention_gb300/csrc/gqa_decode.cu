@@ -219,7 +219,8 @@ gqa_status_t run(const CallShape& c, bool paged, const void* q, const void* k, c
                  uint64_t outer, int capacity, int ring, int num_pages, int max_pages, void* out,
                  gqa_out_dtype_t out_dtype, void* workspace, size_t workspace_bytes,
                  cudaStream_t stream, const void* w_k = nullptr, bool multi_query = false,
-                 const float* k_scales = nullptr, const float* v_scales = nullptr) {
+                 const float* k_scales = nullptr, const float* v_scales = nullptr,
+                 bool nibble = false) {
     if (!gqa::tensor_map_encoder()) return GQA_ERR_CUDA;
     void* ws = nullptr;
     WorkspaceLayout lay;
@@ -260,6 +261,8 @@ gqa_status_t run(const CallShape& c, bool paged, const void* q, const void* k, c
     a.p.test_flags = g_test_mode.load(std::memory_order_relaxed);
     a.grid = grid;
     a.stream = stream;
+    if (nibble)   // 4-bit cache
+        return gqa::launch_nibble(a, c.geo == Geometry::kSliding) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
     if (k_scales) {   // 8-bit cache
         a.k_scales = k_scales;
         a.v_scales = v_scales;
@@ -497,6 +500,39 @@ gqa_status_t gqa_decode_quant_paged(const void* q, const void* k_pages, const vo
                static_cast<uint64_t>(P), max_pages * GQA_PAGE_SIZE, 0, P, max_pages, out,
                out_dtype, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream),
                nullptr, false, k_scales, v_scales);
+}
+
+gqa_status_t gqa_decode_nibble(const void* q, const void* kv, const int32_t* seq_lens, int B, int S,
+                               int H, int KVH, int D, int window, void* out,
+                               gqa_out_dtype_t out_dtype, void* workspace, size_t workspace_bytes,
+                               gqa_stream_t stream) {
+    const CallShape c{geometry_of(H, KVH, D), B, H, KVH, D, window};
+    if (S < 1 || S > GQA_MAX_SEQ) return GQA_ERR_INVALID_ARGUMENT;
+    gqa_status_t st = check_common(c, q, out, seq_lens, out_dtype);
+    if (st != GQA_OK || B == 0) return st;
+    if (!kv || !aligned(kv, 16)) return GQA_ERR_INVALID_ARGUMENT;
+    return run(c, false, q, kv, kv, nullptr, seq_lens, static_cast<uint64_t>(S),
+               static_cast<uint64_t>(B), S, 0, 0, 0, out, out_dtype, workspace, workspace_bytes,
+               reinterpret_cast<cudaStream_t>(stream), nullptr, false, nullptr, nullptr, true);
+}
+
+gqa_status_t gqa_decode_nibble_paged(const void* q, const void* kv_pages,
+                                     const int32_t* block_table, const int32_t* seq_lens, int B,
+                                     int P, int max_pages, int page_size, int H, int KVH, int D,
+                                     int window, void* out, gqa_out_dtype_t out_dtype,
+                                     void* workspace, size_t workspace_bytes, gqa_stream_t stream) {
+    const CallShape c{geometry_of(H, KVH, D), B, H, KVH, D, window};
+    if (page_size != GQA_PAGE_SIZE || P < 1 || max_pages < 1 ||
+        static_cast<int64_t>(max_pages) * GQA_PAGE_SIZE > GQA_MAX_SEQ)
+        return GQA_ERR_INVALID_ARGUMENT;
+    gqa_status_t st = check_common(c, q, out, seq_lens, out_dtype);
+    if (st != GQA_OK || B == 0) return st;
+    if (!kv_pages || !block_table || !aligned(kv_pages, 16) || !aligned(block_table, 4))
+        return GQA_ERR_INVALID_ARGUMENT;
+    return run(c, true, q, kv_pages, kv_pages, block_table, seq_lens, GQA_PAGE_SIZE,
+               static_cast<uint64_t>(P), max_pages * GQA_PAGE_SIZE, 0, P, max_pages, out,
+               out_dtype, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream),
+               nullptr, false, nullptr, nullptr, true);
 }
 
 gqa_status_t gqa_check_inputs_host(const int32_t* seq_lens, int B, int capacity, int window,

@@ -480,6 +480,149 @@ gqa_status_t gqa_decode_quant_paged(const void *q, const void *k_pages, const vo
                                     void *workspace, size_t workspace_bytes, gqa_stream_t stream);
 
 /*
+ * The 4-bit KV cache: 17/64 of a bf16 cache's bytes.  256 channels of one KV head are a
+ * plane: plane h of a slidingDecodeGQA cache is head h, planes 2h and 2h + 1 of a decodeGQA
+ * cache are channels [0, 256) and [256, 512) of head h.  The K and V of a position in a
+ * plane are one row of GQA_NIBBLE_ROW bytes:
+ *     [0, 128)    codes of K, channel 2i in the low half of byte i, 2i + 1 in the high half
+ *     [128, 256)  codes of V
+ *     [256, 264)  scales of K, byte j for the channels [32 j, 32 j + 32)
+ *     [264, 272)  scales of V
+ *   contiguous  kv        uint8 [B, KVH * D / 256, S, 272], row s is position s
+ *   paged       kv_pages  uint8 [P, KVH * D / 256, 16, 272], page p, slot j as elsewhere
+ * A code u in 1 .. 15 stands for (u - 8) * s; s is the f16 number with the bits
+ * (scale byte << 7), of three mantissa bits, at most 60 (byte 0xa7).  Writing takes, for each
+ * 32 channels, the smallest s with amax <= 7.5 s, amax their largest magnitude, and rounds
+ * x / s to the nearest whole number of at most 7, ties away from zero: a value is off by at most
+ * s / 2 (values beyond 450 are clamped to 420; 32 channels below 2^-18 are zeros).  32 channels
+ * with a NaN or an infinity among them are held as NaN (scale byte 0xff, codes 8).  Other
+ * bytes are not written by these calls: a scale byte above 0xa7 reads as NaN in
+ * gqa_read_nibble*, and makes outputs that attend it unspecified in gqa_decode_nibble*; code 0
+ * reads as -8.  No counterpart on the reference pages: a format of this library.
+ *
+ * A row stands by itself: writing a position touches no other, nothing has to be zeroed
+ * before the first use, and no row that was not written is used.  kv is 16-byte aligned.
+ * Geometries: those of gqa_decode.
+ *
+ * Quantised append of K/V rows, already normed and rotated at their positions, packed one
+ * sequence after the other:
+ *
+ *   k_new, v_new   bf16 [N, KVH, D]
+ *   token_offsets  int32 [B + 1] (device), ascending: sequence b's tokens are rows
+ *                  [token_offsets[b], token_offsets[b + 1]) of k_new and v_new
+ *   seq_lens       int32 [B] (device): lengths AFTER the append; with n_b new tokens
+ *                  they go to the positions [L_b - n_b, L_b)
+ * Sequences without new tokens are skipped, and so is a sequence whose offsets lie outside
+ * [0, N] or whose length is below n_b or above the capacity.  A page id outside [0, P)
+ * skips its positions (the decode call then reports it).  The positions written by one call
+ * must be distinct: sequences that share a page must not both write to the same slot of it.
+ * N == 0 or B == 0: GQA_OK, nothing enqueued.  Errors as for gqa_decode and
+ * gqa_decode_paged (N outside [0, 256 * 262144]: GQA_ERR_INVALID_ARGUMENT).
+ * One kernel launch, no workspace.
+ */
+#define GQA_NIBBLE_PLANE 256
+#define GQA_NIBBLE_ROW 272
+
+gqa_status_t gqa_append_nibble(const void *k_new, const void *v_new, const int32_t *token_offsets,
+                               const int32_t *seq_lens, int B, int N, int S, int KVH, int D,
+                               void *kv, gqa_stream_t stream);
+
+gqa_status_t gqa_append_nibble_paged(const void *k_new, const void *v_new,
+                                     const int32_t *token_offsets, const int32_t *block_table,
+                                     const int32_t *seq_lens, int B, int N, int P, int max_pages,
+                                     int page_size, int KVH, int D, void *kv_pages,
+                                     gqa_stream_t stream);
+
+/*
+ * Reading the 4-bit cache back: gqa_read_quant and gqa_read_quant_paged over it.  bf16
+ * outputs are exact.  One kernel launch, no workspace; the same arguments and errors
+ * otherwise.
+ */
+gqa_status_t gqa_read_nibble(const void *kv, const int32_t *seq_lens, int B, int S, int KVH, int D,
+                             int window, void *k_out, void *v_out, int out_rows,
+                             gqa_out_dtype_t out_dtype, gqa_stream_t stream);
+
+gqa_status_t gqa_read_nibble_paged(const void *kv_pages, const int32_t *block_table,
+                                   const int32_t *seq_lens, int B, int P, int max_pages,
+                                   int page_size, int KVH, int D, int window, void *k_out,
+                                   void *v_out, int out_rows, gqa_out_dtype_t out_dtype,
+                                   gqa_stream_t stream);
+
+/*
+ * The producer for any number of new tokens per sequence (prompts, chunks, the draft
+ * tokens of gqa_decode_mq, or one token each): gqa_prepare_decode's norms and rotary
+ * positions, on tokens packed as for gqa_append_quant.
+ *
+ *   q_raw          bf16 [N, H, D], k_raw, v_raw bf16 [N, KVH, D] (v_raw NULL: values = keys, as
+ *                  for gqa_prepare_decode)
+ *   token_offsets  int32 [B + 1] (device), ascending; sequence b's tokens, n_b of them, stand
+ *                  at the positions [L_b - n_b, L_b)
+ *   seq_lens       int32 [B] (device): lengths L_b AFTER the append
+ *   q_out          bf16 [N, H, D], packed alike (with n_b = T for all b it is gqa_decode_mq's
+ *                  q [B, T, H, D])
+ *   k_cache, v_cache  bf16 [B, rows, KVH, D]: position s goes to row s (ring = 0; skipped from
+ *                  `rows` on) or s mod rows (ring = 1; the last `rows` positions of the sequence,
+ *                  earlier ones of the call are skipped); or page pools as for
+ *                  gqa_prepare_decode_paged, where a page id outside [0, P) skips the write
+ * A sequence whose offsets lie outside [0, N] or whose length is below n_b is skipped whole,
+ * its rows of q_out included; a token that is not written to the cache still gets its q_out.
+ * Arithmetic is fp32, the angles' reduction exact; outputs are rounded to bf16 (nearest
+ * even).  The positions written by one call must be distinct.  N == 0 or B == 0: GQA_OK,
+ * nothing enqueued.  One kernel launch, no workspace.  Errors as for gqa_prepare_decode (N
+ * outside [0, 256 * 262144]: GQA_ERR_INVALID_ARGUMENT).
+ */
+gqa_status_t gqa_prepare_tokens(const void *q_raw, const void *k_raw, const void *v_raw,
+                                const void *w_q, const void *w_k, const int32_t *token_offsets,
+                                const int32_t *seq_lens, int B, int N, int H, int KVH, int D,
+                                void *q_out, void *k_cache, void *v_cache, int rows, int ring,
+                                gqa_stream_t stream);
+
+gqa_status_t gqa_prepare_tokens_paged(const void *q_raw, const void *k_raw, const void *v_raw,
+                                      const void *w_q, const void *w_k,
+                                      const int32_t *token_offsets, const int32_t *block_table,
+                                      const int32_t *seq_lens, int B, int N, int P, int max_pages,
+                                      int page_size, int H, int KVH, int D, void *q_out,
+                                      void *k_pages, void *v_pages, gqa_stream_t stream);
+
+/*
+ * gqa_prepare_tokens into the 4-bit cache (v_raw is required).  A key or value is rounded to
+ * bf16 and coded from there by gqa_append_nibble's rule; it is computed to some 2^-30, so its
+ * bf16 number, and with it its code, is that of the exact value but for about one in 10^6.  A
+ * token past the capacity or on a page id outside [0, P) is not written.  One token per
+ * sequence (token_offsets[b] = b) is the decode step's producer for this cache.
+ */
+gqa_status_t gqa_prepare_tokens_nibble(const void *q_raw, const void *k_raw, const void *v_raw,
+                                       const void *w_q, const void *w_k,
+                                       const int32_t *token_offsets, const int32_t *seq_lens,
+                                       int B, int N, int H, int KVH, int D, void *q_out, void *kv,
+                                       int S, gqa_stream_t stream);
+
+gqa_status_t gqa_prepare_tokens_nibble_paged(const void *q_raw, const void *k_raw,
+                                             const void *v_raw, const void *w_q, const void *w_k,
+                                             const int32_t *token_offsets,
+                                             const int32_t *block_table, const int32_t *seq_lens,
+                                             int B, int N, int P, int max_pages, int page_size,
+                                             int H, int KVH, int D, void *q_out, void *kv_pages,
+                                             gqa_stream_t stream);
+
+/*
+ * gqa_decode and gqa_decode_paged over the 4-bit cache: the same attention core on the
+ * values (u - 8) * s.  Scores, softmax and sums are held in fp32, and the weights are
+ * applied to at least 16 significant bits.  Everything else -- q, window, out, workspace
+ * (the same size), status bits, errors -- is as for gqa_decode and gqa_decode_paged.
+ */
+gqa_status_t gqa_decode_nibble(const void *q, const void *kv, const int32_t *seq_lens, int B, int S,
+                               int H, int KVH, int D, int window, void *out,
+                               gqa_out_dtype_t out_dtype, void *workspace, size_t workspace_bytes,
+                               gqa_stream_t stream);
+
+gqa_status_t gqa_decode_nibble_paged(const void *q, const void *kv_pages,
+                                     const int32_t *block_table, const int32_t *seq_lens, int B,
+                                     int P, int max_pages, int page_size, int H, int KVH, int D,
+                                     int window, void *out, gqa_out_dtype_t out_dtype,
+                                     void *workspace, size_t workspace_bytes, gqa_stream_t stream);
+
+/*
  * Host-side check of the device-resident inputs, for tests and debugging: the
  * caller copies seq_lens (and the block table) to host memory and passes them
  * here.  The decode calls never read these arrays on the host (they stay on the
