@@ -262,7 +262,8 @@ gqa_status_t run(const CallShape& c, bool paged, const void* q, const void* k, c
     a.grid = grid;
     a.stream = stream;
     if (nibble)   // 4-bit cache
-        return gqa::launch_nibble(a, c.geo == Geometry::kSliding) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+        return gqa::launch_nibble(a, c.geo == Geometry::kSliding, paged) == cudaSuccess ? GQA_OK
+                                                                                       : GQA_ERR_CUDA;
     if (k_scales) {   // 8-bit cache
         a.k_scales = k_scales;
         a.v_scales = v_scales;

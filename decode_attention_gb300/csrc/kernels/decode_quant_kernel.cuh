@@ -54,6 +54,7 @@
 #pragma once
 
 #include "decode_kernel.cuh"
+#include "piece_walk.cuh"
 #include "quant_cache.cuh"
 
 namespace gqa {
@@ -97,60 +98,6 @@ struct QuantPolicy {
     static_assert(kThreads >= kPlanWarps * 32, "the plan takes eight warps");
 };
 
-// One piece of work.
-struct QuantPiece {
-    int b, kvh;
-    int p0, p1;     // positions, whole blocks
-    int lo, hi;     // attended positions of the sequence
-    int slot;       // workspace slot of the partial; -1: the piece is the whole segment
-    int done;       // no more pieces
-};
-
-// The static pieces of one unit of the plan in order: a search and a division for the first (on
-// every call's way to its first copy), steps from there.  Each segment's tiles begin with kExtra
-// that hold no positions.
-struct StaticWalk {
-    static constexpr int kExtra = QuantPlanTuning::kExtra;
-    uint32_t x, stop;   // the unit's tiles
-    int b, kvh, k;      // the segment that holds tile x, and x's place in it
-
-    __device__ __forceinline__ static int tiles(const PlanSmem& pl, int b) {
-        return kExtra + pl.sn[b] / kQuantBlock;   // (sn is whole blocks)
-    }
-    __device__ __forceinline__ StaticWalk(const PlanSmem& pl, int B, uint32_t first, uint32_t end)
-        : x(first), stop(end), b(0), kvh(0), k(0) {
-        if (x >= stop) return;
-        b = upper_seq(pl.spref, B, x);
-        const uint32_t st = static_cast<uint32_t>(tiles(pl, b)), rel = x - pl.spref[b];
-        kvh = static_cast<int>(rel / st);
-        k = static_cast<int>(rel - static_cast<uint32_t>(kvh) * st);
-    }
-    __device__ __forceinline__ bool next(const PlanSmem& pl, int KVH, int unit, Piece& w) {
-        while (x < stop) {
-            const int st = tiles(pl, b), k0 = k;
-            const int take = min(static_cast<int>(min(stop - x, 0x7fffffffu)), st - k0);
-            w.b = b;
-            w.kvh = kvh;
-            w.p0 = pl.lo[b] + max(k0 - kExtra, 0) * kQuantBlock;
-            w.p1 = pl.lo[b] + (k0 + take - kExtra) * kQuantBlock;
-            w.slot = unit + b * KVH + kvh;
-            x += static_cast<uint32_t>(take);
-            k += take;
-            if (k == st) {
-                k = 0;
-                if (++kvh == KVH) {
-                    kvh = 0;
-                    if (x < stop)
-                        do ++b;
-                        while (pl.sn[b] == 0);   // (ends: tile x is in a later sequence)
-                }
-            }
-            if (k0 + take > kExtra) return true;   // else only tiles without positions
-        }
-        return false;
-    }
-};
-
 template <class Pol>
 struct alignas(1024) QuantSmem {
     static constexpr int kTileBytes = kQuantBlock * Pol::D;
@@ -160,7 +107,7 @@ struct alignas(1024) QuantSmem {
         alignas(8) uint64_t piece_full, piece_empty;
         float scales[Pol::NC * Pol::RING][2];
         int bad[Pol::NC * Pol::RING];            // the block's page id is out of range
-        QuantPiece piece;
+        BlockPiece piece;
         float wm[Pol::NC][8], wl[Pol::NC][8];    // M and l per column of each warp (pair)
         alignas(16) float wacc[Pol::SPLIT][Pol::NC][Pol::kMergeCols][Pol::kMergeStride];   // dims being merged
     };
@@ -559,7 +506,7 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
         // its rings.  (One thread spends ~700 cycles on 16 KB -- its TMA instructions,
         // the scales, its barriers -- which is the time HBM takes to deliver them.)
         const uint32_t edge = static_cast<uint32_t>(static_unit_begin(pl, unit + (lane & 1)));
-        StaticWalk walk(pl, B, __shfl_sync(0xffffffffu, edge, 0), __shfl_sync(0xffffffffu, edge, 1));
+        StaticWalk<QuantPlanTuning> walk(pl, B, __shfl_sync(0xffffffffu, edge, 0), __shfl_sync(0xffffffffu, edge, 1));
         if (lane != 0) return;
         constexpr int kFeeds = Pol::kFeeds, kLoads = 2;   // rings of a producer
         const int me = (warp - Pol::kConsumers) % kFeeds;
@@ -674,7 +621,7 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
     uint32_t taken = 0;   // blocks this warp has processed (its ring's fills, in order)
     for (uint32_t n = 0;; ++n) {
         const bool there = __all_sync(0xffffffffu, wait_bounded(piece_full, n & 1u, &sm.abort_flag, p.ws_flags));
-        QuantPiece pc{};
+        BlockPiece pc{};
         pc.done = 1;
         if (there) pc = un.piece;
         bool gone = pc.done != 0;

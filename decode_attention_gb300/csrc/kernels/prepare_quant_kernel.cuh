@@ -37,12 +37,12 @@ struct PrepareQuantParams {
 // position below 2^18 by 2^-36 turns.  (In fp64, at 2 operations a clock, the angles of the eight
 // CTAs of a sequence would cost more than its data.)
 
-// One k or v head vector over a warp, as head_norm_rope: x becomes floats that round to a code
-// as the values do.
-template <int D>
-__device__ __forceinline__ void head_norm_rope_to_odd(float (&x)[2][D / 64], const __nv_bfloat16* w,
-                                                      const float2* cs, const float2* cs_l, int n_rot,
-                                                      int lane) {
+// One k or v head vector over a warp, as head_norm_rope, in sums of two floats: x becomes what
+// `round` makes of the values (to_odd: floats that round to a code as the values do).
+template <int D, class Round>
+__device__ __forceinline__ void head_norm_rope_twofold(float (&x)[2][D / 64], const __nv_bfloat16* w,
+                                                       const float2* cs, const float2* cs_l, int n_rot,
+                                                       int lane, Round round) {
     constexpr int kHalf = D / 2;
     constexpr int kPer = kHalf / 32;
     float ss = 0.0f, ss_l = 0.0f;   // (the square of a bf16 value is exact)
@@ -77,8 +77,8 @@ __device__ __forceinline__ void head_norm_rope_to_odd(float (&x)[2][D / 64], con
                 b = add(mul(b, c), mul(a0, s));
             }
         }
-        x[0][e] = to_odd(a);
-        x[1][e] = to_odd(b);
+        x[0][e] = round(a);
+        x[1][e] = round(b);
     }
 }
 
@@ -155,7 +155,8 @@ __global__ void __launch_bounds__(kPrepareThreads)
         return;
     }
 
-    head_norm_rope_to_odd<D>(x, is_k ? p.w_k : nullptr, cs, cs_l, p.n_rot, lane);
+    head_norm_rope_twofold<D>(x, is_k ? p.w_k : nullptr, cs, cs_l, p.n_rot, lane,
+                              [](Twofold a) { return to_odd(a); });
     float amax = 0.0f;   // largest finite magnitude
 #pragma unroll
     for (int h = 0; h < 2; ++h)

@@ -7,14 +7,14 @@
 // then v), the next one's load in flight behind each.  Few tokens are shared by several CTAs
 // (blockIdx.y).
 //
-// For the 4-bit cache a k or v vector is rounded to bf16 first, as a row that an append gets, and
-// coded from there.  An fp32 error moves a value over a border between two bf16 numbers once in
-// some 10^4, and one in forty of those goes over a border between codes, a whole step.  Norm,
+// For the 4-bit cache a k or v vector is rounded to fp32 and to bf16, as a row that an append gets,
+// and coded from there.  An fp32 error moves a value over a border between two bf16 numbers once
+// in some 10^4, and one in forty of those goes over a border between codes, a whole step.  Norm,
 // weight and rotation of k and v are therefore taken to some 2^-30 there (twofold.cuh).
 #pragma once
 
 #include "nibble_cache.cuh"
-#include "prepare_quant_kernel.cuh"   // head_norm_rope, head_norm_rope_to_odd
+#include "prepare_quant_kernel.cuh"   // head_norm_rope, head_norm_rope_twofold
 
 namespace gqa {
 
@@ -130,7 +130,8 @@ __global__ void __launch_bounds__(kTokensThreads)
             if (!kNibble || is_q)
                 head_norm_rope<D>(x, w, cst, p.n_rot, lane);
             else
-                head_norm_rope_to_odd<D>(x, w, cst, cst_l, p.n_rot, lane);
+                head_norm_rope_twofold<D>(x, w, cst, cst_l, p.n_rot, lane,
+                                          [](Twofold a) { return fast_sum(a.h, a.l).h; });
 
             uint32_t y[2][kPer / 2];   // in bf16
 #pragma unroll

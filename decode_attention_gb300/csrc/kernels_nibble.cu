@@ -1,29 +1,82 @@
-// Decode attention kernels over the 4-bit cache, both geometries.
+// Decode attention kernels over the 4-bit cache, both geometries, contiguous and paged.
+#include <mutex>
+
+#include "kernels/combine_kernel.cuh"
 #include "kernels/decode_nibble_kernel.cuh"
 #include "launch.h"
 
 namespace gqa {
 
-cudaError_t launch_nibble(const LaunchArgs& a, bool sliding) {
-    DecodeNibbleParams p;
-    p.d = a.p;
-    p.cache.kv = static_cast<uint8_t*>(const_cast<void*>(a.k));
-    p.cache.block_table = a.p.block_table;
-    p.cache.rows = static_cast<int>(a.rows);
-    p.cache.max_pages = a.p.max_pages;
-    p.cache.num_pages = a.p.num_pages;
-    p.cache.planes = sliding ? 16 : 8;
+namespace {
+
+template <class Pol, bool kPaged>
+cudaError_t launch(const LaunchArgs& a, const DecodeNibbleParams& params) {
+    constexpr size_t kSmem = sizeof(NibbleSmem<Pol>) + 128;   // + alignment slack
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+    constexpr int kMaxDevices = 64;
+    static std::once_flag once[kMaxDevices];
+    static cudaError_t attr_err[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    std::call_once(once[dev], [&] {
+        attr_err[dev] = cudaFuncSetAttribute(gqa_decode_nibble_kernel<Pol, kPaged>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(kSmem));
+    });
+    if (attr_err[dev] != cudaSuccess) return attr_err[dev];
+
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.p.B * a.p.KVH));
-    cfg.blockDim = dim3(kDecodeNibbleWarps * 32);
+    // The workspace's kMaxCtas + B KVH + kMaxDynUnits partial slots: this kernel's units take
+    // the first `units` + B KVH, its dynamic chunks the rest (at least a quarter of theirs).
+    constexpr int kMostUnits = kMaxCtas + kMaxDynUnits * 3 / 4;
+    const int grid = a.grid < kMostUnits / Pol::GROUPS ? a.grid : kMostUnits / Pol::GROUPS;
+    const int units = grid * Pol::GROUPS;
+    DecodeNibbleParams p = params;
+    p.d.dyn_slot_base = units + a.p.B * a.p.KVH;
+    p.d.max_dyn = kMaxCtas + kMaxDynUnits - units < kMaxDynUnits ? kMaxCtas + kMaxDynUnits - units
+                                                                 : kMaxDynUnits;
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(Pol::kThreads);
+    cfg.dynamicSmemBytes = kSmem;
     cfg.stream = a.stream;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
-    return sliding ? cudaLaunchKernelEx(&cfg, gqa_decode_nibble_kernel<2, 256>, p)
-                   : cudaLaunchKernelEx(&cfg, gqa_decode_nibble_kernel<8, 512>, p);
+    e = cudaLaunchKernelEx(&cfg, gqa_decode_nibble_kernel<Pol, kPaged>, p);
+    if (e != cudaSuccess) return e;
+
+    // split segments, as over the 8-bit cache (kernels_quant.cu has what both forms measure)
+    const int segments = a.p.B * a.p.KVH;
+    const bool wide = segments * (Pol::G * Pol::D / 128) <= 4 * grid;
+    const int chunk = wide ? 128 : 4 * kCombineThreads;   // outputs per item
+    const int items = segments * ((Pol::G * Pol::D + chunk - 1) / chunk);
+    const int most = kCombineBlocksPerSm * grid;
+    cudaLaunchConfig_t ccfg = cfg;
+    ccfg.gridDim = dim3(static_cast<unsigned>(items < most ? items : most));
+    ccfg.blockDim = dim3(kCombineThreads);
+    ccfg.dynamicSmemBytes = 0;
+    if (wide) return cudaLaunchKernelEx(&ccfg, gqa_combine_wide_kernel<Pol::G, Pol::D>, p.d, segments);
+    return cudaLaunchKernelEx(&ccfg, gqa_combine_kernel<Pol::G, Pol::D, true>, p.d, segments);
+}
+
+}  // namespace
+
+cudaError_t launch_nibble(const LaunchArgs& a, bool sliding, bool paged) {
+    DecodeNibbleParams p;
+    p.d = a.p;
+    p.kv = static_cast<const uint8_t*>(a.k);
+    p.rows = static_cast<int>(a.rows);
+    const bool many = a.p.B * a.p.KVH >= (sliding ? 2 : 1) * a.grid;
+    if (sliding && many)
+        return paged ? launch<NibbleSlidingMany, true>(a, p) : launch<NibbleSlidingMany, false>(a, p);
+    if (sliding) return paged ? launch<NibbleSliding, true>(a, p) : launch<NibbleSliding, false>(a, p);
+    if (many)
+        return paged ? launch<NibbleGlobalMany, true>(a, p) : launch<NibbleGlobalMany, false>(a, p);
+    return paged ? launch<NibbleGlobal, true>(a, p) : launch<NibbleGlobal, false>(a, p);
 }
 
 }  // namespace gqa

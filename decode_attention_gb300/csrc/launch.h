@@ -49,7 +49,7 @@ size_t smem_bytes_mq(bool sliding);
 cudaError_t launch_quant(const LaunchArgs& a, bool sliding, bool paged);
 
 // Decode over the 4-bit cache: a.k is the cache.
-cudaError_t launch_nibble(const LaunchArgs& a, bool sliding);
+cudaError_t launch_nibble(const LaunchArgs& a, bool sliding, bool paged);
 
 // SM count of the current device (cached per device), or 0.
 int device_sms();

@@ -586,8 +586,8 @@ gqa_status_t gqa_prepare_tokens_paged(const void *q_raw, const void *k_raw, cons
 
 /*
  * gqa_prepare_tokens into the 4-bit cache (v_raw is required).  A key or value is rounded to
- * bf16 and coded from there by gqa_append_nibble's rule; it is computed to some 2^-30, so its
- * bf16 number, and with it its code, is that of the exact value but for about one in 10^6.  A
+ * fp32, from there to bf16, and coded by gqa_append_nibble's rule; it is computed to some
+ * 2^-30, so its bf16 number is that of the exact value but for about one in 10^6.  A
  * token past the capacity or on a page id outside [0, P) is not written.  One token per
  * sequence (token_offsets[b] = b) is the decode step's producer for this cache.
  */

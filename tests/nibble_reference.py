@@ -64,7 +64,9 @@ def norm_rope(x, w, pos, pairs, theta):
 
 
 def bf16(x: np.ndarray) -> np.ndarray:
-    """Nearest bf16 number, ties to even, of finite values away from the ends of the range."""
+    """Finite values away from the ends of the range rounded to fp32 and from there to bf16, each to
+    nearest even (the fp32 step counts where it ends on a tie)."""
+    x = np.asarray(x).astype(np.float32).astype(np.float64)
     _, e = np.frexp(x)
     unit = np.exp2(e - 8.0)
     return np.rint(x / unit) * unit

@@ -388,6 +388,67 @@ def mode(flags):
         gqa.gqa_set_test_mode(prev)
 
 
+FEW, MANY = "few", "many"
+
+
+def batch(layer, count, lens):
+    """`lens`, for MANY padded with short lengths to at least 2 * 152 segments: another form of the call."""
+    B = 24 if layer == "sliding" else 80
+    return lens + [(37 * i) % 150 for i in range(B - len(lens))] if count == MANY else lens
+
+
+@pytest.mark.parametrize("layer", ["sliding", "global"])
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("count", [FEW, MANY])
+def test_one_piece_per_segment_agrees(layer, paged, count):
+    """Split segments and their merge against GQA_TEST_SINGLE_PIECE, which has none: each within the
+    tolerance of the reference."""
+    geo = GEO[layer]
+    lens = batch(layer, count, [1500, 33, 700, 0, 16])
+    cache = filled(geo, len(lens), 1500, paged, 103)
+    q = queries(geo, len(lens), 104)
+    ws = gqa.new_workspace(len(lens), 1504, geo["H"], geo["KVH"], geo["D"], 0)
+    segments = len(lens) * geo["KVH"]
+
+    def pieces():
+        torch.cuda.synchronize()
+        e = ws[256:256 + 16 * segments].view(torch.int32).reshape(segments, 4).cpu().numpy()
+        return (e[:, 1] + e[:, 3]).max()
+
+    skip = [b for b in range(len(lens)) if b > 4 and b % 7]
+    out = run(cache, q, lens, 0, out_dtype=torch.float32, workspace=ws)
+    assert pieces() > 1
+    check(cache, q, lens, 0, out, skip)
+    with mode(gqa.GQA_TEST_SINGLE_PIECE):
+        out = run(cache, q, lens, 0, out_dtype=torch.float32, workspace=ws)
+    assert pieces() == 1
+    check(cache, q, lens, 0, out, skip)
+
+
+@pytest.mark.parametrize("layer", ["sliding", "global"])
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("count", [FEW, MANY])
+def test_stalled_call_takes_the_timeout_exit(layer, paged, count):
+    """GQA_TEST_STALL: a producer waits 1 ms on a barrier that nothing completes.  The call ends, the
+    status says so, and the workspace serves the next call."""
+    geo = GEO[layer]
+    lens = batch(layer, count, [1, 700, 2100, 3000])
+    cache = filled(geo, len(lens), 3000, paged, 105)
+    q = queries(geo, len(lens), 106)
+    ws = gqa.new_workspace(len(lens), 3008, geo["H"], geo["KVH"], geo["D"], 0)
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    with mode(gqa.GQA_TEST_STALL):
+        run(cache, q, lens, 0, workspace=ws)
+    torch.cuda.synchronize()
+    assert time.perf_counter() - t0 < 1.0
+    assert gqa.gqa_device_status(ws) & gqa.GQA_DEVICE_WAIT_TIMEOUT
+    for _ in range(2):
+        out = run(cache, q, lens, 0, out_dtype=torch.float32, workspace=ws)
+        check(cache, q, lens, 0, out, [b for b in range(len(lens)) if b > 3 and b % 7])
+    assert gqa.gqa_device_status(ws) == 0
+
+
 def test_neighbours_stay_as_they_were():
     """The 8-bit and bf16 calls beside the new ones, on one workspace in turn."""
     geo = GEO["sliding"]
