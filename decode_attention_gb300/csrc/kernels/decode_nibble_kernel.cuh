@@ -1,33 +1,32 @@
 // Decode attention over the 4-bit cache (nibble_cache.cuh): attn.core of the gemma-4-31B Model
 // Spec for one new token per sequence.
 //
-// Mathematics.  With x_s = log2(e) <q, k_s> the weights are 2^(x_s - M + 12), M a whole number at
-// most 3 below the running maximum and never above what it was; o = sum of weights times v_s over the
-// sum of weights.  The accumulators are rescaled by powers of two, and seldom; weights lie in (0, 2^15],
-// where f16 hi + lo parts hold them to 22 bits.  The 12 stands apart from M, so that scores of 2^24
-// and more, where floats have a spacing above 1, need no sum of the two.
+// Mathematics.  With x_s = log2(e) <q, k_s> the weights are 2^(x_s - M); o = sum of weights times v_s
+// over the sum of weights, for any M.  M is a whole number, set 8 below a maximum (rounded up, so that
+// from 2^24 on, where floats have a spacing above 1, it is at most 8 below) and kept until a weight
+// would pass 2^15: the accumulators are rescaled by powers of two, and seldom.  Weights lie in
+// (0, 2^15], where f16 hi + lo parts hold them to 22 bits, or to 2^-25 of a unit, 2^-33 of the largest.
 //
 // Both contractions run as warp-level f16 mma (m16n8k16, fp32 accumulate) with the cache as the A
-// operand, so that the g <= 8 query heads of a KV head fill the 8 columns of B.  A value
-// (u - 8) s is exact in f16 and takes one fma of two codes: the codes j and j + 4 of a word (or code j
-// of two positions) lie in the low four bits of its halves, and 0x6400 | u is the f16 number
-// 1024 + u, so the value is (1024 + u) s - 1032 s; codes one place up are 1024 + 16 u, times
-// s / 16, less 72 s; a shift by 8 brings the rest.  (With bf16 in place of f16, whose 7 bits of
-// mantissa leave no room for a second place, it takes three shifts for a word and not one.)  The
-// constants are exact as well: 1032 s has 11 bits and is at most 61920.  q is scaled by a power of
-// two per head (at g = 8 per half of D), which makes its bf16 numbers exact in f16 down to 2^-31 of the
-// largest, and within 2^-39 of it below.
-//   scores  S[pos, h] = K[pos, :] . q[h, :] for the 16 positions of a block.  Lane (g, t) reads the
-//           chunks (16 bytes, 32 channels, one scale) t and t + 4 of the rows of its A fragments; what
-//           order the channels take in k does not matter, q's B fragments take the same
-//   P.V     O^T[c, h] += V^T[c, pos] P[pos, h]: lane (g, t) reads the chunk of its g from the rows of
-//           its four positions, a byte permute pairs positions, and code 2m (2m + 1) of every chunk is
-//           the row g (g + 8) of the m-th tile.  movmatrix turns the weights from the scores'
-//           layout into B fragments.  At g = 2 the hi and lo parts of P are columns of one mma; at
-//           g = 8 they are two mma.
-// A row of the scores' fragment g (g + 8) stands for position perm(g) (8 + perm(g)), perm(g) =
-// g / 2 + 4 (g % 2): with rows of 17 16-byte units this is what keeps the 8 lanes of a shared-memory
-// phase on distinct banks in both contractions.
+// operand, so that the g <= 8 query heads of a KV head fill the 8 columns of B.
+//   scores  S[pos, h] = sum over chunks c (32 channels, one scale) of s_c (U_c . q_c - 8 sum q_c), U the
+//           codes.  ldmatrix gives lane (g, t) the word t of a chunk in rows g and g + 8.  Codes j and
+//           j + 4 of a word lie in the low four bits of its halves: masked they are the f16 numbers
+//           u 2^-24, one place up u 2^-20 (subnormal, and exact in an mma); a shift by 8 brings the
+//           rest.  So a word takes five operations and no conversion; q's fragments make up for the two
+//           places, a chunk's two mma are scaled in fp32, and one mma of all chunks' scales (exact in
+//           f16) with the sums of q (hi and lo parts) takes the 8 off.
+//   P.V     O^T[c, h] += V^T[c, pos] P[pos, h]: lane (g, t) reads the chunk g from the rows of its
+//           four positions, a byte permute pairs positions, and code 2m (2m + 1) of every chunk is
+//           the row g (g + 8) of the m-th tile.  Here the scales differ along k, so values are made:
+//           0x6400 | u is the f16 number 1024 + u and (u - 8) s = (1024 + u) s - 1032 s one fma of two
+//           codes; one place up it is 1024 + 16 u, times s / 16, less 72 s.  All of it is exact (1032 s
+//           has 11 bits and is at most 61920).  (bf16, whose 7 bits of mantissa leave no room for a
+//           second place, takes three shifts for a word and not one.)  movmatrix turns the weights
+//           from the scores' layout into B fragments.  At g = 2 the hi and lo parts of P are columns
+//           of one mma; at g = 8 they are two mma.
+// q is scaled by a power of two per head (at g = 8 per half of D): its bf16 numbers are exact in f16 down
+// to 2^-27 of the largest, and within 2^-35 of it below.
 // An mma truncates its sum, so long chains of them drift: a block's products start from zero and
 // are added to the accumulators by ordinary additions.
 //
@@ -36,6 +35,19 @@
 // warps of a unit (at g = 8 pairs, a plane each) on a block each with a ring of slots of their
 // own, states merged through shared memory at a piece's end, split segments by the combine kernel.  A
 // slot is one block of K, V and scales: one bulk copy per plane of exactly the attended rows.
+//
+// Bound by instructions: some 650 for a block of a plane (4352 bytes), of which 128 mask codes, 64 make
+// values, 48 (32) are mma, and an SM's share of HBM brings a block to each scheduler every 740 cycles.
+// Three consumer warps per scheduler (160 registers each, what the producers leave; with four, at 112,
+// spills cost more than they hide) issue in 0.58 of the cycles.  What the steps took, GPU time of
+// decode_sliding_b64_paged / decode_global_b16_long: 8 consumer warps and the mask and the constant of
+// 1024 + u two operations, 85 / 990 us; 12 warps 86 / 860; one operation 80 / 766; producers that fill
+// their rings lane by lane and sleep 76 / 785; q's fragments in shared memory (no spills) 71 / 755; a
+// merge that reads whole states 72 / 718; scores' scales after the mma 67.5 / 736; P.V in two halves (less
+// registers) 68 / 713; the pair's exchange apart from the tiles (no fence between proxies) 68 / 709.
+// Without its copies the kernel takes 739 us where it took 755, without its arithmetic 472.  Tried: P.V
+// of one block between another's scores, 81 / 874 (slots are held longer); sums kept in the mma's
+// accumulator and flushed every 16 blocks, 75 / 711.
 #pragma once
 
 #include "decode_kernel.cuh"
@@ -64,17 +76,18 @@ struct NibblePolicy {
     static constexpr int NC = kBlocksAtOnce;             // blocks a unit works on at a time
     static constexpr int RING = kRing;                   // slots per block in work
     static constexpr int GW = NC * SPLIT;                // consumer warps per unit
-    static constexpr int kConsumers = GROUPS * GW;
-    static constexpr int kFeeds = NC / 2;                // producers per unit, two rings each
-    static constexpr int kWarps = kConsumers + kFeeds * GROUPS;
-    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kConsumers = GROUPS * GW;       // whole warpgroups; then one of producers
+    static constexpr int kThreads = (kConsumers + 4) * 32;
+    static constexpr int kLaunchRegs = 128, kConsumerRegs = 160, kProducerRegs = 32;
     static constexpr bool kSplitCols = G == 2;           // hi and lo parts of P in one mma
-    static constexpr int kMergeCols = kSplitCols ? 2 * G : G;
-    static constexpr int kMergeDims = 128 / SPLIT;       // channels of a warp merged per round
-    static constexpr int kMergeTiles = kMergeDims / 16;  // tiles of a round: 2 channels of each chunk
-    static constexpr int kMergePitch = 2 * kMergeTiles + 2;   // floats per chunk
+    static constexpr int kLanes = kSplitCols ? 16 : 32;  // lanes whose accumulators are no copies
+    static constexpr int kRound = kSplitCols ? 8 : 4;    // tiles merged at a time
     static_assert((G == 2 || G == 8) && (NC == 2 || NC == 4), "shape");
     static_assert(kThreads >= kPlanWarps * 32, "the plan takes eight warps");
+    static_assert(kConsumers % 4 == 0 && GROUPS <= 4, "warpgroups");
+    static_assert(kConsumers * kConsumerRegs + 4 * kProducerRegs <= (kConsumers + 4) * kLaunchRegs &&
+                      kThreads * kLaunchRegs <= 65536,
+                  "no share waits for registers that the block was not launched with");
 };
 
 template <class Pol>
@@ -87,9 +100,11 @@ struct alignas(128) NibbleSmem {
         int bad[Pol::NC * Pol::RING];            // the block's page id is out of range
         BlockPiece piece;
         float wm[Pol::NC][8], wl[Pol::NC][8];    // M and l per column of each warp (pair)
-        alignas(16) float wacc[Pol::SPLIT][Pol::NC][Pol::kMergeCols][8 * Pol::kMergePitch];   // being merged
     };
     uint8_t kv[Pol::GROUPS][Pol::NC * Pol::RING][Pol::SPLIT][kTileBytes];   // [slot][plane][16 rows][272 B]
+    alignas(16) float4 sum[Pol::GROUPS][Pol::SPLIT][Pol::NC][Pol::kRound][Pol::kLanes];   // accumulators being merged
+    uint4 q[Pol::GROUPS][Pol::SPLIT][8][32];   // B fragments of q (NibbleConsumer::begin)
+    float4 cross[Pol::GROUPS][Pol::NC][2][Pol::SPLIT][32];   // scores on their way between a pair's warps
     Unit unit[Pol::GROUPS];
     alignas(8) uint64_t stall_bar;               // kTestStall: a barrier nothing completes
     PlanSmem plan;
@@ -105,39 +120,64 @@ struct NibbleScale {
     __device__ __forceinline__ explicit NibbleScale(uint32_t bits)
         : s(bits), less(ptx::f16x2_mul(bits, 0xe408e408u)), s16(ptx::f16x2_mul(bits, 0x2c002c00u)),
           less16(ptx::f16x2_mul(bits, 0xd480d480u)) {}
-    __device__ __forceinline__ uint32_t low(uint32_t w) const {
-        return ptx::f16x2_fma((w & 0x000f000fu) | 0x64006400u, s, less);
+    // base: 0x64006400 in a register
+    __device__ __forceinline__ uint32_t low(uint32_t w, uint32_t base) const {
+        return ptx::f16x2_fma(ptx::and_or<0x000f000fu>(w, base), s, less);
     }
-    __device__ __forceinline__ uint32_t high(uint32_t w) const {
-        return ptx::f16x2_fma((w & 0x00f000f0u) | 0x64006400u, s16, less16);
+    __device__ __forceinline__ uint32_t high(uint32_t w, uint32_t base) const {
+        return ptx::f16x2_fma(ptx::and_or<0x00f000f0u>(w, base), s16, less16);
     }
 };
+
+// wait_bounded (decode_kernel.cuh) for waits that are long as a rule: the thread is suspended between
+// its looks at the barrier.  (Producers that wait for a slot took a fifth of the issue slots.)
+__device__ __forceinline__ bool wait_suspended(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                               uint32_t* flags, uint64_t limit_ns = kWaitLimitNs) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = ptx::globaltimer_ns();
+    for (uint32_t round = 0;; ++round) {
+        if (ptx::mbar_try_wait_for(bar, parity, 20000u)) return true;
+        if (*abort_flag) return false;
+        // time limit, with an iteration cap in case the timer does not advance
+        if (ptx::globaltimer_ns() - t0 > limit_ns || round > kWaitMaxRounds) {
+            *abort_flag = 1;
+            atomicOr(flags, kFlagWaitTimeout);
+            return false;
+        }
+    }
+}
 
 template <class Pol>
 struct NibbleConsumer {
     static constexpr int G = Pol::G, D = Pol::D;
     static constexpr int kTiles = kNibblePlane / 16;
-    static constexpr float kBase = 12.0f;   // exponent of the weight of a score equal to M
+    static constexpr float kBase = 8.0f;    // exponent of the largest weight when M is set
     static constexpr float kTop = 15.0f;    // largest exponent of a weight (f16 ends at 2^16)
     static constexpr float kLowest = -3.402823466e38f;   // M of no score yet
 
-    uint32_t qb[kTiles][2];      // B fragments of q (column g = head g % G) for this warp's plane
-    float q_undo[2];             // undo their scaling for columns 2t and 2t + 1, times log2(e)
-    float acc[kTiles][4];        // tile m: channels 2m (0, 1) and 2m + 1 (2, 3) of chunk(g); columns 2t, 2t + 1
+    // Rows that a lane's B fragments of P.V stand for, less 2t.
+    __device__ static constexpr int place(int j) { return j < 2 ? j : 6 + j; }   // 0, 1, 8, 9
+
+    float q_undo[2];             // undo q's scaling for columns 2t and 2t + 1, times log2(e)
+    uint32_t qs[2];              // sums of scaled q over chunks 2t, 2t + 1 of head g, times -2^-5: hi and lo parts
+    // tile m: channels 2n (0, 1) and 2n + 1 (2, 3) of chunk g, n = m or, where g & 2, m ^ 8; columns 2t, 2t + 1
+    float acc[kTiles][4];
     float ms[2];                 // M of columns 2t, 2t + 1
     float l[2];                  // this lane's share of their normalisers
+    uint32_t base;               // 0x64006400
 
-    __device__ static __forceinline__ int perm(int g) { return (g >> 1) + 4 * (g & 1); }
-
-    // q_heads: [G][D] bf16 in global memory; `half`: which plane of the head is this warp's.
-    __device__ __forceinline__ void begin(const __nv_bfloat16* q_heads, int half, int lane) {
+    // q_heads: [G][D] bf16 in global memory; `half`: which plane of the head is this warp's; q_at: where
+    // the plane's B fragments of q (column g = head g % G) stand in shared memory.  The unit's warps write
+    // a part each.
+    __device__ __forceinline__ void begin(const __nv_bfloat16* q_heads, uint32_t q_at, int own, int half,
+                                          int lane) {
         const int g = lane >> 2, t = lane & 3;
-        const __nv_bfloat16* row = q_heads + (g % G) * D + half * kNibblePlane + 32 * t;
+        const __nv_bfloat16* row = q_heads + (g % G) * D + half * kNibblePlane + 8 * t;
         uint32_t top = 0;   // largest |q|: the bits of |bf16| order like the values
         uint4 raw[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {   // channels 8 (i % 4) .. + 7 of chunk t + 4 (i / 4)
-            raw[i] = __ldg(reinterpret_cast<const uint4*>(row + (i >> 2) * 128 + (i & 3) * 8));
+        for (int i = 0; i < 8; ++i) {   // channels 8t .. + 7 of chunk i
+            raw[i] = __ldg(reinterpret_cast<const uint4*>(row + 32 * i));
             top = __vmaxu2(top, __vmaxu2(__vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu),
                                          __vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu)));
         }
@@ -145,15 +185,28 @@ struct NibbleConsumer {
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int e = max(static_cast<int>(top >> 7) - 127, -88);   // |q| < 2^(e + 1)
-        const float f = __int_as_float((14 - e + 127) << 23);
+        const float f = __int_as_float((10 - e + 127) << 23), f16 = f * 16.0f;
+        float even = 0.0f, odd = 0.0f;   // sums over the chunks 2t and 2t + 1
 #pragma unroll
         for (int i = 0; i < 8; ++i) {   // pairs of channels (0, 4), (1, 5), (2, 6), (3, 7)
-            qb[2 * i][0] = ptx::f16x2_pack(bf16lo(raw[i].x) * f, bf16lo(raw[i].z) * f);
-            qb[2 * i][1] = ptx::f16x2_pack(bf16hi(raw[i].x) * f, bf16hi(raw[i].z) * f);
-            qb[2 * i + 1][0] = ptx::f16x2_pack(bf16lo(raw[i].y) * f, bf16lo(raw[i].w) * f);
-            qb[2 * i + 1][1] = ptx::f16x2_pack(bf16hi(raw[i].y) * f, bf16hi(raw[i].w) * f);
+            const uint4 h = make_uint4(ptx::f16x2_pack(bf16lo(raw[i].x) * f16, bf16lo(raw[i].z) * f16),
+                                       ptx::f16x2_pack(bf16hi(raw[i].x) * f, bf16hi(raw[i].z) * f),
+                                       ptx::f16x2_pack(bf16lo(raw[i].y) * f16, bf16lo(raw[i].w) * f16),
+                                       ptx::f16x2_pack(bf16hi(raw[i].y) * f, bf16hi(raw[i].w) * f));
+            if (i % Pol::NC == own)
+                ptx::sts128(q_at + i * 512 + lane * 16, h.x, h.y, h.z, h.w);
+            const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+            float sum = 0.0f;   // (of scaled values: q itself may add up beyond fp32)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sum = fmaf(bf16hi(u[k]), f, fmaf(bf16lo(u[k]), f, sum));
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            if (i >> 1 == t) (i & 1 ? odd : even) = sum * -0x1p-5f;   // -8, and 2^-8 to stay in f16
         }
-        const float undo = __int_as_float((e - 14 + 127) << 23) * kLog2e;
+        qs[0] = ptx::f16x2_pack(even, odd);
+        const float2 rest = ptx::f16x2_unpack(qs[0]);
+        qs[1] = ptx::f16x2_pack(even - rest.x, odd - rest.y);
+        const float undo = __int_as_float((e - 10 + 127) << 23) * kLog2e;
         q_undo[0] = __shfl_sync(0xffffffffu, undo, 8 * t);
         q_undo[1] = __shfl_sync(0xffffffffu, undo, 8 * t + 4);
 #pragma unroll
@@ -162,77 +215,109 @@ struct NibbleConsumer {
             for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
         ms[0] = ms[1] = kLowest;
         l[0] = l[1] = 0.0f;
+        base = ptx::in_register(0x64006400u);
     }
 
     // This plane's share of a block's scores in units of log2: rows g (0, 1) and g + 8 (2, 3),
     // columns 2t, 2t + 1.
-    __device__ __forceinline__ void scores(uint32_t tile, float (&z)[4], int lane) {
+    __device__ __forceinline__ void scores(uint32_t tile, uint32_t q_at, float (&z)[4], int lane) {
         const int g = lane >> 2, t = lane & 3;
-        const uint32_t row = tile + perm(g) * kNibbleRow;
+        const uint32_t row = tile + g * kNibbleRow + kNibbleScales;
         constexpr uint32_t k8 = 8 * kNibbleRow;
-        float c[4][4];   // four independent chains
+        // matrices of ldmatrix: rows 0 .. 7 and 8 .. 15 of a chunk, then of the next
+        const uint32_t at = tile + (lane & 15) * kNibbleRow + (lane >> 4) * 16;
+        const uint2 sa = ptx::lds64(row), sb = ptx::lds64(row + k8);
+        float d[4];
+        // -8 times the scales times the sums of q, in the codes' unit of 2^-20: lane (g, t) holds the scales
+        // of chunks 2t and 2t + 1 in rows g and g + 8, twice (for the sums' hi and lo parts)
+        const uint32_t a0 = __byte_perm(ptx::lds16(row + 2 * t), 0u, 0x1404) >> 1;
+        const uint32_t a1 = __byte_perm(ptx::lds16(row + k8 + 2 * t), 0u, 0x1404) >> 1;
+        ptx::mma_f16_16816_zero(d, a0, a1, a0, a1, qs[0], qs[1]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) z[i] = d[i] * 0x1p-12f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) c[i][j] = 0.0f;
-        const uint2 sa = ptx::lds64(row + kNibbleScales), sb = ptx::lds64(row + k8 + kNibbleScales);
-        const uint32_t sel = 0x0404u | (t << 4) | (t << 12);   // byte t to the upper bytes of both halves
+        for (int i = 0; i < 8; i += 2) {
+            uint32_t w[4];
+            ptx::ldmatrix_x4(at + 16 * i, w[0], w[1], w[2], w[3]);
+            const uint32_t pick = i & 2 ? 0x3424 : 0x1404;   // scales i and i + 1 of a row as f16
+            const float2 fa = ptx::f16x2_unpack(__byte_perm(i & 4 ? sa.y : sa.x, 0u, pick) >> 1);
+            const float2 fb = ptx::f16x2_unpack(__byte_perm(i & 4 ? sb.y : sb.x, 0u, pick) >> 1);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint4 a = ptx::lds128(row + 16 * t + 64 * i), b = ptx::lds128(row + k8 + 16 * t + 64 * i);
-            const NibbleScale fa(__byte_perm(i ? sa.y : sa.x, 0u, sel) >> 1);
-            const NibbleScale fb(__byte_perm(i ? sb.y : sb.x, 0u, sel) >> 1);
-            const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const int u = 8 * i + 2 * w;
-                ptx::mma_f16_16816(c[w], fa.low(wa[w]), fb.low(wb[w]), fa.high(wa[w]), fb.high(wb[w]),
-                                   qb[u][0], qb[u][1]);
-                const uint32_t ha = wa[w] >> 8, hb = wb[w] >> 8;
-                ptx::mma_f16_16816(c[w], fa.low(ha), fb.low(hb), fa.high(ha), fb.high(hb),
-                                   qb[u + 1][0], qb[u + 1][1]);
+            for (int k = 0; k < 2; ++k) {
+                const uint4 q = ptx::lds128(q_at + (i + k) * 512 + lane * 16);
+                const uint32_t a = w[2 * k], b = w[2 * k + 1], ha = a >> 8, hb = b >> 8;
+                ptx::mma_f16_16816_zero(d, a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u,
+                                        q.x, q.y);
+                ptx::mma_f16_16816(d, ha & 0x000f000fu, hb & 0x000f000fu, ha & 0x00f000f0u, hb & 0x00f000f0u,
+                                   q.z, q.w);
+                const float s0 = k ? fa.y : fa.x, s1 = k ? fb.y : fb.x;
+                z[0] = fmaf(d[0], s0, z[0]);
+                z[1] = fmaf(d[1], s0, z[1]);
+                z[2] = fmaf(d[2], s1, z[2]);
+                z[3] = fmaf(d[3], s1, z[3]);
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            z[i] = ((c[0][i] + c[1][i]) + (c[2][i] + c[3][i])) * q_undo[i & 1];
+        for (int i = 0; i < 4; ++i) z[i] = z[i] * 0x1p20f * q_undo[i & 1];   // (one factor may pass 2^127)
+    }
+
+    // The accumulators of columns 2t and 2t + 1 times a and b.
+    __device__ __forceinline__ void scale_by(float a, float b) {
+        const uint64_t f = ptx::f2_pack(a, b);
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) {
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+                const float2 x = ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(acc[i][j], acc[i][j + 1]), f));
+                acc[i][j] = x.x;
+                acc[i][j + 1] = x.y;
+            }
+        }
     }
 
     // The rest of a block, from its scores: weights, M, l, and P.V for this warp's plane.  Rows
     // [first, last) are attended; bad: their page does not exist, and their weights are NaN.
-    __device__ __forceinline__ void weigh(const float (&z)[4], uint32_t tile, int first, int last, bool bad,
+    __device__ __forceinline__ void weigh(float (&x)[4], uint32_t tile, int first, int last, bool bad,
                                           int lane) {
-        const int g = lane >> 2, t = lane & 3, pos = perm(g);
-        const bool row_ok[2] = {pos >= first && pos < last, pos + 8 >= first && pos + 8 < last};
-        float x[4], y[4];
+        const int g = lane >> 2, t = lane & 3;
+        // the scales of chunk g in positions 2t, 2t + 1, 2t + 8, 2t + 9
+        const uint32_t row = tile + 2 * t * kNibbleRow;
+        uint32_t sc[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {   // rows outside the range weigh 2^-inf
-            x[i] = row_ok[i >> 1] ? (bad ? __uint_as_float(0x7fc00000u) : z[i]) : -INFINITY;
-            y[i] = x[i] - ms[i & 1] + kBase;
+        for (int j = 0; j < 4; ++j) sc[j] = ptx::lds8(row + place(j) * kNibbleRow + kNibbleScales + 8 + g);
+        if (first > 0 || last < kNibblePage || bad) {
+            // rows outside the range weigh 2^-inf, and as they hold anything, and 0 * NaN is NaN, their
+            // scales are taken as 0
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int pos = g + 8 * (i >> 1);
+                x[i] = pos >= first && pos < last ? (bad ? __uint_as_float(0x7fc00000u) : x[i]) : -INFINITY;
+                if (2 * t + place(i) < first || 2 * t + place(i) >= last) sc[i] = 0;
+            }
         }
+        float y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = x[i] - ms[i & 1];
         // M moves only when a weight would pass 2^kTop (and on the first block)
         const float ym = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
         if (__any_sync(0xffffffffu, ym > kTop)) {
+            float alpha[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 float top = fmaxf(x[j], x[j + 2]);
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                top = ceilf(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)));
-                const float m = fmaxf(ms[j], top);   // (never of a NaN)
-                const float alpha = ptx::ex2(ms[j] - m);
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                const float m = fmaxf(ms[j], __fadd_ru(ceilf(top), -kBase));   // (never of a NaN)
+                alpha[j] = ptx::ex2(ms[j] - m);
                 ms[j] = m;
-                l[j] *= alpha;
-#pragma unroll
-                for (int i = 0; i < kTiles; ++i) {
-                    acc[i][j] *= alpha;
-                    acc[i][j + 2] *= alpha;
-                }
-                y[j] = x[j] - m + kBase;
-                y[j + 2] = x[j + 2] - m + kBase;
+                l[j] *= alpha[j];
+                y[j] = x[j] - m;
+                y[j + 2] = x[j + 2] - m;
             }
+            scale_by(alpha[0], alpha[1]);
         }
-        uint32_t hi[2], lo[2];   // B fragments: column g, positions perm(2t), perm(2t + 1) of each half
+        uint32_t hi[2], lo[2];   // B fragments: column g, positions 2t, 2t + 1 of each half
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const float p0 = ptx::ex2(y[2 * i]), p1 = ptx::ex2(y[2 * i + 1]);
@@ -248,50 +333,62 @@ struct NibbleConsumer {
                 lo[i] = ptx::movmatrix_trans(lo[i]);
             }
         }
-        // the chunk of this g in positions t, t + 4, t + 8, t + 12; rows outside the range hold
-        // anything, and 0 * NaN is NaN: their scale is taken as 0
-        const int chunk = perm(g);
-        const uint32_t row = tile + t * kNibbleRow;
-        uint32_t sc[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            sc[j] = ptx::lds8(row + 4 * j * kNibbleRow + kNibbleScales + 8 + chunk);
-            if (t + 4 * j < first || t + 4 * j >= last) sc[j] = 0;
-        }
         const NibbleScale f0(__byte_perm(sc[0], sc[1], 0x5410) << 7), f1(__byte_perm(sc[2], sc[3], 0x5410) << 7);
-        uint4 v[4];
+        // Half a chunk at a time (whole ones took 16 registers more).  Lanes (g, t) and (g + 2, t - 1) share
+        // banks: one of them takes its halves the other way round.
+        const uint32_t codes = row + kNibblePlane / 2 + 16 * g, flip = 4 * (g & 2);   // 0 or 8 bytes
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            v[j] = ptx::lds128(row + 4 * j * kNibbleRow + kNibblePlane / 2 + 16 * chunk);
-        const uint32_t w[4][4] = {{v[0].x, v[0].y, v[0].z, v[0].w}, {v[1].x, v[1].y, v[1].z, v[1].w},
-                                  {v[2].x, v[2].y, v[2].z, v[2].w}, {v[3].x, v[3].y, v[3].z, v[3].w}};
+        for (int half = 0; half < 2; ++half) {
+            uint2 v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+            for (int j = 0; j < 4; ++j) v[j] = ptx::lds64(codes + place(j) * kNibbleRow + (half ? 8 - flip : flip));
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {   // codes 2k, 2k + 1 of word i
-                uint32_t a = __byte_perm(w[0][i], w[1][i], k < 2 ? 0x5410 : 0x7632);
-                uint32_t b = __byte_perm(w[2][i], w[3][i], k < 2 ? 0x5410 : 0x7632);
-                if (k & 1) {
-                    a >>= 8;
-                    b >>= 8;
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {   // codes 2k, 2k + 1 of a word
+                    uint32_t a = __byte_perm(i ? v[0].y : v[0].x, i ? v[1].y : v[1].x, k < 2 ? 0x5410 : 0x7632);
+                    uint32_t b = __byte_perm(i ? v[2].y : v[2].x, i ? v[3].y : v[3].x, k < 2 ? 0x5410 : 0x7632);
+                    if (k & 1) {
+                        a >>= 8;
+                        b >>= 8;
+                    }
+                    const uint32_t a0 = f0.low(a, base), a1 = f0.high(a, base);
+                    const uint32_t a2 = f1.low(b, base), a3 = f1.high(b, base);
+                    float d[4];
+                    if (Pol::kSplitCols) {
+                        ptx::mma_f16_16816_zero(d, a0, a1, a2, a3, hi[0], hi[1]);
+                    } else {
+                        ptx::mma_f16_16816_zero(d, a0, a1, a2, a3, lo[0], lo[1]);
+                        ptx::mma_f16_16816(d, a0, a1, a2, a3, hi[0], hi[1]);
+                    }
+                    float (&sum)[4] = acc[8 * half + 4 * i + k];
+#pragma unroll
+                    for (int j = 0; j < 4; j += 2) {
+                        const float2 x = ptx::f2_unpack(
+                            ptx::f2_add(ptx::f2_pack(sum[j], sum[j + 1]), ptx::f2_pack(d[j], d[j + 1])));
+                        sum[j] = x.x;
+                        sum[j + 1] = x.y;
+                    }
                 }
-                float d[4];
-                const uint32_t a0 = f0.low(a), a1 = f0.high(a), a2 = f1.low(b), a3 = f1.high(b);
-                if (Pol::kSplitCols) {
-                    ptx::mma_f16_16816_zero(d, a0, a1, a2, a3, hi[0], hi[1]);
-                } else {
-                    ptx::mma_f16_16816_zero(d, a0, a1, a2, a3, lo[0], lo[1]);
-                    ptx::mma_f16_16816(d, a0, a1, a2, a3, hi[0], hi[1]);
-                }
+        }
+    }
+
+    // Tiles [r kRound, (r + 1) kRound) of the accumulators to this warp's place in shared memory.  (At
+    // kSplitCols the columns 4 .. 7 are copies.)
+    __device__ __forceinline__ void put(float4 (*sum)[Pol::kLanes], int r, int lane) {
+        if (Pol::kSplitCols && (lane & 2)) return;
+        const int at = Pol::kSplitCols ? (lane >> 2) * 2 + (lane & 1) : lane;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[4 * i + k][j] += d[j];
-            }
+        for (int i = 0; i < Pol::kRound; ++i) {
+            const float (&x)[4] = acc[r * Pol::kRound + i];
+            sum[i][at] = make_float4(x[0], x[1], x[2], x[3]);
+        }
     }
 
     // The end of this warp's share of a piece: M and l of its columns to wm and wl (the planes of a
-    // head hold the same), with M itself as the exponent of the weights.
-    __device__ __forceinline__ void finish(typename NibbleSmem<Pol>::Unit& sm, int own, int half,
-                                           int lane) {
+    // head hold the same), and the first round's tiles.
+    __device__ __forceinline__ void finish(typename NibbleSmem<Pol>::Unit& un, float4 (*sum)[Pol::kLanes],
+                                           int own, int half, int lane) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             float ls = l[j];
@@ -299,89 +396,79 @@ struct NibbleConsumer {
             ls += __shfl_xor_sync(0xffffffffu, ls, 8);
             ls += __shfl_xor_sync(0xffffffffu, ls, 16);
             if (half == 0 && lane < 4) {
-                sm.wm[own][2 * lane + j] = ms[j];
-                sm.wl[own][2 * lane + j] = ls * 0x1p-12f;
+                un.wm[own][2 * lane + j] = ms[j];
+                un.wl[own][2 * lane + j] = ls;
             }
         }
+        put(sum, 0, lane);
     }
 
-    // Merge of the warps' states: the output (slot < 0; the piece is the whole segment) or
-    // the partial (acc, m, l) at workspace slot `slot`.  The M are whole numbers, so the
-    // factors 2^(M_w - M) are exact.  Called by all consumer warps, after finish() and a barrier.
-    __device__ __forceinline__ void merge(typename NibbleSmem<Pol>::Unit& sm, const DecodeParams& p,
-                                          size_t out_base, int slot, int bar, int own, int half,
-                                          int lane) {
-        const int g = lane >> 2, t = lane & 3, tid = own * 32 + lane;
-        constexpr int kThreads = Pol::NC * 32;          // of each plane
-        constexpr int W = Pol::kMergeDims, kPer = Pol::kMergeTiles, kPitch = Pol::kMergePitch;
-        // a round merges G heads x W channels; a thread takes two channels of every kHeadStep-th head
-        constexpr int kHeadStep = kThreads / (W / 2);
-        static_assert(kHeadStep * (W / 2) == kThreads && G % kHeadStep == 0, "two channels per thread");
+    // Merge of the warps' accumulators (of this plane): the output (slot < 0; the piece is the whole
+    // segment) or the partial (acc, m, l) at workspace slot `slot`.  The M are whole numbers, so the factors
+    // 2^(M_w - M) are exact.  Called by all consumer warps, after finish() and a barrier.
+    __device__ __forceinline__ void merge(const typename NibbleSmem<Pol>::Unit& un,
+                                          float4 (*sums)[Pol::kRound][Pol::kLanes], const DecodeParams& p,
+                                          size_t out_base, int slot, int bar, int own, int half, int lane) {
+        const int h0 = Pol::kSplitCols ? 0 : 2 * (lane & 3);
+        float f[2][Pol::NC], scale[2];   // of heads h0 and h0 + 1
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            float top = -INFINITY;
+            float top = -INFINITY, ls = 0.0f;
 #pragma unroll
-            for (int w = 0; w < Pol::NC; ++w) top = fmaxf(top, sm.wm[w][2 * t + j]);
-            // (a warp without a score weighs 0 beside one with; its NaN stay)
-            const float f = ptx::ex2(ms[j] - top) * 0x1p-12f;
+            for (int w = 0; w < Pol::NC; ++w) top = fmaxf(top, un.wm[w][h0 + j]);
 #pragma unroll
-            for (int i = 0; i < kTiles; ++i) {
-                acc[i][j] *= f;
-                acc[i][j + 2] *= f;
+            for (int w = 0; w < Pol::NC; ++w) {   // (a warp without a score weighs 0 beside one with)
+                f[j][w] = ptx::ex2(un.wm[w][h0 + j] - top);
+                ls = fmaf(f[j][w], un.wl[w][h0 + j], ls);
             }
-        }
-        float top[G / kHeadStep], ls[G / kHeadStep], inv[G / kHeadStep];   // of this thread's heads
-#pragma unroll
-        for (int k = 0; k < G / kHeadStep; ++k) {
-            const int h = k * kHeadStep + tid / (W / 2);
-            top[k] = -INFINITY;
-            ls[k] = 0.0f;
-#pragma unroll
-            for (int w = 0; w < Pol::NC; ++w) top[k] = fmaxf(top[k], sm.wm[w][h]);
-#pragma unroll
-            for (int w = 0; w < Pol::NC; ++w) ls[k] += ptx::ex2(sm.wm[w][h] - top[k]) * sm.wl[w][h];
-            inv[k] = slot < 0 ? 1.0f / ls[k] : 1.0f;
-            if (slot >= 0 && half == 0 && tid % (W / 2) == 0)
-                *reinterpret_cast<float2*>(p.ws_ml + (static_cast<size_t>(slot) * G + h) * 2) =
-                    make_float2(top[k], ls[k]);
+            scale[j] = slot < 0 ? 1.0f / ls : 1.0f;
+            if (slot >= 0 && half == 0 && own == 0 && lane < (Pol::kSplitCols ? 1 : 4))
+                *reinterpret_cast<float2*>(p.ws_ml + (static_cast<size_t>(slot) * G + h0 + j) * 2) =
+                    make_float2(top, ls);
         }
         const bool floats = slot >= 0 || p.out_f32;
         float* to = slot < 0 ? static_cast<float*>(p.out) + out_base
                              : p.ws_acc + static_cast<size_t>(slot) * G * D;
-        const int pair = tid % (W / 2), chunk = pair / kPer, within = 2 * (pair % kPer);
+        // a warp reads four tiles together, whose channels fill sectors: of all g (at kSplitCols) or of two
+        constexpr int kSteps = Pol::kRound / 4 * (Pol::kSplitCols ? 1 : 4);
 #pragma unroll
-        for (int r = 0; r < kTiles / kPer; ++r) {
-            if (2 * t < Pol::kMergeCols) {   // (at kSplitCols t = 1 holds the lo parts' products)
-#pragma unroll
-                for (int i = 0; i < kPer; ++i)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        *reinterpret_cast<float2*>(&sm.wacc[half][own][2 * t + j][perm(g) * kPitch + 2 * i]) =
-                            make_float2(acc[r * kPer + i][j], acc[r * kPer + i][j + 2]);
+        for (int r = 0; r < kTiles / Pol::kRound; ++r) {
+            if (r > 0) {
+                ptx::named_barrier_sync(bar, Pol::GW * 32);
+                put(sums[own], r, lane);
+                ptx::named_barrier_sync(bar, Pol::GW * 32);
             }
-            ptx::named_barrier_sync(bar, Pol::GW * 32);
 #pragma unroll
-            for (int k = 0; k < G / kHeadStep; ++k) {
-                const int h = k * kHeadStep + tid / (W / 2);
-                float2 s = make_float2(0.0f, 0.0f);
+            for (int step = own; step < kSteps; step += Pol::NC) {
+                const int i = 4 * (Pol::kSplitCols ? step : step >> 2) + (lane >> 3);
+                const int g = Pol::kSplitCols ? lane & 7 : 2 * (step & 3) + ((lane >> 2) & 1);
+                float2 o[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};   // channels 2m, 2m + 1 of the chunk, of both heads
 #pragma unroll
-                for (int w = 0; w < Pol::NC; ++w)
-#pragma unroll
-                    for (int c = 0; c < Pol::kMergeCols; c += G) {
-                        const float2 x =
-                            *reinterpret_cast<const float2*>(&sm.wacc[half][w][c + h][chunk * kPitch + within]);
-                        s.x += x.x;
-                        s.y += x.y;
+                for (int w = 0; w < Pol::NC; ++w) {
+                    float4 x;
+                    if (Pol::kSplitCols) {   // columns of the hi parts and of the lo parts
+                        const float4 hi = sums[w][i][2 * g], lo = sums[w][i][2 * g + 1];
+                        x = make_float4(hi.x + lo.x, hi.y + lo.y, hi.z + lo.z, hi.w + lo.w);
+                    } else {
+                        x = sums[w][i][4 * g + (lane & 3)];
                     }
-                const size_t at = static_cast<size_t>(h) * D + half * kNibblePlane + 32 * chunk + 2 * kPer * r + within;
-                if (floats)
-                    *reinterpret_cast<float2*>(to + at) = make_float2(s.x * inv[k], s.y * inv[k]);
-                else
-                    *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + out_base + at) =
-                        __floats2bfloat162_rn(s.x * inv[k], s.y * inv[k]);
+                    o[0].x = fmaf(x.x, f[0][w], o[0].x);
+                    o[1].x = fmaf(x.y, f[1][w], o[1].x);
+                    o[0].y = fmaf(x.z, f[0][w], o[0].y);
+                    o[1].y = fmaf(x.w, f[1][w], o[1].y);
+                }
+                const int m = (r * Pol::kRound + i) ^ (4 * (g & 2));   // (weigh()'s halves)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const size_t at = static_cast<size_t>(h0 + j) * D + half * kNibblePlane + 32 * g + 2 * m;
+                    const float2 y = make_float2(o[j].x * scale[j], o[j].y * scale[j]);
+                    if (floats)
+                        *reinterpret_cast<float2*>(to + at) = y;
+                    else
+                        *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + out_base + at) =
+                            __floats2bfloat162_rn(y.x, y.y);
+                }
             }
-            // (wacc is filled again: in the next round, or after the barrier that ends the next piece)
-            if (r + 1 < kTiles / kPer) ptx::named_barrier_sync(bar, Pol::GW * 32);
         }
     }
 };
@@ -411,7 +498,7 @@ __global__ void __launch_bounds__(Pol::kThreads, 1) gqa_decode_nibble_kernel(con
             ptx::mbar_init(ptx::smem_addr(&un.empty[s]), SPLIT);
         }
         ptx::mbar_init(ptx::smem_addr(&un.piece_full), 1);
-        ptx::mbar_init(ptx::smem_addr(&un.piece_empty), Pol::GW + Pol::kFeeds - 1);   // who reads it
+        ptx::mbar_init(ptx::smem_addr(&un.piece_empty), Pol::GW);   // who reads it
         if (tid == 0) {
             ptx::mbar_init(ptx::smem_addr(&sm.stall_bar), 1);
             sm.abort_flag = 0;
@@ -452,201 +539,188 @@ __global__ void __launch_bounds__(Pol::kThreads, 1) gqa_decode_nibble_kernel(con
     if (!has_work) return;
 
     // this warp's unit (a group without a unit has nothing to do)
-    const int group = warp < Pol::kConsumers ? warp / Pol::GW : (warp - Pol::kConsumers) / Pol::kFeeds;
+    const int group = warp < Pol::kConsumers ? warp / Pol::GW : warp - Pol::kConsumers;
     const int unit = cta + ctas * group;
-    if (unit >= pl.g_eff) return;
-    typename NibbleSmem<Pol>::Unit& un = sm.unit[group];
-    const uint32_t kv_base = ptx::smem_addr(&sm.kv[group][0][0][0]);
+    const bool idle = group >= GROUPS || unit >= pl.g_eff;
+    typename NibbleSmem<Pol>::Unit& un = sm.unit[idle ? 0 : group];
+    const uint32_t kv_base = ptx::smem_addr(&sm.kv[idle ? 0 : group][0][0][0]);
     const uint32_t piece_full = ptx::smem_addr(&un.piece_full), piece_empty = ptx::smem_addr(&un.piece_empty);
 
     if (warp >= Pol::kConsumers) {
-        // ======== producers: a thread per two rings of the unit ========
-        // The unit's first walks the schedule and publishes each piece; each fills the slots of
-        // its rings.
+        // ======== producer: a warp per unit ========
+        // All lanes walk the schedule; lane 0 publishes each piece, lane k fills ring k.
+        ptx::fewer_registers<Pol::kProducerRegs>();
+        if (idle) return;
         const uint32_t edge = static_cast<uint32_t>(static_unit_begin(pl, unit + (lane & 1)));
         StaticWalk<NibblePlanTuning> walk(pl, B, __shfl_sync(0xffffffffu, edge, 0),
                                           __shfl_sync(0xffffffffu, edge, 1));
-        if (lane != 0) return;
-        constexpr int kFeeds = Pol::kFeeds, kLoads = 2;   // rings of a producer
-        const int me = (warp - Pol::kConsumers) % kFeeds;
         const uint64_t policy = ptx::policy_evict_first();
         ptx::fence_proxy_async_smem();   // the plan used the slots
-        const bool dynamic = pl.n_dyn > 0;
         const size_t plane = static_cast<size_t>(kPaged ? kBlock : np.rows) * kNibbleRow;   // bytes of a plane
-        uint32_t filled[kLoads];   // blocks sent to rings me, me + kFeeds
-#pragma unroll
-        for (int k = 0; k < kLoads; ++k) filled[k] = 0;
+        const int ring = lane < NC ? lane : 0;
+        uint32_t filled = 0;   // blocks sent to this lane's ring
+        int turn = 0;          // its next slot, and how often the ring went round
+        uint32_t laps = 0;
         bool ok = true;
-        for (uint32_t n = 0; ok; ++n) {
-            int b, kvh, blk0, blk1, lo, hi;
-            if (me == 0) {
-                // the description is free once the others have read the one before
-                ok = wait_bounded(piece_empty, (n & 1u) ^ 1u, &sm.abort_flag, p.ws_flags);
-                if (!ok) break;
-                Piece w;
-                bool whole = false;   // the piece is its segment
-                if (walk.next(pl, KVH, unit, w)) {
-                    whole = w.p1 - w.p0 == pl.n[w.b];
-                } else {
-                    int claimed = -1;
-                    if (!dynamic || !claim_piece(pl, p, claimed, w)) {
+        for (uint32_t n = 0;; ++n) {
+            // the description is free once the consumers have read the one before
+            if (ok) ok = wait_suspended(piece_empty, (n & 1u) ^ 1u, &sm.abort_flag, p.ws_flags);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            Piece w;
+            bool whole = false;   // the piece is its segment
+            if (walk.next(pl, KVH, unit, w)) {
+                whole = w.p1 - w.p0 == pl.n[w.b];
+            } else {
+                int claimed = pl.n_dyn;
+                if (pl.n_dyn > 0) {
+                    if (lane == 0) claimed = static_cast<int>(atomicAdd(p.ws_claim, 1u));
+                    claimed = __shfl_sync(0xffffffffu, claimed, 0);
+                }
+                if (!claim_piece(pl, p, claimed, w)) {
+                    if (lane == 0) {
                         un.piece.done = 1;
                         ptx::mbar_arrive(piece_full);
-                        break;
                     }
+                    break;
                 }
-                const int L = sm.len[w.b];
-                un.piece.b = b = w.b;
-                un.piece.kvh = kvh = w.kvh;
+            }
+            const int hi = sm.len[w.b], lo = p.window > 0 && hi > p.window ? hi - p.window : 0;
+            if (lane == 0) {
+                un.piece.b = w.b;
+                un.piece.kvh = w.kvh;
                 un.piece.p0 = w.p0;
                 un.piece.p1 = w.p1;
-                un.piece.lo = lo = p.window > 0 && L > p.window ? L - p.window : 0;
-                un.piece.hi = hi = L;
+                un.piece.lo = lo;
+                un.piece.hi = hi;
                 un.piece.slot = whole ? -1 : w.slot;
                 un.piece.done = 0;
-                blk0 = w.p0 / kBlock;
-                blk1 = w.p1 / kBlock;
                 ptx::mbar_arrive(piece_full);
-            } else {
-                ok = wait_bounded(piece_full, n & 1u, &sm.abort_flag, p.ws_flags);
-                if (!ok || un.piece.done) break;
-                b = un.piece.b;
-                kvh = un.piece.kvh;
-                blk0 = un.piece.p0 / kBlock;
-                blk1 = un.piece.p1 / kBlock;
-                lo = un.piece.lo;
-                hi = un.piece.hi;
-                ptx::mbar_arrive(piece_empty);
             }
+            if (lane >= NC) continue;
+            int blk = w.p0 / kBlock + lane;
+            const int blk1 = w.p1 / kBlock;
             const int32_t* bt_row =
-                kPaged ? p.block_table + static_cast<size_t>(b) * p.max_pages : nullptr;
+                kPaged ? p.block_table + static_cast<size_t>(w.b) * p.max_pages : nullptr;
             // the head's planes of sequence b, or of page 0
             const uint8_t* head =
-                np.kv + (static_cast<size_t>(kPaged ? 0 : b) * KVH + kvh) * SPLIT * plane;
-            int page[kLoads];   // page ids of the next round, loaded one round ahead
-            if (kPaged) {
-#pragma unroll
-                for (int k = 0; k < kLoads; ++k) {
-                    const int blk = blk0 + me + kFeeds * k;
-                    page[k] = blk < blk1 ? __ldg(bt_row + blk) : 0;
+                np.kv + (static_cast<size_t>(kPaged ? 0 : w.b) * KVH + w.kvh) * SPLIT * plane;
+            int page = kPaged && blk < blk1 ? __ldg(bt_row + blk) : 0;   // (loaded one round ahead)
+            for (; blk < blk1; blk += NC) {
+                const int s = ring * RING + turn;
+                ok = wait_suspended(ptx::smem_addr(&un.empty[s]), (laps & 1u) ^ 1u, &sm.abort_flag, p.ws_flags);
+                if (!ok) break;
+                const uint32_t full_bar = ptx::smem_addr(&un.full[s]);
+                // the attended rows of the block (at least one), no others
+                const int r0 = max(lo - blk * kBlock, 0), r1 = min(hi - blk * kBlock, kBlock);
+                const uint32_t bytes = static_cast<uint32_t>(r1 - r0) * kNibbleRow;
+                const uint8_t* src = head;
+                bool bad = false;
+                if (kPaged) {
+                    bad = page < 0 || page >= p.num_pages;
+                    src += (static_cast<size_t>(page) * KVH * SPLIT * kBlock + r0) * kNibbleRow;
+                    un.bad[s] = bad;
+                    if (blk + NC < blk1) page = __ldg(bt_row + blk + NC);
+                } else {
+                    src += (static_cast<size_t>(blk) * kBlock + r0) * kNibbleRow;
                 }
-            }
-            for (int round = blk0; ok && round < blk1; round += NC) {
+                if (bad) {   // nothing to load: the consumer's weights are NaN
+                    atomicOr(p.ws_flags, kFlagBadPage);
+                    ptx::mbar_arrive(full_bar);
+                } else {
+                    ptx::mbar_arrive_expect_tx(full_bar, SPLIT * bytes);
 #pragma unroll
-                for (int k = 0; k < kLoads; ++k) {
-                    const int ring = me + kFeeds * k, blk = round + ring;
-                    if (blk >= blk1) break;
-                    const int s = ring * RING + static_cast<int>(filled[k] % RING);
-                    ok = wait_bounded(ptx::smem_addr(&un.empty[s]), ((filled[k] / RING) & 1u) ^ 1u,
-                                      &sm.abort_flag, p.ws_flags);
-                    if (!ok) break;
-                    const uint32_t full_bar = ptx::smem_addr(&un.full[s]);
-                    // the attended rows of the block (at least one), no others
-                    const int r0 = max(lo - blk * kBlock, 0), r1 = min(hi - blk * kBlock, kBlock);
-                    const uint32_t bytes = static_cast<uint32_t>(r1 - r0) * kNibbleRow;
-                    const uint8_t* src;
-                    bool bad = false;
-                    if (kPaged) {
-                        bad = page[k] < 0 || page[k] >= p.num_pages;
-                        src = head + (static_cast<size_t>(page[k]) * KVH * SPLIT * kBlock + r0) * kNibbleRow;
-                        un.bad[s] = bad;
-                        if (blk + NC < blk1) page[k] = __ldg(bt_row + blk + NC);
-                    } else {
-                        src = head + (static_cast<size_t>(blk) * kBlock + r0) * kNibbleRow;
-                    }
-                    if (bad) {   // nothing to load: the consumer's weights are NaN
-                        atomicOr(p.ws_flags, kFlagBadPage);
-                        ptx::mbar_arrive(full_bar);
-                    } else {
-                        ptx::mbar_arrive_expect_tx(full_bar, SPLIT * bytes);
-#pragma unroll
-                        for (int h = 0; h < SPLIT; ++h)
-                            ptx::bulk_copy_g2s(kv_base + (s * SPLIT + h) * kTileBytes + r0 * kNibbleRow,
-                                               src + h * plane, bytes, full_bar, policy);
-                    }
-                    ++filled[k];
-                    if ((p.test_flags & kTestStall) && group == 0 && me == 0 && k == 0 && filled[0] == 1)
-                        ok = wait_bounded(ptx::smem_addr(&sm.stall_bar), 0u, &sm.abort_flag,
-                                          p.ws_flags, kTestStallNs);
+                    for (int h = 0; h < SPLIT; ++h)
+                        ptx::bulk_copy_g2s(kv_base + (s * SPLIT + h) * kTileBytes + r0 * kNibbleRow,
+                                           src + h * plane, bytes, full_bar, policy);
+                }
+                ++filled;
+                if (++turn == RING) {
+                    turn = 0;
+                    ++laps;
+                }
+                if ((p.test_flags & kTestStall) && group == 0 && lane == 0 && filled == 1) {
+                    ok = wait_suspended(ptx::smem_addr(&sm.stall_bar), 0u, &sm.abort_flag, p.ws_flags, kTestStallNs);
                     if (!ok) break;
                 }
             }
         }
         // every copy issued lands before the CTA can exit (its consumer may have given up)
-#pragma unroll
-        for (int k = 0; k < kLoads; ++k)
-            for (uint32_t f = filled[k] > RING ? filled[k] - RING : 0u; f < filled[k]; ++f)
-                wait_drain(ptx::smem_addr(&un.full[(me + kFeeds * k) * RING + f % RING]), (f / RING) & 1u);
+        for (uint32_t f = filled > RING ? filled - RING : 0u; f < filled; ++f)
+            wait_drain(ptx::smem_addr(&un.full[ring * RING + f % RING]), (f / RING) & 1u);
         return;
     }
 
     // ===================== consumers =====================
+    ptx::more_registers<Pol::kConsumerRegs>();
+    if (idle) return;
     // Every warp of a unit passes the same barriers for every piece, whatever its waits return:
     // one that gave up (or saw the end) makes all of them leave at the piece's last barrier.
     const int gwarp = warp - group * Pol::GW, own = gwarp / SPLIT, half = gwarp % SPLIT;
     const int bar = 1 + group, pair_bar = 1 + GROUPS + group * NC + own;
+    const uint32_t q_at = ptx::smem_addr(&sm.q[group][half][0][0]);
+    float4 (*sums)[Pol::kRound][Pol::kLanes] = sm.sum[group][half];
     NibbleConsumer<Pol> c;
-    uint32_t taken = 0;   // blocks this warp has processed (its ring's fills, in order)
+    int turn = 0;         // the next slot of this warp's ring, and how often the ring went round
+    uint32_t laps = 0;
+    uint32_t swaps = 0;   // blocks whose scores crossed over
     for (uint32_t n = 0;; ++n) {
         const bool there = __all_sync(0xffffffffu, wait_bounded(piece_full, n & 1u, &sm.abort_flag, p.ws_flags));
         BlockPiece pc{};
         pc.done = 1;
         if (there) pc = un.piece;
         bool gone = pc.done != 0;
-        if (SPLIT > 1) gone = ptx::named_barrier_or(pair_bar, 2 * 32, gone);
         __syncwarp();
         const size_t out_base = (static_cast<size_t>(pc.b) * H + pc.kvh * G) * D;
         if (!gone) {
             if (lane == 0) ptx::mbar_arrive(piece_empty);   // every lane has read it
-            c.begin(p.q + out_base, half, lane);
+            c.begin(p.q + out_base, q_at, own, half, lane);
+        }
+        if (ptx::named_barrier_or(bar, Pol::GW * 32, gone)) break;   // (q is there)
+        {
             // (block i of a piece is warp i % NC's, whatever came before: the order of the sums
             // does not depend on the schedule)
             for (int pos = pc.p0 + own * kBlock; pos < pc.p1; pos += NC * kBlock) {
-                const int s = own * RING + static_cast<int>(taken % RING);
-                gone = !__all_sync(0xffffffffu, wait_bounded(ptx::smem_addr(&un.full[s]), (taken / RING) & 1u,
+                const int s = own * RING + turn;
+                gone = !__all_sync(0xffffffffu, wait_bounded(ptx::smem_addr(&un.full[s]), laps & 1u,
                                                              &sm.abort_flag, p.ws_flags));
                 const uint32_t tile = kv_base + (s * SPLIT + half) * kTileBytes;
                 float z[4];
                 if (SPLIT == 1) {
                     if (gone) break;
-                    c.scores(tile, z, lane);
+                    c.scores(tile, q_at, z, lane);
                 } else {
-                    // the planes' scores cross over through the K codes of this warp's tile, which
-                    // it has read: lane l's at row l / 2
-                    const uint32_t at = (lane >> 1) * kNibbleRow + (lane & 1) * 16;
-                    const uint32_t other = kv_base + (s * SPLIT + 1 - half) * kTileBytes;
+                    // the planes' scores cross over (in two places in turn: a warp may be a block ahead)
+                    float4* cross = sm.cross[group][own][swaps++ & 1u][0];
                     if (!gone) {
-                        c.scores(tile, z, lane);
-                        __syncwarp();
-                        ptx::sts128(tile + at, __float_as_uint(z[0]), __float_as_uint(z[1]),
-                                    __float_as_uint(z[2]), __float_as_uint(z[3]));
+                        c.scores(tile, q_at, z, lane);
+                        cross[half * 32 + lane] = make_float4(z[0], z[1], z[2], z[3]);
                     }
                     gone = ptx::named_barrier_or(pair_bar, 2 * 32, gone);
                     if (gone) break;
-                    const uint4 o = ptx::lds128(other + at);
-                    z[0] += __uint_as_float(o.x);
-                    z[1] += __uint_as_float(o.y);
-                    z[2] += __uint_as_float(o.z);
-                    z[3] += __uint_as_float(o.w);
+                    const float4 o = cross[(1 - half) * 32 + lane];
+                    z[0] += o.x;
+                    z[1] += o.y;
+                    z[2] += o.z;
+                    z[3] += o.w;
                 }
-                const bool bad = kPaged && un.bad[s] != 0;
-                c.weigh(z, tile, pc.lo - pos, pc.hi - pos, bad, lane);
-                if (SPLIT > 1) ptx::fence_proxy_async_smem();   // (the scores, before the next copy)
+                c.weigh(z, tile, pc.lo - pos, pc.hi - pos, kPaged && un.bad[s] != 0, lane);
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&un.empty[s]));
-                ++taken;
+                if (++turn == RING) {
+                    turn = 0;
+                    ++laps;
+                }
             }
-            c.finish(un, own, half, lane);
+            c.finish(un, sums[own], own, half, lane);
         }
         if (ptx::named_barrier_or(bar, Pol::GW * 32, gone)) break;
-        c.merge(un, p, out_base, pc.slot, bar, own, half, lane);
+        c.merge(un, sums, p, out_base, pc.slot, bar, own, half, lane);
+        // (the sums are written again after the barrier that begins the next piece)
     }
 }
 
-// slidingDecodeGQA and decodeGQA, for few and for many segments
-using NibbleSliding = NibblePolicy<2, 2, 4, 4>;
-using NibbleSlidingMany = NibblePolicy<2, 4, 2, 4>;
-using NibbleGlobal = NibblePolicy<8, 1, 4, 4>;
-using NibbleGlobalMany = NibblePolicy<8, 2, 2, 4>;
+// slidingDecodeGQA and decodeGQA
+using NibbleSliding = NibblePolicy<2, 3, 4, 3>;
+using NibbleGlobal = NibblePolicy<8, 3, 2, 2>;
 
 }  // namespace gqa

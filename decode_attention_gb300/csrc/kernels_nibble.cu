@@ -70,12 +70,7 @@ cudaError_t launch_nibble(const LaunchArgs& a, bool sliding, bool paged) {
     p.d = a.p;
     p.kv = static_cast<const uint8_t*>(a.k);
     p.rows = static_cast<int>(a.rows);
-    const bool many = a.p.B * a.p.KVH >= (sliding ? 2 : 1) * a.grid;
-    if (sliding && many)
-        return paged ? launch<NibbleSlidingMany, true>(a, p) : launch<NibbleSlidingMany, false>(a, p);
     if (sliding) return paged ? launch<NibbleSliding, true>(a, p) : launch<NibbleSliding, false>(a, p);
-    if (many)
-        return paged ? launch<NibbleGlobalMany, true>(a, p) : launch<NibbleGlobalMany, false>(a, p);
     return paged ? launch<NibbleGlobal, true>(a, p) : launch<NibbleGlobal, false>(a, p);
 }
 

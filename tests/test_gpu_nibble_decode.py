@@ -182,6 +182,38 @@ def test_scores_of_any_size(layer, size):
 
 
 @pytest.mark.parametrize("layer", ["sliding", "global"])
+@pytest.mark.parametrize("same_sign", [False, True])
+def test_largest_queries_over_the_smallest_keys(layer, same_sign):
+    """Queries around 2^127, of one sign or both (their sum is beyond fp32), over keys of the smallest
+    scale: scores of some 2^110 to 2^120, finite, and 2^90 apart, so that one position of a head has all
+    the weight."""
+    geo = GEO[layer]
+    lens = [1, 30, 200]
+    cache = filled(geo, 3, 200, False, 55)
+    r = cache.want.copy()
+    r[..., 256:264] = 1
+    cache.set_rows(r)
+    cache.k, cache.v = nib.decode(cache.want, geo["D"])
+    g = torch.Generator(device="cuda").manual_seed(56)
+    q = torch.rand((3, geo["H"], geo["D"]), generator=g, device="cuda") + 0.9
+    if not same_sign:
+        q *= torch.sign(torch.rand(q.shape, generator=g, device="cuda") - 0.5)
+    q = (q * 2.0 ** 126).to(torch.bfloat16)
+    out, qd, G = f64(run(cache, q, lens, 0, out_dtype=torch.float32)), f64(q), geo["H"] // geo["KVH"]
+    for b, L in enumerate(lens):
+        for h in range(geo["KVH"]):
+            s = qd[b, h * G:(h + 1) * G] @ cache.k[b, :L, h].T
+            top = np.sort(s, axis=1)
+            # (the rounding of D products in fp32, at most 2^-24 of each for 40 roundings in sequence, and
+            # of the codes' offset of 8, up to 8 / 3 of them, may change the order of what is nearer)
+            clear = np.ones(G, bool) if L == 1 else top[:, -1] - top[:, -2] > 2.0 ** -16 * np.abs(qd[b, h * G:(h + 1) * G]).sum(1) * 7 * 2.0 ** -17
+            want = cache.v[b, s.argmax(1), h]
+            assert np.isfinite(out[b]).all()
+            assert np.abs(out[b, h * G:(h + 1) * G] - want)[clear].max(initial=0) <= 2.0 ** -16 * np.abs(want).max()
+            assert L > 1 or clear.all()
+
+
+@pytest.mark.parametrize("layer", ["sliding", "global"])
 def test_scales_at_the_ends(layer):
     """Values of the smallest and the largest scales side by side, in K and in V."""
     geo = GEO[layer]
