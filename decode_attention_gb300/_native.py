@@ -994,8 +994,8 @@ def gqa_read_nibble_paged(kv_pages: torch.Tensor, block_table: torch.Tensor,
                         stream)
 
 
-def _producer_inputs(q_raw, k_raw, v_raw, w_q, w_k, token_offsets, seq_lens, q_out):
-    """The producer's inputs and q_out as specs; v_raw may be None."""
+def _producer_specs(q_raw, k_raw, v_raw, w_q, w_k, token_offsets, seq_lens, q_out):
+    """The producer's inputs and q_out for _refuse; v_raw may be None."""
     return (("q_raw", q_raw, _BF16, 3), ("k_raw", k_raw, _BF16, 3),
             *((("v_raw", v_raw, _BF16, 3),) if v_raw is not None else ()),
             ("w_q", w_q, _BF16, 1), ("w_k", w_k, _BF16, 1),
@@ -1003,22 +1003,22 @@ def _producer_inputs(q_raw, k_raw, v_raw, w_q, w_k, token_offsets, seq_lens, q_o
             ("seq_lens", seq_lens, torch.int32, 1), ("q_out", q_out, _BF16, 3))
 
 
-def _producer_on(dev: int, specs) -> bool:
-    return all(t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
-               for _, t, dtype, _ in specs)
+def _producer_on(dev: int, q_raw, k_raw, v_raw, w_q, w_k, token_offsets, seq_lens, q_out) -> bool:
+    return (dev >= 0 and _all_on(dev, _BF16, q_raw, k_raw, w_q, w_k, q_out)
+            and (v_raw is None or _all_on(dev, _BF16, v_raw)) and q_raw.dim() == 3
+            and _all_on(dev, torch.int32, token_offsets, seq_lens) and seq_lens.dim() == 1)
 
 
-def _producer_shape(specs, KVH: int, D: int):
-    """(B, N, H) of the producer's inputs for a cache of KVH heads of D."""
-    t = {name: tuple(x.shape) for name, x, _, _ in specs}
-    _require(len(t["q_raw"]) == 3 and len(t["seq_lens"]) == 1, "tensor shapes do not fit together")
-    N, H, _ = t["q_raw"]
-    B, = t["seq_lens"]
-    _require(t["q_raw"] == (N, H, D) and t["q_out"] == (N, H, D), "q_raw and q_out must be [N, H, D]")
-    _require(t["k_raw"] == (N, KVH, D) and t.get("v_raw", t["k_raw"]) == (N, KVH, D),
+def _producer_shape(q_raw, k_raw, v_raw, w_q, w_k, token_offsets, seq_lens, q_out, KVH: int, D: int):
+    """(B, N, H) of the producer's inputs, which passed _producer_on, for a cache of KVH heads of D."""
+    N, H, Dq = shape = q_raw.shape
+    B = seq_lens.shape[0]
+    _require(Dq == D and q_out.shape == shape, "q_raw and q_out must be [N, H, D]")
+    kv = (N, KVH, D)
+    _require(k_raw.shape == kv and (v_raw is None or v_raw.shape == kv),
              "k_raw / v_raw must be [N, KVH, D]")
-    _require(t["w_q"] == (D,) and t["w_k"] == (D,), "w_q / w_k must be [D]")
-    _require(t["token_offsets"] == (B + 1,), "token_offsets must have B + 1 entries")
+    _require(w_q.shape == (D,) and w_k.shape == (D,), "w_q / w_k must be [D]")
+    _require(token_offsets.shape == (B + 1,), "token_offsets must have B + 1 entries")
     return B, N, H
 
 
@@ -1026,15 +1026,15 @@ def _prepare_tokens_nibble(q_raw, k_raw, v_raw, w_q, w_k, token_offsets, block_t
                            q_out, kv, stream):
     dev = _device_of(q_raw)
     _require(v_raw is not None, "v_raw is required")
-    specs = _producer_inputs(q_raw, k_raw, v_raw, w_q, w_k, token_offsets, seq_lens, q_out)
+    inputs = (q_raw, k_raw, v_raw, w_q, w_k, token_offsets, seq_lens, q_out)
     try:
-        ok = dev >= 0 and _producer_on(dev, specs) and _nibble_on(dev, kv, block_table)
+        ok = _producer_on(dev, *inputs) and _nibble_on(dev, kv, block_table)
     except AttributeError:
         ok = False
     if not ok:
-        _refuse(q_raw, *specs, *_nibble_specs(kv, block_table))
-    n, rows, KVH, D = _nibble_shape(kv, seq_lens.numel(), block_table)
-    B, N, H = _producer_shape(specs, KVH, D)
+        _refuse(q_raw, *_producer_specs(*inputs), *_nibble_specs(kv, block_table))
+    n, rows, KVH, D = _nibble_shape(kv, seq_lens.shape[0], block_table)
+    B, N, H = _producer_shape(*inputs, KVH, D)
     head = (q_raw.data_ptr(), k_raw.data_ptr(), v_raw.data_ptr(), w_q.data_ptr(), w_k.data_ptr(),
             token_offsets.data_ptr())
     if block_table is None:
@@ -1069,20 +1069,22 @@ def gqa_prepare_tokens_nibble_paged(q_raw: torch.Tensor, k_raw: torch.Tensor, v_
 def _prepare_tokens(q_raw, k_raw, v_raw, w_q, w_k, token_offsets, block_table, seq_lens, q_out, k, v,
                     ring, stream):
     dev = _device_of(q_raw)
-    specs = _producer_inputs(q_raw, k_raw, v_raw, w_q, w_k, token_offsets, seq_lens, q_out)
-    kind = "cache" if block_table is None else "pages"
-    caches = ((("k_" + kind, k, _BF16, 4),) if k is not None else ()) + (("v_" + kind, v, _BF16, 4),)
-    if block_table is not None:
-        caches += (("block_table", block_table, torch.int32, 2),)
+    inputs = (q_raw, k_raw, v_raw, w_q, w_k, token_offsets, seq_lens, q_out)
     try:
-        ok = dev >= 0 and _producer_on(dev, specs + caches) and v.dim() == 4
+        ok = (_producer_on(dev, *inputs) and _all_on(dev, _BF16, v) and v.dim() == 4
+              and (k is None or _all_on(dev, _BF16, k))
+              and (block_table is None
+                   or (_all_on(dev, torch.int32, block_table) and block_table.dim() == 2)))
     except AttributeError:
         ok = False
     if not ok:
-        _refuse(q_raw, *specs, *caches)
+        kind = "cache" if block_table is None else "pages"
+        _refuse(q_raw, *_producer_specs(*inputs), ("v_" + kind, v, _BF16, 4),
+                *((("k_" + kind, k, _BF16, 4),) if k is not None else ()),
+                *((("block_table", block_table, torch.int32, 2),) if block_table is not None else ()))
     n, rows, KVH, D = shape = v.shape
     _require(k is None or k.shape == shape, "k and v must have the same shape")
-    B, N, H = _producer_shape(specs, KVH, D)
+    B, N, H = _producer_shape(*inputs, KVH, D)
     k_ptr = None if k is None else k.data_ptr()
     head = (q_raw.data_ptr(), k_raw.data_ptr(), None if v_raw is None else v_raw.data_ptr(),
             w_q.data_ptr(), w_k.data_ptr(), token_offsets.data_ptr())
@@ -1091,7 +1093,7 @@ def _prepare_tokens(q_raw, k_raw, v_raw, w_q, w_k, token_offsets, block_table, s
         _call_on(dev, stream, "gqa_prepare_tokens", *head, seq_lens.data_ptr(), B, N, H, KVH, D,
                  q_out.data_ptr(), k_ptr, v.data_ptr(), rows, 1 if ring else 0)
     else:
-        _require(block_table.dim() == 2 and block_table.shape[0] == B, "block_table must have B rows")
+        _require(block_table.shape[0] == B, "block_table must have B rows")
         _call_on(dev, stream, "gqa_prepare_tokens_paged", *head, block_table.data_ptr(),
                  seq_lens.data_ptr(), B, N, n, block_table.shape[1], rows, H, KVH, D,
                  q_out.data_ptr(), k_ptr, v.data_ptr())

@@ -192,6 +192,18 @@ const RopeTurns& rope_turns(int D) {
     return D == 256 ? sliding : global;
 }
 
+template <int D, bool kNibble>
+gqa_status_t launch_tokens(const gqa::PrepareTokensParams& p, int sms, gqa_stream_t stream) {
+    constexpr int kWarps = gqa::kTokensThreads / 32;
+    const int n_units = (p.H + 2 * p.KVH) * D / gqa::kTokensUnit, groups = (n_units + kWarps - 1) / kWarps;
+    // Few tokens: their heads are dealt to several CTAs, so that there is work for all.
+    const int wanted = (4 * sms + p.N - 1) / p.N;
+    const int parts = wanted < groups ? wanted : groups;
+    const unsigned x = clamp_grid(static_cast<uint64_t>(p.N), kNibble ? 2 : 3, sms);
+    return launch(gqa::gqa_prepare_tokens_kernel<D, kNibble>, p, dim3(x, static_cast<unsigned>(parts)),
+                  gqa::kTokensThreads, stream);
+}
+
 gqa_status_t run_producer(const ProducerArgs& a, const gqa::NibbleCache& cache, bool nibble,
                           gqa_stream_t stream) {
     const int sms = gqa::device_sms();
@@ -217,13 +229,8 @@ gqa_status_t run_producer(const ProducerArgs& a, const gqa::NibbleCache& cache, 
     const RopeTurns& r = rope_turns(a.D);
     p.n_rot = r.pairs;
     std::memcpy(p.turn, r.turn, sizeof p.turn);
-    constexpr int kWarps = gqa::kTokensThreads / 32;
-    const unsigned groups = static_cast<unsigned>((a.H + 2 * a.KVH + kWarps - 1) / kWarps);
-    const dim3 grid(clamp_grid(static_cast<uint64_t>(a.N), 4, sms), a.N < 4 * sms ? groups : 1u);
-    void (*kernel)(gqa::PrepareTokensParams) =
-        a.D == 256 ? (nibble ? gqa::gqa_prepare_tokens_kernel<256, true> : gqa::gqa_prepare_tokens_kernel<256, false>)
-                   : (nibble ? gqa::gqa_prepare_tokens_kernel<512, true> : gqa::gqa_prepare_tokens_kernel<512, false>);
-    return launch(kernel, p, grid, gqa::kTokensThreads, stream);
+    if (a.D == 256) return nibble ? launch_tokens<256, true>(p, sms, stream) : launch_tokens<256, false>(p, sms, stream);
+    return nibble ? launch_tokens<512, true>(p, sms, stream) : launch_tokens<512, false>(p, sms, stream);
 }
 
 }  // namespace

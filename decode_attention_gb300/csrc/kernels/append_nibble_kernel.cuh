@@ -21,32 +21,6 @@ struct AppendNibbleParams {
     int B, N;
 };
 
-// Codes (one word) and the scale byte of a lane's eight channels, packed bf16 in channel order; four
-// neighbouring lanes hold a group.
-__device__ __forceinline__ uint32_t nibble_word(const uint4& w, uint32_t* scale) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-    // largest magnitude: the bits of |bf16| order like the values, infinity and NaN above
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = __vmaxu2(m, u[i] & 0x7fff7fffu);
-    m = max(m & 0xffffu, m >> 16);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    if (m >= 0x7f80u) {
-        *scale = kNibbleNanScale;
-        return 0x88888888u;
-    }
-    *scale = nibble_scale_byte(__uint_as_float(m << 16));
-    const float inv = nibble_inverse(nibble_scale(*scale));
-    uint32_t r = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        r |= nibble_code(__uint_as_float(u[i] << 16), inv) << (8 * i);
-        r |= nibble_code(__uint_as_float(u[i] & 0xffff0000u), inv) << (8 * i + 4);
-    }
-    return r;
-}
-
 template <int kPlanes>
 __global__ void __launch_bounds__(kAppendNibbleThreads)
     gqa_append_nibble_kernel(const AppendNibbleParams p) {
@@ -80,7 +54,8 @@ __global__ void __launch_bounds__(kAppendNibbleThreads)
 #pragma unroll
         for (int j = 0; j < kPlanes; ++j) {
             uint32_t ks, vs;
-            const uint32_t kw = nibble_word(k[j], &ks), vw = nibble_word(v[j], &vs);
+            const uint32_t ku[4] = {k[j].x, k[j].y, k[j].z, k[j].w}, vu[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+            const uint32_t kw = nibble_codes(ku, &ks), vw = nibble_codes(vu, &vs);
             uint8_t* r = row + j * stride;
             reinterpret_cast<uint32_t*>(r)[lane] = kw;
             reinterpret_cast<uint32_t*>(r + kNibblePlane / 2)[lane] = vw;

@@ -37,6 +37,12 @@ constexpr int kNibbleScales = 256;    // offset of the scales in a row
 constexpr int kNibblePage = 16;       // positions per page
 constexpr uint32_t kNibbleTopScale = 0xa7, kNibbleNanScale = 0xff;
 
+// Two floats as packed bf16 (lo in the low half).
+__device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
+    const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&t);
+}
+
 // The scale that a byte stands for.
 __device__ __forceinline__ float nibble_scale(uint32_t byte) {
     return __half2float(__ushort_as_half(static_cast<unsigned short>(byte << 7)));
@@ -52,17 +58,45 @@ __device__ __forceinline__ uint32_t nibble_scale_byte(float amax) {
     return min(static_cast<uint32_t>(c), kNibbleTopScale);
 }
 
-// What x is multiplied by ahead of nibble_code: 1 / s and 2^-16 of it more.  x is a bf16 number
-// and s has four bits, so x / s is a tie between two codes or at least 2^-8 of itself away from
-// one: the excess turns ties away from zero and changes nothing else.
-__device__ __forceinline__ float nibble_inverse(float s) {
-    return s > 0.0f ? (1.0f / s) * (1.0f + 0x1p-16f) : 0.0f;
-}
-
-// The code u of x, inv = nibble_inverse(s).
-__device__ __forceinline__ uint32_t nibble_code(float x, float inv) {
-    const float y = fminf(fmaxf(x * inv, -7.0f), 7.0f) + (0x1.8p23f + 8.0f);   // rounded to whole steps
-    return __float_as_uint(y) & 15u;
+// Codes (one word) and the scale byte of a lane's eight channels, packed bf16 in channel order; four
+// neighbouring lanes hold a group.  Some 60 operations.
+//
+// The byte.  amax has the bits (e << 7 | f): it is A 2^n, A = 128 + f.  In the octave above 120 the scales'
+// bounds 7.5 s are 120, 135, 150, ... times 2^n, one byte apart, so the byte is that of 120, 8 e - 920, and
+// ceil((A - 120) / 15) more.  (Below byte 8 the scales are subnormal and spaced evenly.)
+// The codes.  x is a bf16 number and s has four bits, so x / s is a tie between two codes or at least
+// 2^-8 of itself away from one: the reciprocal taken 2^-16 too large turns ties away from zero and
+// changes nothing else.  x is kept below 7.5 s (a bf16 number), rounded by one fma to 1.5 2^23 + 8 + x / s,
+// and the words' low bits are added up by place, less what the rest of the words adds up to.
+__device__ __forceinline__ uint32_t nibble_codes(const uint32_t (&u)[4], uint32_t* scale) {
+    // largest magnitude: the bits of |bf16| order like the values, infinity and NaN above
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __vmaxu2(m, u[i] & 0x7fff7fffu);
+    m = max(m & 0xffffu, m >> 16);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    if (m >= 0x7f80u) {
+        *scale = kNibbleNanScale;
+        return 0x88888888u;
+    }
+    int c = static_cast<int>((m >> 4) & 0xff8u) - 920 + static_cast<int>((((m & 0x7fu) + 22u) * 137u) >> 11);
+    if (c < 8) c = static_cast<int>(nibble_scale_byte(__uint_as_float(m << 16)));
+    c = min(c, static_cast<int>(kNibbleTopScale));
+    *scale = static_cast<uint32_t>(c);
+    const float s = nibble_scale(*scale);
+    const float inv = c > 0 ? ptx::rcp(s) * (1.0f + 0x1p-16f) : 0.0f;
+    const uint32_t below = ((__float_as_uint(7.5f * s) >> 16) - 1u) & 0x7fffu;   // (s == 0: x is, too)
+    const uint32_t top = below | (below << 16), low = top | 0x80008000u;
+    constexpr uint32_t kOne = 0x4b400000u;   // of 1.5 2^23
+    uint32_t r = 0u - kOne * 0x11111111u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t x = ptx::bf16x2_max(ptx::bf16x2_min(u[i], top), low);
+        r += __float_as_uint(fmaf(__uint_as_float(x << 16), inv, 0x1.8p23f + 8.0f)) << (8 * i);
+        r += __float_as_uint(fmaf(__uint_as_float(x & 0xffff0000u), inv, 0x1.8p23f + 8.0f)) << (8 * i + 4);
+    }
+    return r;
 }
 
 // Where the cache holds a row: contiguous [B, planes, rows, 272] or pools [P, planes, 16, 272].

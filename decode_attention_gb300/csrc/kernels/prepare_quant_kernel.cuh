@@ -37,14 +37,15 @@ struct PrepareQuantParams {
 // position below 2^18 by 2^-36 turns.  (In fp64, at 2 operations a clock, the angles of the eight
 // CTAs of a sequence would cost more than its data.)
 
-// One k or v head vector over a warp, as head_norm_rope, in sums of two floats: x becomes what
-// `round` makes of the values (to_odd: floats that round to a code as the values do).
-template <int D, class Round>
-__device__ __forceinline__ void head_norm_rope_twofold(float (&x)[2][D / 64], const __nv_bfloat16* w,
+// One k or v head vector over a warp (or over each kLanes lanes of one; lane: this one's place among
+// them), as head_norm_rope, in sums of two floats: x becomes what `round` makes of the values (to_odd:
+// floats that round to a code as the values do).
+template <int D, int kLanes = 32, class Round>
+__device__ __forceinline__ void head_norm_rope_twofold(float (&x)[2][D / 2 / kLanes], const __nv_bfloat16* w,
                                                        const float2* cs, const float2* cs_l, int n_rot,
                                                        int lane, Round round) {
     constexpr int kHalf = D / 2;
-    constexpr int kPer = kHalf / 32;
+    constexpr int kPer = kHalf / kLanes;
     float ss = 0.0f, ss_l = 0.0f;   // (the square of a bf16 value is exact)
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -55,7 +56,7 @@ __device__ __forceinline__ void head_norm_rope_twofold(float (&x)[2][D / 64], co
             ss_l += t.l;
         }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
+    for (int off = kLanes / 2; off > 0; off >>= 1) {
         const Twofold t = exact_sum(ss, __shfl_xor_sync(0xffffffffu, ss, off));
         ss = t.h;
         ss_l = __fadd_rn(ss_l, __shfl_xor_sync(0xffffffffu, ss_l, off)) + t.l;

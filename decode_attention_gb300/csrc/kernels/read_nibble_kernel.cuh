@@ -3,7 +3,8 @@
 // are.
 //
 // One item is kPlanes planes of a position, taken by a warp: lane l reads the word of channels
-// 8l .. 8l + 7 of K and of V and writes them.
+// 8l .. 8l + 7 of K and of V.  In bf16 it writes them, 16 bytes; in fp32 it takes half a word of another
+// lane, twice, so that a store fills whole lines.
 #pragma once
 
 #include "nibble_cache.cuh"
@@ -21,21 +22,17 @@ struct ReadNibbleParams {
     int B, window, out_rows;
 };
 
-// Eight channels of a word as floats, in channel order.
-__device__ __forceinline__ void nibble_values(uint32_t w, uint32_t scale, float (&x)[8]) {
+// n channels of a word (from its lowest bits on) as floats, in channel order.
+template <int n>
+__device__ __forceinline__ void nibble_values(uint32_t w, uint32_t scale, float (&x)[n]) {
     const float s = scale > kNibbleTopScale ? __uint_as_float(0x7fc00000u) : nibble_scale(scale);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)   // 2^23 + u less 2^23 + 8
+    for (int i = 0; i < n; ++i)   // 2^23 + u less 2^23 + 8
         x[i] = (__uint_as_float(0x4b000000u | ((w >> (4 * i)) & 15u)) - (0x1p23f + 8.0f)) * s;
 }
 
-__device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
-    const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&t);
-}
-
 template <int kPlanes, bool kF32>
-__global__ void __launch_bounds__(kReadNibbleThreads)
+__global__ void __launch_bounds__(kReadNibbleThreads, kF32 ? 6 : 8)
     gqa_read_nibble_kernel(const ReadNibbleParams p) {
     __shared__ BlockIndex idx;
     ptx::grid_dependency_wait();
@@ -77,20 +74,27 @@ __global__ void __launch_bounds__(kReadNibbleThreads)
             ks[j] = __ldg(r + kNibbleScales + lane / 4);
             vs[j] = __ldg(r + kNibbleScales + 8 + lane / 4);
         }
-        const size_t at = ((static_cast<size_t>(b) * p.out_rows + pos) * c.planes + plane) * kNibblePlane + lane * 8;
+        const size_t at = ((static_cast<size_t>(b) * p.out_rows + pos) * c.planes + plane) * kNibblePlane;
 #pragma unroll
         for (int j = 0; j < kPlanes; ++j)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                float y[8];
-                nibble_values(t ? vw[j] : kw[j], t ? vs[j] : ks[j], y);
-                void* out = t ? p.v_out : p.k_out;
+                const uint32_t w = t ? vw[j] : kw[j], sc = t ? vs[j] : ks[j];
                 if (kF32) {
-                    float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at + j * kNibblePlane);
-                    __stcs(o, make_float4(y[0], y[1], y[2], y[3]));
-                    __stcs(o + 1, make_float4(y[4], y[5], y[6], y[7]));
+                    float* out = static_cast<float*>(t ? p.v_out : p.k_out) + at + j * kNibblePlane + 4 * lane;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {   // channels 128 h + 4 lane .. + 3
+                        const int from = 16 * h + (lane >> 1);
+                        const uint32_t half = __shfl_sync(0xffffffffu, w, from) >> (16 * (lane & 1));
+                        float y[4];
+                        nibble_values(half, __shfl_sync(0xffffffffu, sc, from), y);
+                        __stcs(reinterpret_cast<float4*>(out + 128 * h), make_float4(y[0], y[1], y[2], y[3]));
+                    }
                 } else {
-                    __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + at + j * kNibblePlane),
+                    float y[8];
+                    nibble_values(w, sc, y);
+                    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(t ? p.v_out : p.k_out) + at + j * kNibblePlane;
+                    __stcs(reinterpret_cast<uint4*>(out + 8 * lane),
                            make_uint4(bf16x2_bits(y[0], y[1]), bf16x2_bits(y[2], y[3]),
                                       bf16x2_bits(y[4], y[5]), bf16x2_bits(y[6], y[7])));
                 }
