@@ -8,25 +8,23 @@
 // (0, 2^15], where f16 hi + lo parts hold them to 22 bits, or to 2^-25 of a unit, 2^-33 of the largest.
 //
 // Both contractions run as warp-level f16 mma (m16n8k16, fp32 accumulate) with the cache as the A
-// operand, so that the g <= 8 query heads of a KV head fill the 8 columns of B.
-//   scores  S[pos, h] = sum over chunks c (32 channels, one scale) of s_c (U_c . q_c - 8 sum q_c), U the
-//           codes.  ldmatrix gives lane (g, t) the word t of a chunk in rows g and g + 8.  Codes j and
-//           j + 4 of a word lie in the low four bits of its halves: masked they are the f16 numbers
-//           u 2^-24, one place up u 2^-20 (subnormal, and exact in an mma); a shift by 8 brings the
-//           rest.  So a word takes five operations and no conversion; q's fragments make up for the two
-//           places, a chunk's two mma are scaled in fp32, and one mma of all chunks' scales (exact in
-//           f16) with the sums of q (hi and lo parts) takes the 8 off.
+// operand, so that the g <= 8 query heads of a KV head fill the 8 columns of B.  A value
+// (u - 8) s is exact in f16 and takes one fma of two codes: the codes j and j + 4 of a word (or code j
+// of two positions) lie in the low four bits of its halves, and 0x6400 | u is the f16 number
+// 1024 + u, so the value is (1024 + u) s - 1032 s; codes one place up are 1024 + 16 u, times
+// s / 16, less 72 s; a shift by 8 brings the rest.  (With bf16 in place of f16, whose 7 bits of
+// mantissa leave no room for a second place, it takes three shifts for a word and not one.)  The
+// constants are exact as well: 1032 s has 11 bits and is at most 61920.  q is scaled by a power of
+// two per head (at g = 8 per half of D), which makes its bf16 numbers exact in f16 down to 2^-31 of the
+// largest, and within 2^-39 of it below.
+//   scores  S[pos, h] = K[pos, :] . q[h, :] for the 16 positions of a block.  Lane (g, t) reads the
+//           chunks (16 bytes, 32 channels, one scale) t and t + 4 of rows g and g + 8; what order the
+//           channels take in k does not matter, q's B fragments take the same
 //   P.V     O^T[c, h] += V^T[c, pos] P[pos, h]: lane (g, t) reads the chunk g from the rows of its
 //           four positions, a byte permute pairs positions, and code 2m (2m + 1) of every chunk is
-//           the row g (g + 8) of the m-th tile.  Here the scales differ along k, so values are made:
-//           0x6400 | u is the f16 number 1024 + u and (u - 8) s = (1024 + u) s - 1032 s one fma of two
-//           codes; one place up it is 1024 + 16 u, times s / 16, less 72 s.  All of it is exact (1032 s
-//           has 11 bits and is at most 61920).  (bf16, whose 7 bits of mantissa leave no room for a
-//           second place, takes three shifts for a word and not one.)  movmatrix turns the weights
-//           from the scores' layout into B fragments.  At g = 2 the hi and lo parts of P are columns
-//           of one mma; at g = 8 they are two mma.
-// q is scaled by a power of two per head (at g = 8 per half of D): its bf16 numbers are exact in f16 down
-// to 2^-27 of the largest, and within 2^-35 of it below.
+//           the row g (g + 8) of the m-th tile.  movmatrix turns the weights from the scores'
+//           layout into B fragments.  At g = 2 the hi and lo parts of P are columns of one mma; at
+//           g = 8 they are two mma.
 // An mma truncates its sum, so long chains of them drift: a block's products start from zero and
 // are added to the accumulators by ordinary additions.
 //
@@ -36,18 +34,21 @@
 // own, states merged through shared memory at a piece's end, split segments by the combine kernel.  A
 // slot is one block of K, V and scales: one bulk copy per plane of exactly the attended rows.
 //
-// Bound by instructions: some 650 for a block of a plane (4352 bytes), of which 128 mask codes, 64 make
+// Bound by instructions: some 640 for a block of a plane (4352 bytes), of which 128 mask codes, 128 make
 // values, 48 (32) are mma, and an SM's share of HBM brings a block to each scheduler every 740 cycles.
 // Three consumer warps per scheduler (160 registers each, what the producers leave; with four, at 112,
 // spills cost more than they hide) issue in 0.58 of the cycles.  What the steps took, GPU time of
 // decode_sliding_b64_paged / decode_global_b16_long: 8 consumer warps and the mask and the constant of
 // 1024 + u two operations, 85 / 990 us; 12 warps 86 / 860; one operation 80 / 766; producers that fill
 // their rings lane by lane and sleep 76 / 785; q's fragments in shared memory (no spills) 71 / 755; a
-// merge that reads whole states 72 / 718; scores' scales after the mma 67.5 / 736; P.V in two halves (less
-// registers) 68 / 713; the pair's exchange apart from the tiles (no fence between proxies) 68 / 709.
-// Without its copies the kernel takes 739 us where it took 755, without its arithmetic 472.  Tried: P.V
-// of one block between another's scores, 81 / 874 (slots are held longer); sums kept in the mma's
-// accumulator and flushed every 16 blocks, 75 / 711.
+// merge that reads whole states 72 / 718; P.V in two halves (less registers), the pair's exchange apart
+// from the tiles (no fence between proxies) 69 / 732.  Without its copies the kernel took 739 us where it
+// took 755, without its arithmetic 472.
+// Tried: codes of K masked into the mma as subnormal numbers u 2^-24, a chunk's products scaled in fp32
+// afterwards and the 8 taken off with sums of q, 68 / 711, but sums several times the scores, whose
+// rounding is twice the error (1.0e-6 for 4.6e-7 in a plain fp32 evaluation, 3.1e-7 here); P.V of one
+// block between another's scores, 81 / 874 (slots are held longer); sums kept in the mma's accumulator
+// and flushed every 16 blocks, 75 / 711; four chains of scores in place of two 70 / 763.
 #pragma once
 
 #include "decode_kernel.cuh"
@@ -159,7 +160,6 @@ struct NibbleConsumer {
     __device__ static constexpr int place(int j) { return j < 2 ? j : 6 + j; }   // 0, 1, 8, 9
 
     float q_undo[2];             // undo q's scaling for columns 2t and 2t + 1, times log2(e)
-    uint32_t qs[2];              // sums of scaled q over chunks 2t, 2t + 1 of head g, times -2^-5: hi and lo parts
     // tile m: channels 2n (0, 1) and 2n + 1 (2, 3) of chunk g, n = m or, where g & 2, m ^ 8; columns 2t, 2t + 1
     float acc[kTiles][4];
     float ms[2];                 // M of columns 2t, 2t + 1
@@ -172,12 +172,12 @@ struct NibbleConsumer {
     __device__ __forceinline__ void begin(const __nv_bfloat16* q_heads, uint32_t q_at, int own, int half,
                                           int lane) {
         const int g = lane >> 2, t = lane & 3;
-        const __nv_bfloat16* row = q_heads + (g % G) * D + half * kNibblePlane + 8 * t;
+        const __nv_bfloat16* row = q_heads + (g % G) * D + half * kNibblePlane + 32 * t;
         uint32_t top = 0;   // largest |q|: the bits of |bf16| order like the values
         uint4 raw[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {   // channels 8t .. + 7 of chunk i
-            raw[i] = __ldg(reinterpret_cast<const uint4*>(row + 32 * i));
+        for (int i = 0; i < 8; ++i) {   // channels 8 (i % 4) .. + 7 of chunk t + 4 (i / 4)
+            raw[i] = __ldg(reinterpret_cast<const uint4*>(row + (i >> 2) * 128 + (i & 3) * 8));
             top = __vmaxu2(top, __vmaxu2(__vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu),
                                          __vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu)));
         }
@@ -185,28 +185,17 @@ struct NibbleConsumer {
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int e = max(static_cast<int>(top >> 7) - 127, -88);   // |q| < 2^(e + 1)
-        const float f = __int_as_float((10 - e + 127) << 23), f16 = f * 16.0f;
-        float even = 0.0f, odd = 0.0f;   // sums over the chunks 2t and 2t + 1
+        const float f = __int_as_float((14 - e + 127) << 23);   // 2^(14 - e)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {   // pairs of channels (0, 4), (1, 5), (2, 6), (3, 7)
-            const uint4 h = make_uint4(ptx::f16x2_pack(bf16lo(raw[i].x) * f16, bf16lo(raw[i].z) * f16),
-                                       ptx::f16x2_pack(bf16hi(raw[i].x) * f, bf16hi(raw[i].z) * f),
-                                       ptx::f16x2_pack(bf16lo(raw[i].y) * f16, bf16lo(raw[i].w) * f16),
-                                       ptx::f16x2_pack(bf16hi(raw[i].y) * f, bf16hi(raw[i].w) * f));
-            if (i % Pol::NC == own)
-                ptx::sts128(q_at + i * 512 + lane * 16, h.x, h.y, h.z, h.w);
-            const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-            float sum = 0.0f;   // (of scaled values: q itself may add up beyond fp32)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) sum = fmaf(bf16hi(u[k]), f, fmaf(bf16lo(u[k]), f, sum));
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            if (i >> 1 == t) (i & 1 ? odd : even) = sum * -0x1p-5f;   // -8, and 2^-8 to stay in f16
+            if (i % Pol::NC != own) continue;
+            ptx::sts128(q_at + i * 512 + lane * 16,
+                        ptx::f16x2_pack(bf16lo(raw[i].x) * f, bf16lo(raw[i].z) * f),
+                        ptx::f16x2_pack(bf16hi(raw[i].x) * f, bf16hi(raw[i].z) * f),
+                        ptx::f16x2_pack(bf16lo(raw[i].y) * f, bf16lo(raw[i].w) * f),
+                        ptx::f16x2_pack(bf16hi(raw[i].y) * f, bf16hi(raw[i].w) * f));
         }
-        qs[0] = ptx::f16x2_pack(even, odd);
-        const float2 rest = ptx::f16x2_unpack(qs[0]);
-        qs[1] = ptx::f16x2_pack(even - rest.x, odd - rest.y);
-        const float undo = __int_as_float((e - 10 + 127) << 23) * kLog2e;
+        const float undo = __int_as_float((e - 14 + 127) << 23) * kLog2e;
         q_undo[0] = __shfl_sync(0xffffffffu, undo, 8 * t);
         q_undo[1] = __shfl_sync(0xffffffffu, undo, 8 * t + 4);
 #pragma unroll
@@ -222,43 +211,33 @@ struct NibbleConsumer {
     // columns 2t, 2t + 1.
     __device__ __forceinline__ void scores(uint32_t tile, uint32_t q_at, float (&z)[4], int lane) {
         const int g = lane >> 2, t = lane & 3;
-        const uint32_t row = tile + g * kNibbleRow + kNibbleScales;
+        const uint32_t row = tile + g * kNibbleRow;
         constexpr uint32_t k8 = 8 * kNibbleRow;
-        // matrices of ldmatrix: rows 0 .. 7 and 8 .. 15 of a chunk, then of the next
-        const uint32_t at = tile + (lane & 15) * kNibbleRow + (lane >> 4) * 16;
-        const uint2 sa = ptx::lds64(row), sb = ptx::lds64(row + k8);
-        float d[4];
-        // -8 times the scales times the sums of q, in the codes' unit of 2^-20: lane (g, t) holds the scales
-        // of chunks 2t and 2t + 1 in rows g and g + 8, twice (for the sums' hi and lo parts)
-        const uint32_t a0 = __byte_perm(ptx::lds16(row + 2 * t), 0u, 0x1404) >> 1;
-        const uint32_t a1 = __byte_perm(ptx::lds16(row + k8 + 2 * t), 0u, 0x1404) >> 1;
-        ptx::mma_f16_16816_zero(d, a0, a1, a0, a1, qs[0], qs[1]);
+        float c[2][4];   // two chains
 #pragma unroll
-        for (int i = 0; i < 4; ++i) z[i] = d[i] * 0x1p-12f;
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            uint32_t w[4];
-            ptx::ldmatrix_x4(at + 16 * i, w[0], w[1], w[2], w[3]);
-            const uint32_t pick = i & 2 ? 0x3424 : 0x1404;   // scales i and i + 1 of a row as f16
-            const float2 fa = ptx::f16x2_unpack(__byte_perm(i & 4 ? sa.y : sa.x, 0u, pick) >> 1);
-            const float2 fb = ptx::f16x2_unpack(__byte_perm(i & 4 ? sb.y : sb.x, 0u, pick) >> 1);
+            for (int j = 0; j < 4; ++j) c[i][j] = 0.0f;
+        const uint2 sa = ptx::lds64(row + kNibbleScales), sb = ptx::lds64(row + k8 + kNibbleScales);
+        const uint32_t sel = 0x0404u | (t << 4) | (t << 12);   // byte t to the upper bytes of both halves
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint4 q = ptx::lds128(q_at + (i + k) * 512 + lane * 16);
-                const uint32_t a = w[2 * k], b = w[2 * k + 1], ha = a >> 8, hb = b >> 8;
-                ptx::mma_f16_16816_zero(d, a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u,
-                                        q.x, q.y);
-                ptx::mma_f16_16816(d, ha & 0x000f000fu, hb & 0x000f000fu, ha & 0x00f000f0u, hb & 0x00f000f0u,
-                                   q.z, q.w);
-                const float s0 = k ? fa.y : fa.x, s1 = k ? fb.y : fb.x;
-                z[0] = fmaf(d[0], s0, z[0]);
-                z[1] = fmaf(d[1], s0, z[1]);
-                z[2] = fmaf(d[2], s1, z[2]);
-                z[3] = fmaf(d[3], s1, z[3]);
+        for (int i = 0; i < 2; ++i) {
+            const uint4 a = ptx::lds128(row + 16 * t + 64 * i), b = ptx::lds128(row + k8 + 16 * t + 64 * i);
+            const NibbleScale fa(__byte_perm(i ? sa.y : sa.x, 0u, sel) >> 1);
+            const NibbleScale fb(__byte_perm(i ? sb.y : sb.x, 0u, sel) >> 1);
+            const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const uint4 q = ptx::lds128(q_at + (4 * i + w) * 512 + lane * 16);
+                ptx::mma_f16_16816(c[w & 1], fa.low(wa[w], base), fb.low(wb[w], base), fa.high(wa[w], base),
+                                   fb.high(wb[w], base), q.x, q.y);
+                const uint32_t ha = wa[w] >> 8, hb = wb[w] >> 8;
+                ptx::mma_f16_16816(c[w & 1], fa.low(ha, base), fb.low(hb, base), fa.high(ha, base),
+                                   fb.high(hb, base), q.z, q.w);
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) z[i] = z[i] * 0x1p20f * q_undo[i & 1];   // (one factor may pass 2^127)
+        for (int i = 0; i < 4; ++i) z[i] = (c[0][i] + c[1][i]) * q_undo[i & 1];
     }
 
     // The accumulators of columns 2t and 2t + 1 times a and b.

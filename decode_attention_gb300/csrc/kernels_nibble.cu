@@ -24,6 +24,13 @@ cudaError_t launch(const LaunchArgs& a, const DecodeNibbleParams& params) {
         attr_err[dev] = cudaFuncSetAttribute(gqa_decode_nibble_kernel<Pol, kPaged>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(kSmem));
+        // The consumers take the registers that the producers give back of those the block is launched
+        // with: fewer at launch would leave them waiting.
+        cudaFuncAttributes fa;
+        if (attr_err[dev] == cudaSuccess)
+            attr_err[dev] = cudaFuncGetAttributes(&fa, gqa_decode_nibble_kernel<Pol, kPaged>);
+        if (attr_err[dev] == cudaSuccess && fa.numRegs < Pol::kLaunchRegs)
+            attr_err[dev] = cudaErrorInvalidConfiguration;
     });
     if (attr_err[dev] != cudaSuccess) return attr_err[dev];
 
