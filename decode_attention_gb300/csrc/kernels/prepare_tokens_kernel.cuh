@@ -10,14 +10,19 @@
 // the next two tokens are made while the warps work on two, with one barrier per two.  Few tokens are
 // shared by several CTAs (blockIdx.y).
 //
-// Bound by the memory's rate into a bf16 cache, by instructions into the 4-bit one: some 18 for an
-// element, where the memory's rate leaves time for 20 (D = 512).
+// Into a bf16 cache bound by the memory's rate: 10200 tokens at D = 512 in 127 us, 0.97 of a copy's
+// rate; at D = 256 0.93.  Into the 4-bit cache by instructions, 256 for 512 channels at D = 512, more at D = 256,
+// where half of the channels are coded: 475 and 278 us for 33000 and 17000 tokens, 0.78 and 0.48 of the
+// copy's rate.  Two CTAs an SM: three, at 80 registers, spilled (148 us for 127) or, with the weights in
+// shared memory or packed, took 15 to 25% more instructions (525 to 555 us for 475).  Pairs of channels go
+// through packed fp32 operations (516 to 475, 303 to 278; into bf16 140 to 127 with the registers).
 //
 // For the 4-bit cache a k or v vector is rounded to fp32 and to bf16, as a row that an append gets,
 // and coded from there.  An fp32 error moves a value over a border between two bf16 numbers once
 // in some 10^4, and one in forty of those goes over a border between codes, a whole step.  So k and v
-// are looked at: a vector with a value within its error bound of such a border, one in ten, is taken
-// again with norm, weight and rotation to some 2^-30 (twofold.cuh).
+// are looked at: where a value is within its error bound of a border between bf16 numbers (512 channels
+// one time in eight), both ends are coded, and where the codes differ the vectors are taken again with
+// norm, weight and rotation to some 2^-30 (twofold.cuh).
 #pragma once
 
 #include "nibble_cache.cuh"
@@ -26,6 +31,7 @@
 namespace gqa {
 
 constexpr int kTokensThreads = 256;
+constexpr int kTokensPerSm = 2;   // CTAs
 
 struct PrepareTokensParams {
     const __nv_bfloat16* q_raw;     // [N, H, D]
@@ -52,9 +58,9 @@ constexpr int kTokensRing = 4;     // units of a warp in shared memory: one in w
 template <bool kNibble>
 struct TokensSmem {
     uint4 raw[kTokensThreads / 32][kTokensRing][kTokensUnit / 8];
-    // (cos, sin) of two tokens, and of the next two: pair 8 l + e at [e][l] (a lane's eight on distinct banks
-    // from its neighbours'); and in order, with their low parts, for what is taken again
-    float2 cs[2][2][8][kPrepareMaxRot / 8];
+    // cosines and sines of two tokens, and of the next two: those of the pairs 8 l + 2 e and 8 l + 2 e + 1 at [e][l]
+    // (lanes on distinct banks); and (cos, sin) in order, with their low parts, for what is taken again
+    float4 cs[2][2][4][kPrepareMaxRot / 8];
     float2 cs_h[kNibble ? 2 : 1][kNibble ? 2 : 1][kPrepareMaxRot], cs_l[kNibble ? 2 : 1][kNibble ? 2 : 1][kPrepareMaxRot];
     int2 place[2][2];                                  // sequence (-1: none) and position
     TokenIndex idx;
@@ -63,30 +69,24 @@ struct TokensSmem {
 enum class HeadKind { kQuery, kKey, kValue };
 
 // Norm, weight and rotation of a head vector over D / 16 lanes in fp32, rounded to bf16; raw, y: this
-// lane's elements [8 l, 8 l + 8) of each half, packed.  `turns`: they are rotated by co, si.  kDoubt:
-// returns whether an error of fp32 may have changed a bf16 number of this lane.
+// lane's elements [8 l, 8 l + 8) of each half, packed.  `turns`: they are rotated by co, si.  kDoubt: y and
+// below are what the ends of fp32's error round to; returns whether they differ in this lane.
 template <int D, HeadKind kKind, bool kDoubt>
-__device__ __forceinline__ bool head_to_bf16(const uint32_t (&raw)[2][4], const float (&w)[2][8],
-                                             const float (&co)[8], const float (&si)[8], bool turns,
-                                             uint32_t (&y)[2][4]) {
-    constexpr int kPer = 8, kWords = 4;
-    float x[2][kPer];
+__device__ __forceinline__ bool head_to_bf16(const uint32_t (&raw)[2][4], const uint64_t (&w)[2][4],
+                                             const uint64_t (&co)[4], const uint64_t (&si)[4], bool turns,
+                                             uint32_t (&y)[2][4], uint32_t (&below)[2][4]) {
+    constexpr int kWords = 4;   // pairs of neighbouring channels
+    uint64_t x[2][kWords];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int e = 0; e < kWords; ++e) {
-            x[h][2 * e] = __uint_as_float(raw[h][e] << 16);
-            x[h][2 * e + 1] = __uint_as_float(raw[h][e] & 0xffff0000u);
-        }
+        for (int e = 0; e < kWords; ++e) x[h][e] = ptx::f2_from_bf16x2(raw[h][e]);
     // 1 / sqrt(mean(x^2) + 1e-6); the squares are exact and are added up in pairs
-    float sq[kPer];
+    uint64_t sq[kWords];
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) sq[e] = fmaf(x[0][e], x[0][e], __fmul_rn(x[1][e], x[1][e]));
-#pragma unroll
-    for (int n = kPer / 2; n > 0; n >>= 1)
-#pragma unroll
-        for (int e = 0; e < n; ++e) sq[e] += sq[e + n];
-    float ss = sq[0];
+    for (int e = 0; e < kWords; ++e) sq[e] = ptx::f2_fma(x[0][e], x[0][e], ptx::f2_mul(x[1][e], x[1][e]));
+    const float2 s2 = ptx::f2_unpack(ptx::f2_add(ptx::f2_add(sq[0], sq[2]), ptx::f2_add(sq[1], sq[3])));
+    float ss = s2.x + s2.y;
 #pragma unroll
     for (int off = D / 32; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
     const float inv = ptx::rsqrt(fmaf(ss, 1.0f / static_cast<float>(D), 1e-6f));
@@ -97,21 +97,28 @@ __device__ __forceinline__ bool head_to_bf16(const uint32_t (&raw)[2][4], const 
     // its product 1/2 each.
     constexpr float kError = 9.0f * 0x1p-24f, kTurnError = 2.0f * 0x1p-24f;
     const bool rotated = kKind != HeadKind::kValue && (D == 256 || turns);
-    float err[kPer];   // of a rotated pair
+    const uint64_t inv2 = ptx::f2_pack(inv, inv);
+    float2 err[kWords];   // of rotated pairs
+#pragma unroll
+    for (int e = 0; e < kWords; ++e) err[e] = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-            x[h][e] *= inv;
-            if (kKind != HeadKind::kValue) x[h][e] *= w[h][e];
+        for (int e = 0; e < kWords; ++e) {
+            x[h][e] = ptx::f2_mul(x[h][e], inv2);
+            if (kKind != HeadKind::kValue) x[h][e] = ptx::f2_mul(x[h][e], w[h][e]);
         }
     if (rotated) {
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-            const float a = x[0][e], d = x[1][e];
-            x[0][e] = fmaf(a, co[e], -__fmul_rn(d, si[e]));
-            x[1][e] = fmaf(d, co[e], __fmul_rn(a, si[e]));
-            if (kDoubt) err[e] = (fabsf(a) + fabsf(d)) * kTurnError;
+        for (int e = 0; e < kWords; ++e) {
+            const uint64_t a = x[0][e], d = x[1][e];
+            x[0][e] = ptx::f2_sub(ptx::f2_mul(a, co[e]), ptx::f2_mul(d, si[e]));
+            x[1][e] = ptx::f2_fma(d, co[e], ptx::f2_mul(a, si[e]));
+            if (kDoubt) {
+                const float2 a2 = ptx::f2_unpack(a), d2 = ptx::f2_unpack(d);
+                err[e] = ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(fabsf(a2.x) + fabsf(d2.x), fabsf(a2.y) + fabsf(d2.y)),
+                                                    ptx::f2_pack(kTurnError, kTurnError)));
+            }
         }
     }
     uint32_t differ = 0;
@@ -119,21 +126,22 @@ __device__ __forceinline__ bool head_to_bf16(const uint32_t (&raw)[2][4], const 
     for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int e = 0; e < kWords; ++e) {
-            const float v0 = x[h][2 * e], v1 = x[h][2 * e + 1];
+            const float2 v = ptx::f2_unpack(x[h][e]);
             if (kDoubt) {   // (where both ends round alike, so does v)
-                const float e0 = fmaf(fabsf(v0), kError, rotated ? err[2 * e] : 0.0f);
-                const float e1 = fmaf(fabsf(v1), kError, rotated ? err[2 * e + 1] : 0.0f);
-                y[h][e] = bf16x2_bits(v0 + e0, v1 + e1);
-                differ |= y[h][e] ^ bf16x2_bits(v0 - e0, v1 - e1);
+                const uint64_t r = ptx::f2_pack(fmaf(fabsf(v.x), kError, err[e].x), fmaf(fabsf(v.y), kError, err[e].y));
+                const float2 up = ptx::f2_unpack(ptx::f2_add(x[h][e], r)), down = ptx::f2_unpack(ptx::f2_sub(x[h][e], r));
+                y[h][e] = bf16x2_bits(up.x, up.y);
+                below[h][e] = bf16x2_bits(down.x, down.y);
+                differ |= y[h][e] ^ below[h][e];
             } else {
-                y[h][e] = bf16x2_bits(v0, v1);
+                y[h][e] = bf16x2_bits(v.x, v.y);
             }
         }
     return differ != 0;
 }
 
 template <int D, bool kNibble>
-__global__ void __launch_bounds__(kTokensThreads, kNibble ? 2 : 3)
+__global__ void __launch_bounds__(kTokensThreads, kTokensPerSm)
     gqa_prepare_tokens_kernel(const PrepareTokensParams p) {
     constexpr int kHalf = D / 2, kLanes = D / 16, kHeads = kTokensUnit / D;   // lanes of a vector, vectors of a unit
     constexpr int kWarps = kTokensThreads / 32;
@@ -184,7 +192,9 @@ __global__ void __launch_bounds__(kTokensThreads, kNibble ? 2 : 3)
         if (!found) return;
         Twofold co, si;
         cos_sin_of_turn(static_cast<uint64_t>(pos) * p.turn[pair], &co, &si);
-        sm.cs[s][sub][pair % 8][pair / 8] = make_float2(co.h, si.h);
+        float* at = &sm.cs[s][sub][pair % 8 / 2][pair / 8].x + pair % 2;
+        at[0] = co.h;
+        at[2] = si.h;
         if constexpr (kNibble) {
             sm.cs_h[s][sub][pair] = make_float2(co.h, si.h);
             sm.cs_l[s][sub][pair] = make_float2(co.l, si.l);
@@ -193,17 +203,13 @@ __global__ void __launch_bounds__(kTokensThreads, kNibble ? 2 : 3)
 
     for (int n = 0; n + 1 < kTokensRing; ++n) fetch();
     // weights of this lane's elements [8 l, 8 l + 8) of each half
-    float wq[2][8], wk[2][8];
+    uint64_t wq[2][4], wk[2][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-            const uint32_t a = __ldg(reinterpret_cast<const uint32_t*>(p.w_q + h * kHalf + 8 * l + e));
-            const uint32_t b = __ldg(reinterpret_cast<const uint32_t*>(p.w_k + h * kHalf + 8 * l + e));
-            wq[h][e] = __uint_as_float(a << 16);
-            wq[h][e + 1] = __uint_as_float(a & 0xffff0000u);
-            wk[h][e] = __uint_as_float(b << 16);
-            wk[h][e + 1] = __uint_as_float(b & 0xffff0000u);
+        for (int e = 0; e < 4; ++e) {
+            wq[h][e] = ptx::f2_from_bf16x2(__ldg(reinterpret_cast<const uint32_t*>(p.w_q + h * kHalf + 8 * l) + e));
+            wk[h][e] = ptx::f2_from_bf16x2(__ldg(reinterpret_cast<const uint32_t*>(p.w_k + h * kHalf + 8 * l) + e));
         }
     sm.idx.load(p.token_offsets, p.seq_lens, p.B);
     angles(blockIdx.x, 0);
@@ -230,12 +236,12 @@ __global__ void __launch_bounds__(kTokensThreads, kNibble ? 2 : 3)
             have_slot = p.ring ? pos >= sm.idx.len[b] - c.rows : pos < c.rows;
             slot = static_cast<size_t>(b) * c.rows + (p.ring ? pos % c.rows : pos);
         }
-        float co[8], si[8];
+        uint64_t co[4], si[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float2 x = sm.cs[s][sub][e][turns ? l : 0];
-            co[e] = x.x;
-            si[e] = x.y;
+        for (int e = 0; e < 4; ++e) {
+            const float4 x = sm.cs[s][sub][e][turns ? l : 0];
+            co[e] = ptx::f2_pack(x.x, x.y);
+            si[e] = ptx::f2_pack(x.z, x.w);
         }
         for (int u = first; u < n_units; u += step) {
             fetch();
@@ -249,14 +255,14 @@ __global__ void __launch_bounds__(kTokensThreads, kNibble ? 2 : 3)
             // this lane's head of q, k or v
             const int mine = (is_q ? u : is_k ? u - q_units : u - q_units - kv_units) * kHeads + head;
             const uint32_t raw[2][4] = {{r0.x, r0.y, r0.z, r0.w}, {r1.x, r1.y, r1.z, r1.w}};
-            uint32_t y[2][4];
+            uint32_t y[2][4], below[2][4];
             bool doubt = false;
             if (is_q)
-                head_to_bf16<D, HeadKind::kQuery, false>(raw, wq, co, si, turns, y);
+                head_to_bf16<D, HeadKind::kQuery, false>(raw, wq, co, si, turns, y, below);
             else if (is_k)
-                doubt = head_to_bf16<D, HeadKind::kKey, kNibble>(raw, wk, co, si, turns, y);
+                doubt = head_to_bf16<D, HeadKind::kKey, kNibble>(raw, wk, co, si, turns, y, below);
             else
-                doubt = head_to_bf16<D, HeadKind::kValue, kNibble>(raw, wk, co, si, turns, y);
+                doubt = head_to_bf16<D, HeadKind::kValue, kNibble>(raw, wk, co, si, turns, y, below);
             if (!kNibble || is_q) {
                 __nv_bfloat16* dst = is_q ? p.q_out + (static_cast<size_t>(i) * p.H + mine) * D
                                           : (is_k ? p.k_cache : p.v_cache) + (slot * p.KVH + mine) * D;
@@ -267,6 +273,29 @@ __global__ void __launch_bounds__(kTokensThreads, kNibble ? 2 : 3)
                 continue;
             }
             if constexpr (kNibble) {
+                uint32_t codes[2], scale[2];
+                if (__any_sync(0xffffffffu, doubt)) {
+                    // The ends by magnitude, y the larger.  Codes and scale grow with it, so where both ends'
+                    // agree, all between do (ends of two signs are not compared).
+                    bool open = false;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t up = y[h][e], down = below[h][e];
+                            const uint32_t minus = ((up >> 15) & 0x00010001u) * 0xffffu;
+                            open |= ((up ^ down) & 0x80008000u) != 0;
+                            y[h][e] = (down & minus) | (up & ~minus);
+                            below[h][e] = (up & minus) | (down & ~minus);
+                        }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t other;
+                        codes[h] = nibble_codes(y[h], &scale[h]);
+                        open |= nibble_codes(below[h], &other) != codes[h] || other != scale[h];
+                    }
+                    doubt = open;
+                }
                 if (__any_sync(0xffffffffu, doubt)) {
                     float x[2][8];
 #pragma unroll
@@ -285,14 +314,13 @@ __global__ void __launch_bounds__(kTokensThreads, kNibble ? 2 : 3)
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    uint32_t scale;
-                    const uint32_t codes = nibble_codes(y[h], &scale);
+                    codes[h] = nibble_codes(y[h], &scale[h]);
                     // D = 256: both halves in the head's plane; D = 512: one each
                     uint8_t* r = row + (D == 256 ? mine : 2 * mine + h) * stride;
                     const int at = D == 256 ? h * 16 + l : l;   // the word's place in the plane
-                    *reinterpret_cast<uint32_t*>(r + (is_k ? 0 : kNibblePlane / 2) + 4 * at) = codes;
+                    *reinterpret_cast<uint32_t*>(r + (is_k ? 0 : kNibblePlane / 2) + 4 * at) = codes[h];
                     if (l % 4 == 0)
-                        r[kNibbleScales + (is_k ? 0 : 8) + at / 4] = static_cast<uint8_t>(scale);
+                        r[kNibbleScales + (is_k ? 0 : 8) + at / 4] = static_cast<uint8_t>(scale[h]);
                 }
             }
         }
