@@ -66,6 +66,18 @@ struct DecodeNibbleParams {
 struct NibblePlanTuning {
     static constexpr int kAlign = kNibblePage, kExtra = 12;
     static constexpr int kMinShare = 1024, kChunksPerCta = 4;
+    // Few positions in long segments are better off with fewer units, whose pieces are longer (in blocks, a
+    // piece's cost among them).  One, two and three to a CTA, us: slidingDecodeGQA, one sequence of 400
+    // positions 8.0 8.6 8.6, of the whole window 8.8 8.8 9.8, two 10.0 9.8 11.0, five 14.2 13.1 13.8, eight
+    // 18.2 16.4 16.5; decodeGQA, one of 2048 10.5 12.1 14.1, of 16384 22.8 20.5 21.7, of 32768 36.4 29.6 28.8.
+    // Segments of 100 positions, 16 sequences: 12.0 12.1 10.8 and 12.8 12.4 11.7.
+    static constexpr int kUnitsPerCta = 3;
+    __device__ static uint32_t units(uint32_t grid, uint32_t tiles, uint32_t segments) {
+        const uint32_t ctas = grid / kUnitsPerCta;
+        if (tiles <= 14 * ctas && tiles >= (kExtra + 16) * segments) return ctas;
+        if (tiles <= 48 * ctas && tiles > (kExtra + 32) * segments) return 2 * ctas;
+        return grid;
+    }
 };
 
 template <int kG, int kGroups, int kBlocksAtOnce, int kRing>
@@ -86,6 +98,7 @@ struct NibblePolicy {
     static_assert((G == 2 || G == 8) && (NC == 2 || NC == 4), "shape");
     static_assert(kThreads >= kPlanWarps * 32, "the plan takes eight warps");
     static_assert(kConsumers % 4 == 0 && GROUPS <= 4, "warpgroups");
+    static_assert(GROUPS == NibblePlanTuning::kUnitsPerCta, "units");
     static_assert(kConsumers * kConsumerRegs + 4 * kProducerRegs <= (kConsumers + 4) * kLaunchRegs &&
                       kThreads * kLaunchRegs <= 65536,
                   "no share waits for registers that the block was not launched with");
