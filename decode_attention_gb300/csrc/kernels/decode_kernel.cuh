@@ -424,15 +424,13 @@ __device__ __forceinline__ void store_out4(const DecodeParams& p, size_t idx, fl
 // Tune: kAlign widens the ranges to whole blocks of kAlign positions, which makes every
 // piece start and end on a block when `unit` is whole blocks too (the caller masks the
 // positions outside the attended range); kExtra: see static_tiles; kMinShare and
-// kChunksPerCta: the two constants above; units(): how many of them have static tiles.
+// kChunksPerCta: the two constants above.
 // ---------------------------------------------------------------------------
 constexpr int kPlanWarps = kMaxBatch / 32;   // 8
 
 struct PlanTuning {
     static constexpr int kAlign = 1, kExtra = 0;
     static constexpr int kMinShare = kDynMinShare, kChunksPerCta = kDynChunksPerCta;
-    // Units to use of `grid`, for so many static tiles of so many segments.
-    __device__ static uint32_t units(uint32_t grid, uint32_t /* tiles */, uint32_t /* segments */) { return grid; }
 };
 
 template <class Tune = PlanTuning>
@@ -615,8 +613,7 @@ __device__ __forceinline__ void build_plan(PlanSmem& pl, const DecodeParams& p, 
             pl.n_dyn = d_tot + d1_tot;
             pl.c_dyn = c;
             pl.c_dyn1 = c1;
-            const uint32_t units =   // single piece: CTA 0 takes all
-                single ? 1u : Tune::units(static_cast<uint32_t>(grid), st_tot, static_cast<uint32_t>(B * KVH));
+            const uint32_t units = single ? 1u : static_cast<uint32_t>(grid);   // single piece: CTA 0 takes all
             pl.g_eff = static_cast<int>(st_tot < units ? st_tot : units);
         }
         // xsum lies in a stage buffer that TMA writes next: order these generic-proxy

@@ -72,11 +72,10 @@ struct NibblePlanTuning {
     // 18.2 16.4 16.5; decodeGQA, one of 2048 10.5 12.1 14.1, of 16384 22.8 20.5 21.7, of 32768 36.4 29.6 28.8.
     // Segments of 100 positions, 16 sequences: 12.0 12.1 10.8 and 12.8 12.4 11.7.
     static constexpr int kUnitsPerCta = 3;
-    __device__ static uint32_t units(uint32_t grid, uint32_t tiles, uint32_t segments) {
-        const uint32_t ctas = grid / kUnitsPerCta;
+    __device__ static uint32_t units(uint32_t ctas, uint32_t tiles, uint32_t segments) {
         if (tiles <= 14 * ctas && tiles >= (kExtra + 16) * segments) return ctas;
         if (tiles <= 48 * ctas && tiles > (kExtra + 32) * segments) return 2 * ctas;
-        return grid;
+        return kUnitsPerCta * ctas;
     }
 };
 
@@ -505,6 +504,13 @@ __global__ void __launch_bounds__(Pol::kThreads, 1) gqa_decode_nibble_kernel(con
         sm.len[b] = min(max(__ldg(p.seq_lens + b), 0), p.capacity);
     build_plan<NibblePlanTuning>(pl, p, ctas * GROUPS, warp, lane, cta, kBlock,
                                  reinterpret_cast<uint32_t*>(&sm.kv[0][0][0][0]));
+
+    if (tid == 0) {
+        const int units = static_cast<int>(NibblePlanTuning::units(
+            static_cast<uint32_t>(ctas), static_cast<uint32_t>(pl.n_static), static_cast<uint32_t>(B * KVH)));
+        if (units < pl.g_eff) pl.g_eff = units;
+    }
+    __syncthreads();
 
     // zeros for empty sequences and the segments' partial lists, as in decode_kernel.cuh.  (Unit
     // cta + ctas * i is this CTA's i-th: few units still spread over all CTAs.)

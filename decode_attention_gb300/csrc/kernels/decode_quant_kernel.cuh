@@ -71,7 +71,7 @@ struct DecodeQuantParams {
 // fast.  Measured with 4 extra blocks, 256 positions and 8 chunks, and with these:
 // decode_global_b8 37.3 and 31.7 us, decode_sliding_b64_paged 89.4 and 84.6,
 // decode_global_b64_paged 350 and 341.
-struct QuantPlanTuning : PlanTuning {
+struct QuantPlanTuning {
     static constexpr int kAlign = kQuantBlock, kExtra = 12;
     static constexpr int kMinShare = 1024, kChunksPerCta = 4;
 };

@@ -26,7 +26,7 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
-#include "ptx.cuh"
+#include "ptx_more.cuh"
 
 namespace gqa {
 

@@ -5,6 +5,10 @@
 // One item is kPlanes planes of a position, taken by a warp: lane l reads the word of channels
 // 8l .. 8l + 7 of K and of V.  In bf16 it writes them, 16 bytes; in fp32 it takes half a word of another
 // lane, twice, so that a store fills whole lines.
+//
+// Bound by the memory's rate, four fifths of it writes: 16 decodeGQA sequences of up to 32768 positions, paged,
+// 448 to 454 us in bf16, 0.87 of a copy's rate; of up to 16384 in fp32 378 us, 0.93 (570 with a lane's own
+// channels, whose two stores each filled half of their sectors).
 #pragma once
 
 #include "nibble_cache.cuh"

@@ -512,8 +512,8 @@ gqa_status_t gqa_decode_quant_paged(const void *q, const void *k_pages, const vo
  *                  [token_offsets[b], token_offsets[b + 1]) of k_new and v_new
  *   seq_lens       int32 [B] (device): lengths AFTER the append; with n_b new tokens
  *                  they go to the positions [L_b - n_b, L_b)
- * Sequences without new tokens are skipped, and so is a sequence whose offsets lie outside
- * [0, N] or whose length is below n_b or above the capacity.  A page id outside [0, P)
+ * Sequences without new tokens are skipped, and so are rows behind token_offsets[B] and a
+ * sequence whose offsets lie outside [0, N] or whose length is below n_b or above the capacity.  A page id outside [0, P)
  * skips its positions (the decode call then reports it).  The positions written by one call
  * must be distinct: sequences that share a page must not both write to the same slot of it.
  * N == 0 or B == 0: GQA_OK, nothing enqueued.  Errors as for gqa_decode and
@@ -565,7 +565,8 @@ gqa_status_t gqa_read_nibble_paged(const void *kv_pages, const int32_t *block_ta
  *                  earlier ones of the call are skipped); or page pools as for
  *                  gqa_prepare_decode_paged, where a page id outside [0, P) skips the write
  * A sequence whose offsets lie outside [0, N] or whose length is below n_b is skipped whole,
- * its rows of q_out included; a token that is not written to the cache still gets its q_out.
+ * its rows of q_out included, and so are rows that belong to no sequence (behind
+ * token_offsets[B]); a token that is not written to the cache still gets its q_out.
  * Arithmetic is fp32, the angles' reduction exact; outputs are rounded to bf16 (nearest
  * even).  The positions written by one call must be distinct.  N == 0 or B == 0: GQA_OK,
  * nothing enqueued.  One kernel launch, no workspace.  Errors as for gqa_prepare_decode (N
@@ -586,9 +587,9 @@ gqa_status_t gqa_prepare_tokens_paged(const void *q_raw, const void *k_raw, cons
 
 /*
  * gqa_prepare_tokens into the 4-bit cache (v_raw is required).  A key or value is rounded to
- * fp32, from there to bf16, and coded by gqa_append_nibble's rule; it is computed to some
- * 2^-30, so its bf16 number is that of the exact value but for about one in 10^6.  A
- * token past the capacity or on a page id outside [0, P) is not written.  One token per
+ * fp32, from there to bf16, and coded by gqa_append_nibble's rule; where that matters it is
+ * computed to some 2^-30, so its code is that of the exact value so rounded but for fewer than one
+ * in 10^6.  A token past the capacity or on a page id outside [0, P) is not written.  One token per
  * sequence (token_offsets[b] = b) is the decode step's producer for this cache.
  */
 gqa_status_t gqa_prepare_tokens_nibble(const void *q_raw, const void *k_raw, const void *v_raw,
@@ -608,8 +609,11 @@ gqa_status_t gqa_prepare_tokens_nibble_paged(const void *q_raw, const void *k_ra
 /*
  * gqa_decode and gqa_decode_paged over the 4-bit cache: the same attention core on the
  * values (u - 8) * s.  Scores, softmax and sums are held in fp32, and the weights are
- * applied to at least 16 significant bits.  Everything else -- q, window, out, workspace
- * (the same size), status bits, errors -- is as for gqa_decode and gqa_decode_paged.
+ * applied to at least 16 significant bits (weights below 2^-16 of the largest to within 2^-32 of
+ * it).  Elements of q down to 2^-31 of their head's largest (of each half's, at D = 512) count
+ * exactly; smaller ones are rounded to within 2^-39 of it (or 2^-127).
+ * Everything else -- q, window, out, workspace (the same size), status bits, errors -- is
+ * as for gqa_decode and gqa_decode_paged.
  */
 gqa_status_t gqa_decode_nibble(const void *q, const void *kv, const int32_t *seq_lens, int B, int S,
                                int H, int KVH, int D, int window, void *out,
