@@ -5,8 +5,8 @@
 // word of the row.  Rows stand by themselves, so there is no order between items and nothing is
 // read back.
 //
-// Bound by the memory's rate: 66000 tokens of slidingDecodeGQA in 228 us, 0.88 of a copy's rate, with the
-// ALU pipe busy two thirds of the time (codes in floating point and by comparisons took 307 us).  Four planes
+// Bound by the memory's rate: 65500 tokens of slidingDecodeGQA in 220 us, 0.91 of a copy's rate (with codes in
+// floating point and by comparisons 307 us, with a branch for each of their seldom cases 228).  Four planes
 // an item put eight loads of a lane in flight.  (A row is eight sectors and a half; the shared ones meet in L2.)
 #pragma once
 

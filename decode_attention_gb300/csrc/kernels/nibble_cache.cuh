@@ -76,18 +76,18 @@ __device__ __forceinline__ uint32_t nibble_codes(const uint32_t (&u)[4], uint32_
     m = max(m & 0xffffu, m >> 16);
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    if (m >= 0x7f80u) {
-        *scale = kNibbleNanScale;
-        return 0x88888888u;
+    uint32_t c = ((m >> 4) & 0xff8u) - 920u + ((((m & 0x7fu) + 22u) * 137u) >> 11), byte = c;
+    float up = 1.0f + 0x1p-16f;
+    if (c - 8u > kNibbleTopScale - 8u) {   // (seldom) subnormal scales, zeros, beyond the largest, not finite
+        const bool finite = m < 0x7f80u;
+        byte = finite ? nibble_scale_byte(__uint_as_float(m << 16)) : kNibbleNanScale;
+        c = finite && byte > 0 ? byte : 8u;
+        if (!finite) up = 0.0f;            // codes 8
     }
-    int c = static_cast<int>((m >> 4) & 0xff8u) - 920 + static_cast<int>((((m & 0x7fu) + 22u) * 137u) >> 11);
-    if (c < 8) c = static_cast<int>(nibble_scale_byte(__uint_as_float(m << 16)));
-    c = min(c, static_cast<int>(kNibbleTopScale));
-    *scale = static_cast<uint32_t>(c);
-    const float s = nibble_scale(*scale);
-    const float inv = c > 0 ? ptx::rcp(s) * (1.0f + 0x1p-16f) : 0.0f;
-    const uint32_t below = ((__float_as_uint(7.5f * s) >> 16) - 1u) & 0x7fffu;   // (s == 0: x is, too)
-    const uint32_t top = below | (below << 16), low = top | 0x80008000u;
+    *scale = byte;
+    const float s = nibble_scale(c);
+    const float inv = ptx::rcp(s) * up;
+    const uint32_t top = __byte_perm(__float_as_uint(7.5f * s), 0u, 0x3232) - 0x00010001u, low = top | 0x80008000u;
     constexpr uint32_t kOne = 0x4b400000u;   // of 1.5 2^23
     uint32_t r = 0u - kOne * 0x11111111u;
 #pragma unroll

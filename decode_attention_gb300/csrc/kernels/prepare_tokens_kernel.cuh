@@ -10,12 +10,14 @@
 // the next two tokens are made while the warps work on two, with one barrier per two.  Few tokens are
 // shared by several CTAs (blockIdx.y).
 //
-// Into a bf16 cache bound by the memory's rate: 10200 tokens at D = 512 in 127 us, 0.97 of a copy's
-// rate; at D = 256 0.93.  Into the 4-bit cache by instructions, 256 for 512 channels at D = 512, more at D = 256,
-// where half of the channels are coded: 475 and 278 us for 33000 and 17000 tokens, 0.78 and 0.48 of the
-// copy's rate.  Two CTAs an SM: three, at 80 registers, spilled (148 us for 127) or, with the weights in
-// shared memory or packed, took 15 to 25% more instructions (525 to 555 us for 475).  Pairs of channels go
-// through packed fp32 operations (516 to 475, 303 to 278; into bf16 140 to 127 with the registers).
+// Bound by the memory's rate into a bf16 cache, 10200 tokens at D = 512 in 128 us, 0.96 of a copy's rate (at
+// D = 256 0.96), and at D = 512 into the 4-bit one, 33000 tokens in 400 us, 0.93; by instructions into the
+// 4-bit one at D = 256, where half of the channels are coded, 17000 tokens in 229 us, 0.58.  Two CTAs an SM:
+// three, at 80 registers, spilled (148 us for 127) or, with the weights in shared memory or packed, took 15
+// to 25% more instructions (525 to 555 us for 475 then).  Pairs of channels go through packed fp32
+// operations (516 to 475, 303 to 278; into bf16 140 to 127 with the registers), the ends are coded once where
+// they agree and leave codes' seldom cases to one branch (to 451 and 251), and what a warp branches on is
+// seen to be the warp's (to 400 and 229).
 //
 // For the 4-bit cache a k or v vector is rounded to fp32 and to bf16, as a row that an append gets,
 // and coded from there.  An fp32 error moves a value over a border between two bf16 numbers once
@@ -128,8 +130,15 @@ __device__ __forceinline__ bool head_to_bf16(const uint32_t (&raw)[2][4], const 
         for (int e = 0; e < kWords; ++e) {
             const float2 v = ptx::f2_unpack(x[h][e]);
             if (kDoubt) {   // (where both ends round alike, so does v)
-                const uint64_t r = ptx::f2_pack(fmaf(fabsf(v.x), kError, err[e].x), fmaf(fabsf(v.y), kError, err[e].y));
-                const float2 up = ptx::f2_unpack(ptx::f2_add(x[h][e], r)), down = ptx::f2_unpack(ptx::f2_sub(x[h][e], r));
+                float2 up, down;
+                if (kKind == HeadKind::kValue) {   // (by magnitude)
+                    up = ptx::f2_unpack(ptx::f2_mul(x[h][e], ptx::f2_pack(1.0f + kError, 1.0f + kError)));
+                    down = ptx::f2_unpack(ptx::f2_mul(x[h][e], ptx::f2_pack(1.0f - kError, 1.0f - kError)));
+                } else {
+                    const uint64_t r = ptx::f2_pack(fmaf(fabsf(v.x), kError, err[e].x), fmaf(fabsf(v.y), kError, err[e].y));
+                    up = ptx::f2_unpack(ptx::f2_add(x[h][e], r));
+                    down = ptx::f2_unpack(ptx::f2_sub(x[h][e], r));
+                }
                 y[h][e] = bf16x2_bits(up.x, up.y);
                 below[h][e] = bf16x2_bits(down.x, down.y);
                 differ |= y[h][e] ^ below[h][e];
@@ -151,7 +160,8 @@ __global__ void __launch_bounds__(kTokensThreads, kTokensPerSm)
     ptx::allow_dependent_launch();
 
     const NibbleCache& c = p.cache;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (so that branches on it are seen to be a warp's)
     const int l = lane % kLanes, head = lane / kLanes;   // place in a vector, and which of a unit's it is
     const int q_units = p.H / kHeads, kv_units = p.KVH / kHeads, n_units = q_units + 2 * kv_units;
     const int first = blockIdx.y * kWarps + warp, step = gridDim.y * kWarps;
@@ -219,7 +229,9 @@ __global__ void __launch_bounds__(kTokensThreads, kTokensPerSm)
     int s = 0;   // stage of the angles
     for (int i = blockIdx.x, sub = 0; i < p.N; i += gridDim.x) {
         if (sub == 0) angles(i + 2 * gridDim.x, s ^ 1);
-        const int b = sm.place[s][sub].x, pos = sm.place[s][sub].y;
+        const int2 at = sm.place[s][sub];
+        const int b = at.x, pos = at.y;
+        const bool found = __any_sync(0xffffffffu, b >= 0);   // (one answer for the warp)
         // the token's place: null (no slot) when it is not written
         uint8_t* row = nullptr;
         bool have_slot = false;
@@ -236,6 +248,7 @@ __global__ void __launch_bounds__(kTokensThreads, kTokensPerSm)
             have_slot = p.ring ? pos >= sm.idx.len[b] - c.rows : pos < c.rows;
             slot = static_cast<size_t>(b) * c.rows + (p.ring ? pos % c.rows : pos);
         }
+        const bool kept = __any_sync(0xffffffffu, kNibble ? row != nullptr : have_slot);
         uint64_t co[4], si[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -251,7 +264,7 @@ __global__ void __launch_bounds__(kTokensThreads, kTokensPerSm)
             const uint4 r0 = from[0], r1 = from[D / 16];
             __syncwarp();   // (the slot is filled again)
             const bool is_q = u < q_units, is_k = !is_q && u < q_units + kv_units;
-            if (b < 0 || (!is_q && (kNibble ? row == nullptr : !have_slot || (is_k && keqv)))) continue;
+            if (!found || (!is_q && (!kept || (!kNibble && is_k && keqv)))) continue;
             // this lane's head of q, k or v
             const int mine = (is_q ? u : is_k ? u - q_units : u - q_units - kv_units) * kHeads + head;
             const uint32_t raw[2][4] = {{r0.x, r0.y, r0.z, r0.w}, {r1.x, r1.y, r1.z, r1.w}};
@@ -273,11 +286,11 @@ __global__ void __launch_bounds__(kTokensThreads, kTokensPerSm)
                 continue;
             }
             if constexpr (kNibble) {
-                uint32_t codes[2], scale[2];
-                if (__any_sync(0xffffffffu, doubt)) {
-                    // The ends by magnitude, y the larger.  Codes and scale grow with it, so where both ends'
-                    // agree, all between do (ends of two signs are not compared).
-                    bool open = false;
+                // The ends by magnitude, y the larger (a value's are so already).  Codes and scale grow with it, so
+                // where both ends' agree, all between do (ends of two signs are not compared).
+                const bool twice = __any_sync(0xffffffffu, doubt);
+                bool open = false;
+                if (twice && is_k) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -288,15 +301,18 @@ __global__ void __launch_bounds__(kTokensThreads, kTokensPerSm)
                             y[h][e] = (down & minus) | (up & ~minus);
                             below[h][e] = (up & minus) | (down & ~minus);
                         }
+                }
+                uint32_t codes[2], scale[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) codes[h] = nibble_codes(y[h], &scale[h]);
+                if (twice) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t other;
-                        codes[h] = nibble_codes(y[h], &scale[h]);
                         open |= nibble_codes(below[h], &other) != codes[h] || other != scale[h];
                     }
-                    doubt = open;
                 }
-                if (__any_sync(0xffffffffu, doubt)) {
+                if (twice && __any_sync(0xffffffffu, open)) {
                     float x[2][8];
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
@@ -311,10 +327,11 @@ __global__ void __launch_bounds__(kTokensThreads, kTokensPerSm)
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) y[h][e] = bf16x2_bits(x[h][2 * e], x[h][2 * e + 1]);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) codes[h] = nibble_codes(y[h], &scale[h]);
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    codes[h] = nibble_codes(y[h], &scale[h]);
                     // D = 256: both halves in the head's plane; D = 512: one each
                     uint8_t* r = row + (D == 256 ? mine : 2 * mine + h) * stride;
                     const int at = D == 256 ? h * 16 + l : l;   // the word's place in the plane
