@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(Pol::kThreads, 1) gqa_decode_nibble_kernel(con
         smem_raw + ((128u - (ptx::smem_addr(smem_raw) & 127u)) & 127u));
 
     const int tid = threadIdx.x;
-    const int warp = tid >> 5, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int B = p.B, KVH = p.KVH, H = p.H;
     const int cta = blockIdx.x, ctas = static_cast<int>(gridDim.x);
     PlanSmem& pl = sm.plan;
