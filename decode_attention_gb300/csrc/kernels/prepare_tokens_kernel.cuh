@@ -11,20 +11,20 @@
 // shared by several CTAs (blockIdx.y).
 //
 // Bound by the memory's rate into a bf16 cache, 10200 tokens at D = 512 in 128 us, 0.96 of a copy's rate (at
-// D = 256 0.96), and at D = 512 into the 4-bit one, 33000 tokens in 400 us, 0.93; by instructions into the
-// 4-bit one at D = 256, where half of the channels are coded, 17000 tokens in 229 us, 0.58.  Two CTAs an SM:
+// D = 256 0.96), and at D = 512 into the 4-bit one, 33000 tokens in 402 us, 0.92; by instructions into the
+// 4-bit one at D = 256, where half of the channels are coded, 17000 tokens in 234 us, 0.57.  Two CTAs an SM:
 // three, at 80 registers, spilled (148 us for 127) or, with the weights in shared memory or packed, took 15
 // to 25% more instructions (525 to 555 us for 475 then).  Pairs of channels go through packed fp32
 // operations (516 to 475, 303 to 278; into bf16 140 to 127 with the registers), the ends are coded once where
 // they agree and leave codes' seldom cases to one branch (to 451 and 251), and what a warp branches on is
-// seen to be the warp's (to 400 and 229).
+// seen to be the warp's (to 400 and 229; the error's bound, wider since, costs 2 and 5).
 //
 // For the 4-bit cache a k or v vector is rounded to fp32 and to bf16, as a row that an append gets,
 // and coded from there.  An fp32 error moves a value over a border between two bf16 numbers once
 // in some 10^4, and one in forty of those goes over a border between codes, a whole step.  So k and v
-// are looked at: where a value is within its error bound of a border between bf16 numbers (512 channels
-// one time in eight), both ends are coded, and where the codes differ the vectors are taken again with
-// norm, weight and rotation to some 2^-30 (twofold.cuh).
+// are looked at: where a value is within its error bound of a border between bf16 numbers (two in five of
+// 512 rotated channels, one in eight of others), both ends are coded, and where the codes differ (one in a
+// hundred) the vectors are taken again with norm, weight and rotation to some 2^-30 (twofold.cuh).
 #pragma once
 
 #include "nibble_cache.cuh"
@@ -92,12 +92,12 @@ __device__ __forceinline__ bool head_to_bf16(const uint32_t (&raw)[2][4], const 
 #pragma unroll
     for (int off = D / 32; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
     const float inv = ptx::rsqrt(fmaf(ss, 1.0f / static_cast<float>(D), 1e-6f));
-    // The fp32 error of a value y, in units of 2^-24: of |y| what all of the vector share, the sum's 9
-    // levels at most, halved by the root, its scaling 1/4 and the reciprocal root 2.2, then the product
-    // with x, the weight or a rotation's sum 1/2 each, and 1 for the sums below: 8.95 (a rotation: 8.45).
-    // Of |a| + |d|, which a rotated y is made of, the products with x, the weight, cosine or sine and
-    // its product 1/2 each.
-    constexpr float kError = 9.0f * 0x1p-24f, kTurnError = 2.0f * 0x1p-24f;
+    // The fp32 error of a value y, in units of 2^-24, of which a rounding takes one at most.  Of |y|: what all
+    // of the vector share, the sum's 9 levels and its scaling, halved by the root, and the reciprocal root 2.2;
+    // then the product with x and the weight, or a rotation's sum; and 1 for the sums below: 10.2 (a value:
+    // 9.2, a rotation: 9.2).  Of |a| + |d|, which a rotated y is made of, the products with x and the weight,
+    // cosine or sine and its product: 4.
+    constexpr float kError = 10.5f * 0x1p-24f, kValueError = 10.0f * 0x1p-24f, kTurnError = 4.01f * 0x1p-24f;
     const bool rotated = kKind != HeadKind::kValue && (D == 256 || turns);
     const uint64_t inv2 = ptx::f2_pack(inv, inv);
     float2 err[kWords];   // of rotated pairs
@@ -131,9 +131,9 @@ __device__ __forceinline__ bool head_to_bf16(const uint32_t (&raw)[2][4], const 
             const float2 v = ptx::f2_unpack(x[h][e]);
             if (kDoubt) {   // (where both ends round alike, so does v)
                 float2 up, down;
-                if (kKind == HeadKind::kValue) {   // (by magnitude)
-                    up = ptx::f2_unpack(ptx::f2_mul(x[h][e], ptx::f2_pack(1.0f + kError, 1.0f + kError)));
-                    down = ptx::f2_unpack(ptx::f2_mul(x[h][e], ptx::f2_pack(1.0f - kError, 1.0f - kError)));
+                if (kKind == HeadKind::kValue) {   // (by magnitude; both factors are fp32 numbers)
+                    up = ptx::f2_unpack(ptx::f2_mul(x[h][e], ptx::f2_pack(1.0f + kValueError, 1.0f + kValueError)));
+                    down = ptx::f2_unpack(ptx::f2_mul(x[h][e], ptx::f2_pack(1.0f - kValueError, 1.0f - kValueError)));
                 } else {
                     const uint64_t r = ptx::f2_pack(fmaf(fabsf(v.x), kError, err[e].x), fmaf(fabsf(v.y), kError, err[e].y));
                     up = ptx::f2_unpack(ptx::f2_add(x[h][e], r));
