@@ -36,19 +36,20 @@
 //
 // Bound by instructions: some 640 for a block of a plane (4352 bytes), of which 128 mask codes, 128 make
 // values, 48 (32) are mma, and an SM's share of HBM brings a block to each scheduler every 740 cycles.
-// Three consumer warps per scheduler (160 registers each, what the producers leave; with four, at 112,
-// spills cost more than they hide) issue in 0.58 of the cycles.  What the steps took, GPU time of
+// Three consumer warps per scheduler (160 registers each, what the producers leave) issue in 0.58 of the
+// cycles; four, at 112, took 70 / 709 us where three take 67 / 698.  What the steps took, GPU time of
 // decode_sliding_b64_paged / decode_global_b16_long: 8 consumer warps and the mask and the constant of
 // 1024 + u two operations, 85 / 990 us; 12 warps 86 / 860; one operation 80 / 766; producers that fill
-// their rings lane by lane and sleep 76 / 785; q's fragments in shared memory (no spills) 71 / 755; a
+// their rings lane by lane and sleep 76 / 785; q's fragments in shared memory (fewer spills) 71 / 755; a
 // merge that reads whole states 72 / 718; P.V in two halves (less registers), the pair's exchange apart
-// from the tiles (no fence between proxies) 69 / 732.  Without its copies the kernel took 739 us where it
-// took 755, without its arithmetic 472.
+// from the tiles (no fence between proxies) 69 / 732; a warp's index that the compiler sees to be one (no
+// spills, plain branches) 67 / 698.
 // Tried: codes of K masked into the mma as subnormal numbers u 2^-24, a chunk's products scaled in fp32
 // afterwards and the 8 taken off with sums of q, 68 / 711, but sums several times the scores, whose
 // rounding is twice the error (1.0e-6 for 4.6e-7 in a plain fp32 evaluation, 3.1e-7 here); P.V of one
 // block between another's scores, 81 / 874 (slots are held longer); sums kept in the mma's accumulator
-// and flushed every 16 blocks, 75 / 711; four chains of scores in place of two 70 / 763.
+// and flushed every 16 blocks, 75 / 711; four chains of scores in place of two 67 / 711; the first codes of V
+// loaded ahead of the weights 67 / 700, and 151 us for 149 over 64 sequences of up to 8192 positions.
 #pragma once
 
 #include "decode_kernel.cuh"
@@ -68,9 +69,9 @@ struct NibblePlanTuning {
     static constexpr int kMinShare = 1024, kChunksPerCta = 4;
     // Few positions in long segments are better off with fewer units, whose pieces are longer (in blocks, a
     // piece's cost among them).  One, two and three to a CTA, us: slidingDecodeGQA, one sequence of 400
-    // positions 8.0 8.6 8.6, of the whole window 8.8 8.8 9.8, two 10.0 9.8 11.0, five 14.2 13.1 13.8, eight
-    // 18.2 16.4 16.5; decodeGQA, one of 2048 10.5 12.1 14.1, of 16384 22.8 20.5 21.7, of 32768 36.4 29.6 28.8.
-    // Segments of 100 positions, 16 sequences: 12.0 12.1 10.8 and 12.8 12.4 11.7.
+    // positions 7.7 8.4 8.5, of the whole window 8.5 8.5 9.6, two 9.7 9.6 10.8, five 13.5 12.8 13.6, eight
+    // 17.3 15.9 16.1; decodeGQA, one of 2048 9.9 11.8 13.7, of 16384 20.4 19.4 20.6, of 32768 31.9 27.5 27.1.
+    // Segments of 100 positions, 16 sequences: 11.3 11.7 10.5 and 11.5 12.0 11.2.
     static constexpr int kUnitsPerCta = 3;
     __device__ static uint32_t units(uint32_t ctas, uint32_t tiles, uint32_t segments) {
         if (tiles <= 14 * ctas && tiles >= (kExtra + 16) * segments) return ctas;
@@ -477,7 +478,7 @@ __global__ void __launch_bounds__(Pol::kThreads, 1) gqa_decode_nibble_kernel(con
         smem_raw + ((128u - (ptx::smem_addr(smem_raw) & 127u)) & 127u));
 
     const int tid = threadIdx.x;
-    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;   // (branches on it are a warp's)
     const int B = p.B, KVH = p.KVH, H = p.H;
     const int cta = blockIdx.x, ctas = static_cast<int>(gridDim.x);
     PlanSmem& pl = sm.plan;
