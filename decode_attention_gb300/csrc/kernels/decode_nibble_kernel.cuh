@@ -33,6 +33,9 @@
 // warps of a unit (at g = 8 pairs, a plane each) on a block each with a ring of slots of their
 // own, states merged through shared memory at a piece's end, split segments by the combine kernel.  A
 // slot is one block of K, V and scales: one bulk copy per plane of exactly the attended rows.
+// A slot is free when its warps' loads are done: each lane's fence between the proxies stands ahead of the
+// arrival, as a copy may overtake loads that are only issued.  (Without it one call in some 1000 over large
+// sliding batches found other codes in part of a row; it takes no time, 66.9 / 693 us in the cases below.)
 //
 // Bound by instructions: some 640 for a block of a plane (4352 bytes), of which 128 mask codes, 128 make
 // values, 48 (32) are mma, and an SM's share of HBM brings a block to each scheduler every 740 cycles.
@@ -42,7 +45,7 @@
 // 1024 + u two operations, 85 / 990 us; 12 warps 86 / 860; one operation 80 / 766; producers that fill
 // their rings lane by lane and sleep 76 / 785; q's fragments in shared memory (fewer spills) 71 / 755; a
 // merge that reads whole states 72 / 718; P.V in two halves (less registers), the pair's exchange apart
-// from the tiles (no fence between proxies) 69 / 732; a warp's index that the compiler sees to be one (no
+// from the tiles 69 / 732; a warp's index that the compiler sees to be one (no
 // spills, plain branches) 67 / 698.
 // Tried: codes of K masked into the mma as subnormal numbers u 2^-24, a chunk's products scaled in fp32
 // afterwards and the 8 taken off with sums of q, 68 / 711, but sums several times the scores, whose
@@ -703,6 +706,7 @@ __global__ void __launch_bounds__(Pol::kThreads, 1) gqa_decode_nibble_kernel(con
                     z[3] += o.w;
                 }
                 c.weigh(z, tile, pc.lo - pos, pc.hi - pos, kPaged && un.bad[s] != 0, lane);
+                ptx::fence_proxy_async_smem();   // this lane's loads, before the next copy into the slot
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&un.empty[s]));
                 if (++turn == RING) {
