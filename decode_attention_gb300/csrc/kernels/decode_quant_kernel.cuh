@@ -667,8 +667,8 @@ __global__ void __launch_bounds__(Pol::kThreads, 1)
                 const bool part = first > 0 || last < kQuantBlock || bad;
                 if (part) c.clear_rows(k_tile + kTileBytes, first, bad ? 0 : last, half, lane);
                 c.weigh(z, k_tile + kTileBytes, ks, vs, first, last, bad, half, lane);
-                // (the scores and cleared rows, before the next copy)
-                if (SPLIT > 1 || part) ptx::fence_proxy_async_smem();
+                // this lane's loads from the slot, and the scores and cleared rows, before the next copy into it
+                ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&un.empty[s]));
                 ++taken;
