@@ -957,6 +957,7 @@ __global__ void __launch_bounds__(block_threads<Pol>(), 1)
                 Pol::begin(st, &sm.q[qb][0], sm.scratch, warp, lane);
             else
                 Pol::begin(st, &sm.q[qb][0], warp, lane);
+            ptx::fence_proxy_async_smem();   // (as below)
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&sm.q_empty[qb]));
             ++q_n;
@@ -975,6 +976,9 @@ __global__ void __launch_bounds__(block_threads<Pol>(), 1)
             Pol::tile(st, v_tile, d.vlo, d.vhi, sm.scratch, t_idx, warp, lane);
         else
             Pol::tile(st, k_tile, v_tile, d.vlo, d.vhi, sm.scratch, t_idx, warp, lane);
+        // this lane's loads from the stage, before the next copy into it: the arrival does not order the two,
+        // which go through different proxies
+        ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&sm.empty[s]));
         ++t_idx;
