@@ -49,8 +49,8 @@ constexpr int kKeqvTcTilesPerCta = 64;
 // [acc_off, ...)      softmax partial acc:    slots x G x D floats
 // slots = kMaxCtas + B * KVH + kMaxDynUnits bounds the partials one call can
 // store: static unit j keeps its piece of segment u at slot j + u, dynamic
-// chunk k at slot kMaxCtas + B * KVH + k.  (The 8-bit cache's kernel has several units per
-// CTA: its dynamic chunks start at units + B * KVH, and as many fewer of them fit.)
+// chunk k at slot kMaxCtas + B * KVH + k.  (The 8-bit and the 4-bit cache's kernels have several
+// units per CTA: their dynamic chunks start at units + B * KVH, and as many fewer of them fit.)
 // The status word and the counters must be zero before a call; every completed
 // call leaves them so (gqa_device_status zeroes the whole header after a call
 // that raised a status bit, e.g. one that timed out half-way).
@@ -221,7 +221,7 @@ gqa_status_t run(const CallShape& c, bool paged, const void* q, const void* k, c
                  cudaStream_t stream, const void* w_k = nullptr, bool multi_query = false,
                  const float* k_scales = nullptr, const float* v_scales = nullptr,
                  bool nibble = false) {
-    if (!gqa::tensor_map_encoder()) return GQA_ERR_CUDA;
+    if (!nibble && !gqa::tensor_map_encoder()) return GQA_ERR_CUDA;   // (the 4-bit kernel has no tensor maps)
     void* ws = nullptr;
     WorkspaceLayout lay;
     int grid = 0;
