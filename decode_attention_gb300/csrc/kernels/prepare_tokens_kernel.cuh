@@ -96,7 +96,7 @@ __device__ __forceinline__ bool head_to_bf16(const uint32_t (&raw)[2][4], const 
     // of the vector share, the sum's 9 levels and its scaling, halved by the root, and the reciprocal root 2.2;
     // then the product with x and the weight, or a rotation's sum; and 1 for the sums below: 10.2 (a value:
     // 9.2, a rotation: 9.2).  Of |a| + |d|, which a rotated y is made of, the products with x and the weight,
-    // cosine or sine and its product: 4.
+    // cosine or sine (the nearest float of what is good to 2^-30) and its product: 4.
     constexpr float kError = 10.5f * 0x1p-24f, kValueError = 10.0f * 0x1p-24f, kTurnError = 4.01f * 0x1p-24f;
     const bool rotated = kKind != HeadKind::kValue && (D == 256 || turns);
     const uint64_t inv2 = ptx::f2_pack(inv, inv);
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kTokensThreads, kTokensPerSm)
         if (pair == 0) sm.place[s][sub] = make_int2(found ? b : -1, pos);
         if (!found) return;
         Twofold co, si;
-        cos_sin_of_turn(static_cast<uint64_t>(pos) * p.turn[pair], &co, &si);
+        cos_sin_nearest(static_cast<uint64_t>(pos) * p.turn[pair], &co, &si);
         float* at = &sm.cs[s][sub][pair % 8 / 2][pair / 8].x + pair % 2;
         at[0] = co.h;
         at[2] = si.h;
