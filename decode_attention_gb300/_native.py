@@ -1050,7 +1050,8 @@ def gqa_prepare_tokens_nibble(q_raw: torch.Tensor, k_raw: torch.Tensor, v_raw: t
                               w_q: torch.Tensor, w_k: torch.Tensor, token_offsets: torch.Tensor,
                               seq_lens: torch.Tensor, q_out: torch.Tensor, kv: torch.Tensor,
                               stream=None) -> None:
-    """gqa_prepare_tokens into a contiguous 4-bit cache kv [B,KVH*D/256,S,272] (uint8)."""
+    """gqa_prepare_tokens into a contiguous 4-bit cache kv [B,KVH*D/256,S,272] (uint8).  A layer
+    without a value projection passes k_raw as v_raw too."""
     _prepare_tokens_nibble(q_raw, k_raw, v_raw, w_q, w_k, token_offsets, None, seq_lens, q_out, kv,
                            stream)
 

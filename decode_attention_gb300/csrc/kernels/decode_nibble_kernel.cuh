@@ -5,7 +5,7 @@
 // over the sum of weights, for any M.  M is a whole number, set 8 below a maximum (rounded up, so that
 // from 2^24 on, where floats have a spacing above 1, it is at most 8 below) and kept until a weight
 // would pass 2^15: the accumulators are rescaled by powers of two, and seldom.  Weights lie in
-// (0, 2^15], where f16 hi + lo parts hold them to 22 bits, or to 2^-25 of a unit, 2^-33 of the largest.
+// (0, 2^15], where f16 hi + lo parts hold them to 22 bits, or to 2^-25 of a unit, 2^-32 of the largest.
 //
 // Both contractions run as warp-level f16 mma (m16n8k16, fp32 accumulate) with the cache as the A
 // operand, so that the g <= 8 query heads of a KV head fill the 8 columns of B.  A value
@@ -37,16 +37,18 @@
 // arrival, as a copy may overtake loads that are only issued.  (Without it one call in some 1000 over large
 // sliding batches found other codes in part of a row; it takes no time, 66.9 / 693 us in the cases below.)
 //
-// Bound by instructions: some 640 for a block of a plane (4352 bytes), of which 128 mask codes, 128 make
-// values, 48 (32) are mma, and an SM's share of HBM brings a block to each scheduler every 740 cycles.
-// Three consumer warps per scheduler (160 registers each, what the producers leave) issue in 0.58 of the
-// cycles; four, at 112, took 70 / 709 us where three take 67 / 698.  What the steps took, GPU time of
-// decode_sliding_b64_paged / decode_global_b16_long: 8 consumer warps and the mask and the constant of
-// 1024 + u two operations, 85 / 990 us; 12 warps 86 / 860; one operation 80 / 766; producers that fill
+// Bound by latency at few warps: no unit is full.  Three consumer warps per scheduler (160 registers each,
+// what the producers leave) issue in 0.58 of the cycles, some 640 instructions for a block of a plane (4352
+// bytes), of which 128 mask codes, 128 make values, 48 (32) are mma; no pipe is busy more than 0.46, and HBM,
+// which could bring a block to each scheduler every 740 cycles, half of the time.  Between two instructions of
+// a warp pass 6.3 cycles.  At g = 2 a fifth of them are waits at barriers and for loads from global
+// memory, which are the starts and ends of pieces, 1.6 fixed latencies and busy pipes; at g = 8 these are
+// 2.1, the others 0.7.  Four warps, at 112 registers, took 70 / 709 us where three took 67 / 698.  What the
+// steps took, GPU time of decode_sliding_b64_paged / decode_global_b16_long: 8 consumer warps and the mask and
+// the constant of 1024 + u two operations, 85 / 990 us; 12 warps 86 / 860; one operation 80 / 766; producers that fill
 // their rings lane by lane and sleep 76 / 785; q's fragments in shared memory (fewer spills) 71 / 755; a
 // merge that reads whole states 72 / 718; P.V in two halves (less registers), the pair's exchange apart
-// from the tiles 69 / 732; a warp's index that the compiler sees to be one (no
-// spills, plain branches) 67 / 698.
+// from the tiles 69 / 732; a warp's index that the compiler sees to be one (no spills, plain branches) 67 / 698.
 // Tried: codes of K masked into the mma as subnormal numbers u 2^-24, a chunk's products scaled in fp32
 // afterwards and the 8 taken off with sums of q, 68 / 711, but sums several times the scores, whose
 // rounding is twice the error (1.0e-6 for 4.6e-7 in a plain fp32 evaluation, 3.1e-7 here); P.V of one
@@ -74,7 +76,8 @@ struct NibblePlanTuning {
     // piece's cost among them).  One, two and three to a CTA, us: slidingDecodeGQA, one sequence of 400
     // positions 7.7 8.4 8.5, of the whole window 8.5 8.5 9.6, two 9.7 9.6 10.8, five 13.5 12.8 13.6, eight
     // 17.3 15.9 16.1; decodeGQA, one of 2048 9.9 11.8 13.7, of 16384 20.4 19.4 20.6, of 32768 31.9 27.5 27.1.
-    // Segments of 100 positions, 16 sequences: 11.3 11.7 10.5 and 11.5 12.0 11.2.
+    // Segments of 100 positions, 16 sequences: 11.3 11.7 10.5 and 11.5 12.0 11.2.  (The segments of empty
+    // sequences count: a window beside 15 of them takes three units, and 11.9 with their zeros, alone 8.4.)
     static constexpr int kUnitsPerCta = 3;
     __device__ static uint32_t units(uint32_t ctas, uint32_t tiles, uint32_t segments) {
         if (tiles <= 14 * ctas && tiles >= (kExtra + 16) * segments) return ctas;

@@ -567,10 +567,11 @@ gqa_status_t gqa_read_nibble_paged(const void *kv_pages, const int32_t *block_ta
  * A sequence whose offsets lie outside [0, N] or whose length is below n_b is skipped whole,
  * its rows of q_out included, and so are rows that belong to no sequence (behind
  * token_offsets[B]); a token that is not written to the cache still gets its q_out.
- * Arithmetic is fp32, the angles' reduction exact; outputs are rounded to bf16 (nearest
- * even).  The positions written by one call must be distinct.  N == 0 or B == 0: GQA_OK,
- * nothing enqueued.  One kernel launch, no workspace.  Errors as for gqa_prepare_decode (N
- * outside [0, 256 * 262144]: GQA_ERR_INVALID_ARGUMENT).
+ * Arithmetic is fp32 (a head of finite values whose squares add up beyond it becomes zeros), the
+ * angles' reduction exact; outputs are rounded to bf16 (nearest even).  The positions written by
+ * one call must be distinct.  N == 0 or B == 0: GQA_OK, nothing enqueued.  One kernel launch, no
+ * workspace.  Errors as for gqa_prepare_decode (N outside [0, 256 * 262144]:
+ * GQA_ERR_INVALID_ARGUMENT).
  */
 gqa_status_t gqa_prepare_tokens(const void *q_raw, const void *k_raw, const void *v_raw,
                                 const void *w_q, const void *w_k, const int32_t *token_offsets,
@@ -586,7 +587,9 @@ gqa_status_t gqa_prepare_tokens_paged(const void *q_raw, const void *k_raw, cons
                                       void *k_pages, void *v_pages, gqa_stream_t stream);
 
 /*
- * gqa_prepare_tokens into the 4-bit cache (v_raw is required).  A key or value is rounded to
+ * gqa_prepare_tokens into the 4-bit cache.  v_raw is required: there is no 4-bit form of the
+ * single K=V cache, and a layer without a value projection passes k_raw for both (values are
+ * then its rows, normed without weight or rotation).  A key or value is rounded to
  * fp32, from there to bf16, and coded by gqa_append_nibble's rule; where that matters it is
  * computed to some 2^-30, so its code is that of the exact value so rounded but for fewer than one
  * in 10^6.  A token past the capacity or on a page id outside [0, P) is not written.  One token per
